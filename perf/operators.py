@@ -1,0 +1,406 @@
+"""The operators of a training layer that stand beside the gradient collectives, as cases for measurement.
+
+Tokens sorted by expert and back (with weights, and the gradients), activation checkpoints in 8 bits (packed,
+unpacked, written by the gated activation's forward pass and read by its backward pass) and weight gradients taken
+from a checkpoint, whose bf16 results are what the reduce-scatter reads. Sizes are those of the layers in
+`workloads/configs.py`: a mixture-of-experts layer of width 2048 with 128 experts of 768, 8 a token; dense layers of
+width 8192 with feed-forwards of 28672; width 5120 with 13824.
+
+Each case runs in a plain form (elementary torch operations in 32 bits, rounded once) or, where `own` is true, through
+the package's entry points."""
+import math
+
+import numpy as np
+import torch
+
+own = False
+
+BLOCK = 32          # consecutive elements of a row that share one scale in a checkpoint
+TYPES = {"bf16": torch.bfloat16, "fp32": torch.float32}
+
+
+# ---------------------------------------------------------------------------------------------------- the cases
+
+def listed():
+    return [
+        # One token through the router: every launch and every host microsecond shows.
+        {"name": "sort, one token", "kind": "sort", "T": 1, "k": 8, "E": 128, "D": 2048, "type": "bf16", "ids": 64, "masked": 0.0},
+        # A training micro-batch of the mixture-of-experts layer, its last sequences padded.
+        {"name": "sort, 16384 tokens", "kind": "sort", "T": 16384, "k": 8, "E": 128, "D": 2048, "type": "bf16", "ids": 64, "masked": 0.05},
+        # The experts' rows back to their tokens, weighted; an odd number of tokens, some of them padding.
+        {"name": "combine, 8191 tokens", "kind": "combine", "T": 8191, "k": 8, "E": 128, "D": 2048, "type": "bf16", "weighted": True, "masked": 0.05},
+        # The gradient of sorting the tokens is the same sum without weights; here in fp32, few experts, wide rows.
+        {"name": "sort gradient, fp32", "kind": "combine", "T": 2049, "k": 2, "E": 8, "D": 5120, "type": "fp32", "weighted": False, "masked": 0.0},
+        # The gradient of the weighted combination: to the experts' rows and to the weights.
+        {"name": "combine gradient, 8192 tokens", "kind": "combine_grad", "T": 8192, "k": 8, "E": 128, "D": 2048, "type": "bf16", "masked": 0.02},
+        # A dense layer's input kept for the backward pass in 8 bits.
+        {"name": "pack, 8192 x 8192", "kind": "pack", "n": 8192, "D": 8192, "type": "bf16"},
+        # A checkpoint read back for a backward pass in fp32, odd number of tokens.
+        {"name": "unpack, 4097 x 5120 to fp32", "kind": "unpack", "n": 4097, "D": 5120, "type": "fp32"},
+        # The feed-forward's activation, its two inputs checkpointed in the same pass.
+        {"name": "gated, 4096 x 28672", "kind": "gated", "n": 4096, "D": 28672, "type": "bf16"},
+        # Its backward pass from the checkpoints.
+        {"name": "gated gradient, 4100 x 13824", "kind": "gated_grad", "n": 4100, "D": 13824, "type": "bf16"},
+        # Weight gradient of a narrow projection over a short micro-batch: few tiles, a long sum.
+        {"name": "weight gradient, 512 x 2048", "kind": "weight", "n": 1000, "O": 512, "I": 2048, "E": 1, "k": 1, "saved": False, "masked": 0.0},
+        # Weight gradients of every expert's gate projection; the tokens' checkpoint is read through the sort.
+        {"name": "weight gradients, 128 experts", "kind": "weight", "n": 4096, "O": 768, "I": 2048, "E": 128, "k": 8, "saved": True, "masked": 0.0},
+        # Weight gradient of a dense gate projection from the checkpoint of its input.
+        {"name": "weight gradient, 28672 x 8192", "kind": "weight", "n": 4096, "O": 28672, "I": 8192, "E": 1, "k": 1, "saved": True, "masked": 0.0},
+    ]
+
+
+def _log(rng, lo, hi):
+    return max(lo, min(hi, int(round(math.exp(rng.uniform(math.log(lo), math.log(hi + 0.999)))))))
+
+
+def _width(rng, lo, hi):
+    """A row length: most are multiples of 64 or 8, as layers have them, some are any number."""
+    w = _log(rng, lo, hi)
+    step = rng.choice([64, 64, 64, 8, 1])
+    return max(lo, w // step * step)
+
+
+def draw(rng):
+    kind = rng.choice(["sort", "combine", "combine", "combine_grad", "pack", "unpack", "gated", "gated_grad", "weight", "weight", "weight"])
+    kinds = rng.choice(["bf16", "bf16", "bf16", "fp32"])
+    if kind in ("sort", "combine", "combine_grad"):
+        k, E = rng.randint(1, 8), rng.choice([8, 16, 60, 64, 128, 160, 256])
+        T, D = _log(rng, 1, 16384), _width(rng, 64, 8192)
+        while T * k * D > 16384 * 8 * 2048:
+            T = max(1, T // 2)
+        c = {"kind": kind, "T": T, "k": k, "E": E, "D": D, "type": kinds, "masked": rng.choice([0.0, 0.03, 0.5])}
+        if kind == "sort":
+            c["ids"] = rng.choice([32, 64])
+        if kind == "combine":
+            c["weighted"] = rng.random() < 0.5
+        return c
+    if kind == "weight":
+        E = rng.choice([1, 1, 8, 64, 128])
+        k = 1 if E == 1 else rng.randint(1, 8)
+        n, O, I = _log(rng, 1, 8192), _width(rng, 64, 8192 if E == 1 else 2048), _width(rng, 64, 8192 if E == 1 else 2048)
+        return {"kind": kind, "n": n, "O": O, "I": I, "E": E, "k": k, "saved": rng.random() < 0.6, "masked": 0.0 if E == 1 else rng.choice([0.0, 0.1])}
+    n, D = _log(rng, 1, 16384), _width(rng, 64, 28672)
+    while n * D > 4096 * 28672:
+        n = max(1, n // 2)
+    return {"kind": kind, "n": n, "D": D, "type": kinds}
+
+
+# ------------------------------------------------------------------------------------------------ plain operators
+
+def plain_route(experts, E):
+    """(offsets, tokens, slots): stable order by expert; an id outside 0 .. E - 1 has no row, and slot -1."""
+    T, k = experts.shape
+    ids = experts.reshape(-1).long()
+    there = (ids >= 0) & (ids < E)
+    key = torch.where(there, ids, E)
+    order = torch.argsort(key, stable=True)
+    offsets = torch.searchsorted(key[order], torch.arange(E + 1, device=ids.device))
+    position = torch.arange(T * k, device=ids.device)
+    slots = torch.empty_like(order)
+    slots[order] = position
+    slots = torch.where(there, slots, -1).reshape(T, k)
+    tokens = torch.where(position < offsets[E], order // k, -1)
+    return offsets.int(), tokens.int(), slots.int()
+
+
+def plain_dispatch(x, tokens):
+    return torch.where((tokens >= 0)[:, None], x[tokens.clamp(min=0).long()], 0)
+
+
+def plain_combine(rows, slots, weights):
+    some = (slots >= 0)[..., None]
+    picked = torch.where(some, rows[slots.clamp(min=0).long()].float(), 0.0)
+    if weights is not None:
+        picked = picked * torch.where(some, weights[..., None], 0.0)
+    return picked.sum(1).to(rows.dtype)
+
+
+def plain_combine_grad(dout, rows, slots, weights):
+    some = slots >= 0
+    d = dout.float()[:, None, :]
+    picked = torch.where(some[..., None], rows[slots.clamp(min=0).long()].float(), 0.0)
+    dweights = torch.where(some, (d * picked).sum(-1), 0.0)
+    drows = torch.zeros(rows.shape[0] + 1, rows.shape[1], dtype=rows.dtype, device=rows.device)
+    drows[torch.where(some, slots, rows.shape[0]).long()] = (d * weights[..., None]).to(rows.dtype)
+    return drows[:-1], dweights
+
+
+def _scale(bits):
+    """The power of two that a scale byte stands for (bytes 10 to 246)."""
+    return (bits.view(torch.uint8).int() << 23).view(torch.float32)
+
+
+def plain_pack(x):
+    """Codes and scales: 32 elements of a row share the smallest power of two that brings them within 448."""
+    n, D = x.shape
+    nb = -(-D // BLOCK)
+    v = torch.nn.functional.pad(x.float(), (0, nb * BLOCK - D)).view(n, nb, BLOCK)
+    fine = torch.isfinite(v)
+    m, ex = torch.frexp(torch.where(fine, v, 0.0).abs().amax(-1))        # amax = m 2^ex, 1/2 <= m < 1, or 0
+    byte = (ex - 9 + (m > 0.875) + 127).clamp(10, 246)
+    scales = torch.where(m == 0, 10, byte).to(torch.uint8)
+    q = (v / _scale(scales)[..., None]).clamp(-448, 448)
+    codes = torch.where(fine, q, float("nan")).view(n, -1)[:, :D].to(torch.float8_e4m3fn)
+    return codes.contiguous(), scales.view(torch.float8_e8m0fnu)
+
+
+def plain_unpack(codes, scales):
+    n, D = codes.shape
+    return codes.float() * _scale(scales).repeat_interleave(BLOCK, 1)[:, :D]
+
+
+def plain_gated(gate, up):
+    g, u = gate.float(), up.float()
+    return (g * torch.sigmoid(g) * u).to(gate.dtype)
+
+
+def plain_gated_grad(dout, gate, up):
+    d = dout.float()
+    s = torch.sigmoid(gate)
+    t = gate * s
+    dgate = d * up * (s + t * torch.sigmoid(-gate))
+    return dgate.to(dout.dtype), (d * t).to(dout.dtype), (t * up).to(dout.dtype)
+
+
+def plain_weight(dy, x, offsets, tokens):
+    """One gradient an expert: dy's rows of that expert, transposed, times the x of their tokens."""
+    d = dy.float()
+    if offsets is None:
+        return (d.t() @ x).to(dy.dtype)[None]
+    E = offsets.numel() - 1
+    off = offsets.long()
+    most = int((off[1:] - off[:-1]).max())
+    at = off[:-1, None] + torch.arange(max(most, 1), device=dy.device)           # each expert's rows, padded to the most
+    there = (at < off[1:, None])[..., None]
+    at = at.clamp(max=dy.shape[0] - 1)
+    d = torch.where(there, d[at], 0.0)
+    x = torch.where(there, x[tokens[at].clamp(min=0).long()], 0.0)
+    return torch.bmm(d.transpose(1, 2).contiguous(), x).to(dy.dtype)
+
+
+# ---------------------------------------------------------------------------------------------------- state and run
+
+def _experts(T, k, E, masked, g, dev):
+    """Ids as a router gives them: k different experts a token (where there are as many), some more liked than others; masked tokens have none."""
+    liked = 0.5 * torch.randn(E, generator=g, device=dev)
+    score = liked + torch.randn(T, E, generator=g, device=dev)
+    ids = torch.topk(score, min(k, E), 1).indices
+    none = torch.rand(T, generator=g, device=dev) < masked
+    none[0] = False
+    return torch.where(none[:, None], -1, ids)
+
+
+def _activations(n, D, dtype, g, dev):
+    """Unit normals with a few features ten times as large, as a layer's inputs have them."""
+    x = torch.randn(n, D, generator=g, device=dev, dtype=dtype)
+    return x * torch.where(torch.rand(D, generator=g, device=dev) < 0.01, 10.0, 1.0).to(dtype)
+
+
+def prepare(case, seed):
+    dev = torch.device("cuda")
+    g = torch.Generator(device=dev)
+    g.manual_seed(seed)
+    c, s = case, {"kind": case["kind"]}
+    empty = lambda *shape, dtype: torch.empty(*shape, dtype=dtype, device=dev)  # noqa: E731
+    if c["kind"] in ("sort", "combine", "combine_grad"):
+        T, k, E, D, dtype = c["T"], c["k"], c["E"], c["D"], TYPES[c["type"]]
+        ids = _experts(T, k, E, c["masked"], g, dev)
+        if c["kind"] == "sort":
+            s.update(experts=ids.to(torch.int32 if c["ids"] == 32 else torch.int64), E=E, x=_activations(T, D, dtype, g, dev),
+                     offsets=empty(E + 1, dtype=torch.int32), tokens=torch.full((T * k,), -1, dtype=torch.int32, device=dev),
+                     slots=empty(T, k, dtype=torch.int32), rows=torch.zeros(T * k, D, dtype=dtype, device=dev))
+            return s
+        s["slots"] = plain_route(ids, E)[2]
+        s["rows"] = _activations(T * k, D, dtype, g, dev)
+        s["weights"] = torch.softmax(torch.randn(T, k, generator=g, device=dev), 1)
+        if c["kind"] == "combine":
+            s["weights"] = s["weights"] if c["weighted"] else None
+            s["out"] = empty(T, D, dtype=dtype)
+        else:
+            s["dout"] = 1e-3 * torch.randn(T, D, generator=g, device=dev, dtype=dtype)
+            s["drows"], s["dweights"] = torch.zeros_like(s["rows"]), empty(T, k, dtype=torch.float32)
+        return s
+    if c["kind"] == "weight":
+        n, O, I, E, k = c["n"], c["O"], c["I"], c["E"], c["k"]
+        x = _activations(n, I, torch.bfloat16, g, dev)
+        s["x"] = plain_pack(x) if c["saved"] else x
+        s["dy"] = 1e-3 * torch.randn(n * k, O, generator=g, device=dev, dtype=torch.bfloat16)
+        s["offsets"] = s["tokens"] = None
+        if E > 1:
+            s["offsets"], s["tokens"], _ = plain_route(_experts(n, k, E, c["masked"], g, dev), E)
+        s["grads"] = empty(E, O, I, dtype=torch.bfloat16)
+        return s
+    n, D, dtype = c["n"], c["D"], TYPES[c["type"]]
+    saved = lambda: (empty(n, D, dtype=torch.float8_e4m3fn), empty(n, -(-D // BLOCK), dtype=torch.float8_e8m0fnu))  # noqa: E731
+    x = _activations(n, D, dtype, g, dev)
+    if c["kind"] == "pack":
+        s.update(x=x, saved=saved())
+    elif c["kind"] == "unpack":
+        s.update(saved=plain_pack(x), out=empty(n, D, dtype=dtype))
+    else:
+        up = _activations(n, D, dtype, g, dev)
+        if c["kind"] == "gated":
+            s.update(gate=x, up=up, out=empty(n, D, dtype=dtype), gate_saved=saved(), up_saved=saved())
+        else:
+            s.update(gate_saved=plain_pack(x), up_saved=plain_pack(up), dout=1e-3 * torch.randn(n, D, generator=g, device=dev, dtype=dtype),
+                     dgate=empty(n, D, dtype=dtype), dup=empty(n, D, dtype=dtype), out=empty(n, D, dtype=dtype))
+    return s
+
+
+def run(s):
+    return run_own(s) if own else run_plain(s)
+
+
+def run_own(s):
+    import mixed_precision_rs_amd as tide
+    kind = s["kind"]
+    if kind == "sort":
+        tide.route_tokens(s["experts"], s["E"], s["offsets"], s["tokens"], s["slots"])
+        tide.dispatch_tokens(s["x"], s["slots"], s["rows"])
+        return s["offsets"], s["tokens"], s["slots"], s["rows"]
+    if kind == "combine":
+        tide.combine_tokens(s["rows"], s["slots"], s["out"], weights=s["weights"])
+        return s["out"]
+    if kind == "combine_grad":
+        tide.combine_tokens_grad(s["dout"], s["rows"], s["slots"], s["weights"], s["drows"], s["dweights"])
+        return s["drows"], s["dweights"]
+    if kind == "pack":
+        tide.checkpoint_pack(s["x"], s["saved"])
+        return s["saved"]
+    if kind == "unpack":
+        tide.checkpoint_unpack(s["saved"], s["out"])
+        return s["out"]
+    if kind == "gated":
+        tide.gated_silu(s["gate"], s["up"], s["out"], gate_saved=s["gate_saved"], up_saved=s["up_saved"])
+        return s["out"], s["gate_saved"], s["up_saved"]
+    if kind == "gated_grad":
+        tide.gated_silu_grad(s["dout"], s["gate_saved"], s["up_saved"], s["dgate"], s["dup"], out=s["out"])
+        return s["dgate"], s["dup"], s["out"]
+    tide.weight_grads_bf16(s["dy"], s["x"], s["grads"], offsets=s["offsets"], tokens=s["tokens"])
+    return s["grads"]
+
+
+def run_plain(s):
+    kind = s["kind"]
+    if kind == "sort":
+        offsets, tokens, slots = plain_route(s["experts"], s["E"])
+        return offsets, tokens, slots, plain_dispatch(s["x"], tokens)
+    if kind == "combine":
+        return plain_combine(s["rows"], s["slots"], s["weights"])
+    if kind == "combine_grad":
+        return plain_combine_grad(s["dout"], s["rows"], s["slots"], s["weights"])
+    if kind == "pack":
+        return plain_pack(s["x"])
+    if kind == "unpack":
+        return plain_unpack(*s["saved"]).to(s["out"].dtype)
+    if kind == "gated":
+        return plain_gated(s["gate"], s["up"]), plain_pack(s["gate"]), plain_pack(s["up"])
+    if kind == "gated_grad":
+        return plain_gated_grad(s["dout"], plain_unpack(*s["gate_saved"]), plain_unpack(*s["up_saved"]))
+    x = plain_unpack(*s["x"]) if isinstance(s["x"], tuple) else s["x"].float()
+    return plain_weight(s["dy"], x, s["offsets"], s["tokens"])
+
+
+# ------------------------------------------------------------------------------------------------ work and exactness
+
+def work(case):
+    c, wide = case, 4 if case.get("type") == "fp32" else 2
+    if c["kind"] in ("sort", "combine", "combine_grad"):
+        T, k, D = c["T"], c["k"], c["D"]
+        rows = T * k * (1.0 - c["masked"])
+        if c["kind"] == "sort":
+            return {"bytes": T * k * (c["ids"] / 8 + 4) + 4 * rows + 4 * (c["E"] + 1) + wide * D * (T * (1.0 - c["masked"]) + rows), "flops": 0}
+        if c["kind"] == "combine":
+            return {"bytes": T * k * (8 if c["weighted"] else 4) + wide * D * (T + rows), "flops": (2 if c["weighted"] else 1) * rows * D}
+        return {"bytes": T * k * 12 + wide * D * (T * (1.0 - c["masked"]) + 2 * rows), "flops": 3 * rows * D}
+    if c["kind"] == "weight":
+        n, O, I = c["n"], c["O"], c["I"]
+        x = n * (I + -(-I // BLOCK)) if c["saved"] else 2 * n * I
+        rows = n * c["k"] * (1.0 - c["masked"])
+        return {"bytes": 2 * rows * O + x + 2 * c["E"] * O * I + (4 * rows + 4 * (c["E"] + 1) if c["E"] > 1 else 0), "flops": 2 * rows * O * I}
+    n, D = c["n"], c["D"]
+    saved = n * (D + -(-D // BLOCK))
+    if c["kind"] in ("pack", "unpack"):
+        return {"bytes": wide * n * D + saved, "flops": 2 * n * D}
+    if c["kind"] == "gated":
+        return {"bytes": 3 * wide * n * D + 2 * saved, "flops": 10 * n * D}
+    return {"bytes": 4 * wide * n * D + 2 * saved, "flops": 20 * n * D}
+
+
+def _exact_pack(x):
+    """By the definition, in 64 bits: the scale is the least 2^e, -117 <= e <= 119, with amax <= 448 2^e (the largest where none is), the code the nearest of 8-bit e4m3, ties to even."""
+    n, D = x.shape
+    nb = -(-D // BLOCK)
+    v = torch.zeros(n, nb * BLOCK, dtype=torch.float64, device=x.device)
+    v[:, :D] = x.double()
+    bad = ~torch.isfinite(v)
+    v[bad] = 0.0
+    top = v.abs().view(n, nb, BLOCK).max(-1).values
+    e = torch.ceil(torch.log2(torch.clamp(top, min=2.0 ** -140) / 448.0))
+    e = e + (top > 448.0 * torch.exp2(e)).double() - (top <= 448.0 * torch.exp2(e - 1)).double()     # the logarithm's own rounding
+    scale = torch.exp2(e.clamp(-117, 119))
+    q = torch.clamp(v.view(n, nb, BLOCK) / scale[..., None], -448.0, 448.0)
+    step = torch.exp2(torch.clamp(torch.floor(torch.log2(torch.clamp(q.abs(), min=2.0 ** -30))), min=-6.0) - 3.0)
+    q = torch.round(q / step) * step                                                                 # halves to even
+    q = q.view(n, -1)
+    q[bad] = float("nan")
+    return q[:, :D], scale
+
+
+def _exact_saved(saved):
+    codes, scales = saved
+    n, D = codes.shape
+    byte = scales.view(torch.uint8).double()
+    return codes.double() * torch.exp2(byte - 127.0).unsqueeze(-1).expand(-1, -1, BLOCK).reshape(n, -1)[:, :D]
+
+
+def exact(case, seed):
+    s = prepare(case, seed)
+    kind = s["kind"]
+    if kind == "sort":
+        ids = s["experts"].cpu().numpy()
+        T, k = ids.shape
+        flat = ids.reshape(-1)
+        where = np.nonzero((flat >= 0) & (flat < s["E"]))[0]
+        order = where[np.lexsort((where, flat[where]))]
+        rows = torch.zeros(T * k, s["x"].shape[1], dtype=torch.float64, device=s["x"].device)
+        rows[: order.size] = s["x"].double()[torch.from_numpy(order // k).to(s["x"].device)]
+        return None, None, None, rows
+    if kind in ("combine", "combine_grad"):
+        T, k = s["slots"].shape
+        rows = torch.cat([s["rows"].double(), torch.zeros(1, s["rows"].shape[1], dtype=torch.float64, device=s["rows"].device)])
+        at = torch.where(s["slots"] < 0, rows.shape[0] - 1, s["slots"].long())                       # the last row: nothing
+        if kind == "combine":
+            out = torch.zeros(T, rows.shape[1], dtype=torch.float64, device=rows.device)
+            for j in range(k):
+                out += rows[at[:, j]] * (1.0 if s["weights"] is None else s["weights"][:, j: j + 1].double())
+            return out
+        d, w = s["dout"].double(), s["weights"].double()
+        drows, dweights = torch.zeros_like(rows), torch.zeros_like(w)
+        for j in range(k):
+            dweights[:, j] = (rows[at[:, j]] * d).sum(1)
+        for j in range(k):
+            drows[at[:, j]] = w[:, j: j + 1] * d
+        return drows[:-1], dweights
+    if kind == "pack":
+        return _exact_pack(s["x"])
+    if kind == "unpack":
+        return _exact_saved(s["saved"])
+    if kind == "gated":
+        g = s["gate"].double()
+        return g / (1.0 + torch.exp(-g)) * s["up"].double(), _exact_pack(s["gate"]), _exact_pack(s["up"])
+    if kind == "gated_grad":
+        g, u, d = _exact_saved(s["gate_saved"]), _exact_saved(s["up_saved"]), s["dout"].double()
+        e = 1.0 + torch.exp(-g)
+        return d * u * (1.0 / e + g * (e - 1.0) / (e * e)), d * g / e, g / e * u
+    x = _exact_saved(s["x"]) if isinstance(s["x"], tuple) else s["x"].double()
+    dy, (E, O, I) = s["dy"].double(), s["grads"].shape
+    if s["offsets"] is None:
+        return torch.mm(dy.t(), x)[None]
+    out = torch.zeros(E, O, I, dtype=torch.float64, device=x.device)
+    off = s["offsets"].tolist()
+    for e in range(E):
+        at = s["tokens"][off[e]: off[e + 1]].long()
+        out[e] = torch.mm(dy[off[e]: off[e + 1]].t(), x[at])
+    return out
