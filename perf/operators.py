@@ -277,7 +277,7 @@ def run_own(s):
     if kind == "gated_grad":
         tide.gated_silu_grad(s["dout"], s["gate_saved"], s["up_saved"], s["dgate"], s["dup"], out=s["out"])
         return s["dgate"], s["dup"], s["out"]
-    tide.weight_grads_bf16(s["dy"], s["x"], s["grads"], offsets=s["offsets"], tokens=s["tokens"])
+    tide.weight_grads_bf16(s["dy"], s["x"], s["grads"], offsets=s["offsets"], token_of_row=s["tokens"])
     return s["grads"]
 
 
