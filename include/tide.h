@@ -497,6 +497,180 @@ tide_status tide_diag_stream(int32_t kind, const void* const* srcs, int32_t nsrc
  * not by the number of calls. Host-only (diagnostic). */
 tide_status tide_plan_event_count(const tide_plan* plan, int64_t* events);
 
+/*
+ * ---- The training layer beside the collectives -------------------------------
+ *
+ * What a step that trains with the collectives above keeps and moves between
+ * its matrix products: tokens sorted by expert and back, activation checkpoints
+ * in 8 bits, and the weight gradients taken from them, which are the bf16
+ * tensors the reduce-scatter reads.
+ *
+ * Shared by these calls, beyond the conventions at the top:
+ *   - Matrices are row-major with a row stride in ELEMENTS (>= the row's
+ *     length) and any element alignment. A matrix that is written must not
+ *     share memory with another argument; column windows of one wider matrix
+ *     (equal strides) do not share memory. Nothing between a row's end and the
+ *     next row is read or written.
+ *   - They launch kernels and nothing else (no allocation, no copy, no wait),
+ *     keep nothing between calls, and may be captured into a graph. Two calls
+ *     that may run at once need a workspace each.
+ *   - Results do not depend on the order in which workgroups run: the same
+ *     inputs give the same bits.
+ *   - Index contents are checked by the kernels: an expert id outside
+ *     [0, experts) is a pair without an expert, a slot or token outside its
+ *     range is skipped, offsets are clamped to the rows there are.
+ */
+typedef enum tide_dtype {
+    TIDE_DTYPE_BF16 = 0,
+    TIDE_DTYPE_FP32 = 1
+} tide_dtype;
+
+/* An activation checkpoint of a rows x width matrix: codes is rows x width of
+ * e4m3 (OCP: 448 the largest, no infinities), scales rows x ceil(width / 32) of
+ * exponent bytes, element c of a row standing for
+ * code * 2^(scales[c / 32] - 127). Strides in bytes. */
+typedef struct tide_saved {
+    uint8_t* codes;
+    uint8_t* scales;
+    int64_t codes_stride;
+    int64_t scales_stride;
+} tide_saved;
+
+/* Bytes of device workspace tide_route_tokens needs. Host-only. Errors:
+ * INVALID_ARG; UNSUPPORTED (over 512 experts, or tokens * k past 2^31 - 1). */
+tide_status tide_route_workspace(int64_t tokens, int32_t k, int32_t experts, int64_t* bytes);
+
+/*
+ * Sorts the tokens * k (token, choice) pairs by expert, stably: pairs of one
+ * expert keep the order of token * k + choice.
+ *   experts_of: tokens x k expert ids of id_bytes (4 or 8: int32 or int64), as
+ *               the router chose them. An id outside [0, experts) (a padding
+ *               token, a dropped choice) has no row. The same expert twice in
+ *               one token is two rows.
+ *   offsets:    experts + 1; expert e's rows are offsets[e] .. offsets[e+1] - 1.
+ *   token_of_row: tokens * k; the token of each row, rows from
+ *               offsets[experts] on are left as they were.
+ *   slots:      tokens x k; the row of each pair, -1 where it has none.
+ *   workspace:  tide_route_workspace bytes (may be NULL when that is 0).
+ * Errors: INVALID_ARG, ALIGNMENT, UNSUPPORTED (as above), HIP.
+ */
+tide_status tide_route_tokens(const void* experts_of, int32_t id_bytes, int64_t tokens, int32_t k,
+                              int32_t experts, int32_t* offsets, int32_t* token_of_row,
+                              int32_t* slots, void* workspace, int64_t workspace_bytes,
+                              void* stream);
+
+/*
+ * Tokens to experts: rows[slots[t, j]] = x[t]. x is tokens x width, rows is
+ * nrows x width (nrows = tokens * k holds every sort); rows that no slot names
+ * are left as they were. No two slots may be equal. The gradient of this call
+ * is tide_combine_tokens of the rows' gradients without weights.
+ * Errors: INVALID_ARG, ALIGNMENT, OVERFLOW, UNSUPPORTED (tokens * k or nrows
+ * past 2^31 - 1), HIP.
+ */
+tide_status tide_dispatch_tokens(int32_t dtype, const void* x, int64_t x_stride, int64_t tokens,
+                                 int64_t width, const int32_t* slots, int32_t k, void* rows,
+                                 int64_t rows_stride, int64_t nrows, void* stream);
+
+/*
+ * Experts' rows back to their tokens: out[t] = sum over j of weights[t, j] *
+ * rows[slots[t, j]], j ascending, each term added by one fused multiply-add in
+ * fp32, rounded once. weights: tokens x k fp32, or NULL for ones. A pair
+ * without a row adds nothing, whatever its weight holds; a token without any
+ * gets zeros.
+ * Errors: as tide_dispatch_tokens.
+ */
+tide_status tide_combine_tokens(int32_t dtype, const void* rows, int64_t rows_stride,
+                                int64_t nrows, int64_t width, const int32_t* slots,
+                                const float* weights, int64_t tokens, int32_t k, void* out,
+                                int64_t out_stride, void* stream);
+
+/*
+ * Gradient of tide_combine_tokens: drows[slots[t, j]] = weights[t, j] * dout[t]
+ * (rounded once) and dweights[t, j] = dot(dout[t], rows[slots[t, j]]) in fp32,
+ * 0 where the pair has no row. weights may be NULL (ones); dweights may be
+ * NULL, then rows is not read. Rows of drows that no slot names are left as
+ * they were. No two slots may be equal.
+ * Errors: as tide_dispatch_tokens.
+ */
+tide_status tide_combine_tokens_grad(int32_t dtype, const void* dout, int64_t dout_stride,
+                                     const void* rows, int64_t rows_stride, int64_t nrows,
+                                     int64_t width, const int32_t* slots, const float* weights,
+                                     int64_t tokens, int32_t k, void* drows,
+                                     int64_t drows_stride, float* dweights, void* stream);
+
+/*
+ * Packs a matrix into a checkpoint. Each 32 consecutive elements of a row (the
+ * last block of a row may be shorter) share the least scale 2^e, -117 <= e <=
+ * 119, with max |x| <= 448 * 2^e over the block's finite elements; a code is
+ * x / 2^e rounded to nearest even (by half a step of e4m3, 2^-4 of its value,
+ * or 2^-10 * 2^e below 2^-6 * 2^e), values past 448 * 2^119 at 448. An element
+ * that is not finite is stored as NaN.
+ * Errors: INVALID_ARG, ALIGNMENT, OVERFLOW, HIP.
+ */
+tide_status tide_checkpoint_pack(int32_t dtype, const void* x, int64_t x_stride, int64_t rows,
+                                 int64_t width, const tide_saved* saved, void* stream);
+
+/* The values a checkpoint (tide_checkpoint_pack's) stands for, exact in both
+ * types. Errors: as tide_checkpoint_pack. */
+tide_status tide_checkpoint_unpack(int32_t dtype, const tide_saved* saved, int64_t rows,
+                                   int64_t width, void* out, int64_t out_stride, void* stream);
+
+/*
+ * The gated activation out = silu(gate) * up, silu(g) = g / (1 + exp(-g)), in
+ * fp32, rounded once; in the same pass, where gate_saved / up_saved are not
+ * NULL, the checkpoints of gate and up.
+ * Errors: as tide_checkpoint_pack.
+ */
+tide_status tide_gated_silu(int32_t dtype, const void* gate, int64_t gate_stride, const void* up,
+                            int64_t up_stride, int64_t rows, int64_t width, void* out,
+                            int64_t out_stride, const tide_saved* gate_saved,
+                            const tide_saved* up_saved, void* stream);
+
+/*
+ * Gradient of tide_gated_silu at the checkpoints' values: with s = sigmoid(g),
+ * dgate = dout * up * s * (1 + g * (1 - s)) and dup = dout * g * s; where out
+ * is not NULL it receives g * s * up, the activation recomputed for the next
+ * product's weight gradient.
+ * Errors: as tide_checkpoint_pack.
+ */
+tide_status tide_gated_silu_grad(int32_t dtype, const void* dout, int64_t dout_stride,
+                                 const tide_saved* gate_saved, const tide_saved* up_saved,
+                                 int64_t rows, int64_t width, void* dgate, int64_t dgate_stride,
+                                 void* dup, int64_t dup_stride, void* out, int64_t out_stride,
+                                 void* stream);
+
+/* Bytes of device workspace tide_weight_grads_bf16 needs for these sizes.
+ * Host-only. Errors: INVALID_ARG, OVERFLOW, UNSUPPORTED. */
+tide_status tide_weight_grads_workspace(int64_t rows, int64_t out, int64_t in, int32_t experts,
+                                        int64_t* bytes);
+
+/*
+ * Weight gradients of y = x W^T, one expert or many: grads[e] (out x in bf16,
+ * contiguous, the layout of a parameter) = sum over the rows r of expert e of
+ * dy[r]^T x[token_of_row[r]], products of bf16 values added in fp32, rounded
+ * once.
+ *   dy:      rows x out bf16.
+ *   x/saved: exactly one: x_rows x in bf16, or a checkpoint of such a matrix,
+ *            whose values are exact in bf16.
+ *   offsets: experts + 1 device entries as tide_route_tokens writes them; NULL
+ *            (with experts = 1): one expert has all the rows. Rows outside are
+ *            not read into any sum. An expert without rows gets zeros.
+ *   token_of_row: rows device entries; NULL: row r of dy belongs to row r of x
+ *            (x_rows >= rows). A row whose token is outside [0, x_rows) adds
+ *            nothing.
+ *   grads:   host array of `experts` device pointers, read during the call.
+ *   accumulate: not 0: the sum is added to what grads holds, in fp32, before
+ *            the rounding.
+ * Errors: INVALID_ARG, ALIGNMENT, OVERFLOW, UNSUPPORTED (a size past 2^31 - 1,
+ * or too many tiles for one launch), NO_MEMORY, HIP.
+ */
+tide_status tide_weight_grads_bf16(const uint16_t* dy, int64_t dy_stride, int64_t rows,
+                                   int64_t out, const uint16_t* x, int64_t x_stride,
+                                   const tide_saved* saved, int64_t x_rows, int64_t in,
+                                   const int32_t* offsets, const int32_t* token_of_row,
+                                   int32_t experts, uint16_t* const* grads, int32_t accumulate,
+                                   void* workspace, int64_t workspace_bytes, void* stream);
+
 /* Static text for a status code. */
 const char* tide_status_string(tide_status status);
 

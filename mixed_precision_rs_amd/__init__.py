@@ -1,8 +1,10 @@
 """MI355X-native implementation of TIDE's one-GPU hot path: the level-1
 bf16 -> fp32 reduce-scatter into padded rank-major shards and the all-gather
 placement into parameter storage (C ABI in include/tide.h, HIP kernels for
-gfx950 in csrc/). Importing this package loads libtide.so and fails loudly if
-it has not been built."""
+gfx950 in csrc/), and the training layer beside them: tokens sorted by expert
+and back, 8-bit activation checkpoints, and weight gradients from them.
+Importing this package loads libtide.so and fails loudly if it has not been
+built."""
 from ._lib import (  # noqa: F401
     Call,
     ENGINE_KERNEL,
@@ -45,6 +47,19 @@ from ._lib import (  # noqa: F401
     trace_buffer,
     traced,
     version,
+)
+from ._layer import (  # noqa: F401
+    checkpoint_pack,
+    checkpoint_unpack,
+    combine_tokens,
+    combine_tokens_grad,
+    dispatch_tokens,
+    gated_silu,
+    gated_silu_grad,
+    route_tokens,
+    route_workspace_bytes,
+    weight_grads_bf16,
+    weight_grads_workspace_bytes,
 )
 
 lib()  # load now: no silent fallback exists

@@ -35,7 +35,11 @@ EXPORTS = ["tide_plan_create", "tide_plan_destroy", "tide_plan_dims", "tide_plan
            "tide_plan_event_count", "tide_prepare_reduce_scatter_bf16_fp32",
            "tide_prepare_allgather_place_stage", "tide_prepare_stage_grads_bf16",
            "tide_call_enqueue", "tide_call_destroy", "tide_plan_slot_grads",
-           "tide_dma_engine_count", "tide_reduce_scatter_bf16_fp32_noalloc", "tide_diag_stream"]
+           "tide_dma_engine_count", "tide_reduce_scatter_bf16_fp32_noalloc", "tide_diag_stream",
+           "tide_route_workspace", "tide_route_tokens", "tide_dispatch_tokens",
+           "tide_combine_tokens", "tide_combine_tokens_grad", "tide_checkpoint_pack",
+           "tide_checkpoint_unpack", "tide_gated_silu", "tide_gated_silu_grad",
+           "tide_weight_grads_workspace", "tide_weight_grads_bf16"]
 
 
 class TideError(RuntimeError):

@@ -15,14 +15,17 @@
 #include <vector>
 
 #include "tide.h"
+#include "host.hpp"
 #include "sdma.hpp"
 #include "tide_internal.hpp"
 
 using namespace tide;
 
 namespace {
-
 thread_local std::string g_detail;
+}  // namespace
+
+namespace tide {
 
 tide_status fail(tide_status st, const char* fmt, ...) {
     char buf[512];
@@ -38,36 +41,67 @@ tide_status hip_fail(hipError_t e, const char* what) {
     return fail(TIDE_ERR_HIP, "%s: %s (%d)", what, hipGetErrorString(e), (int)e);
 }
 
-#define TIDE_HIP_TRY(expr)                                      \
-    do {                                                        \
-        hipError_t e_ = (expr);                                 \
-        if (e_ != hipSuccess) return hip_fail(e_, #expr);       \
-    } while (0)
-
-// Makes `dev` the current device for the guard's lifetime. Allocations,
-// events and kernel attributes belong to the current device, and a caller's
-// stream may sit on another one.
-class DeviceGuard {
-  public:
-    explicit DeviceGuard(int dev) {
-        if (hipGetDevice(&prev_) != hipSuccess) prev_ = -1;
-        if (prev_ != dev) {
-            status_ = hipSetDevice(dev);
-            changed_ = status_ == hipSuccess && prev_ >= 0;
-        }
+tide_status stream_device(hipStream_t stream, int* dev) {
+    if (stream) {
+        hipError_t e = hipStreamGetDevice(stream, dev);
+        if (e != hipSuccess) return hip_fail(e, "hipStreamGetDevice");
+        return TIDE_OK;
     }
-    ~DeviceGuard() {
-        if (changed_) (void)hipSetDevice(prev_);
-    }
-    DeviceGuard(const DeviceGuard&) = delete;
-    DeviceGuard& operator=(const DeviceGuard&) = delete;
-    hipError_t status() const { return status_; }
+    hipError_t e = hipGetDevice(dev);
+    if (e != hipSuccess) return hip_fail(e, "hipGetDevice");
+    return TIDE_OK;
+}
 
-  private:
-    int prev_ = -1;
-    bool changed_ = false;
-    hipError_t status_ = hipSuccess;
-};
+tide_status matrix(const char* name, const void* p, int64_t rows, int64_t cols, int64_t stride,
+                   int32_t size, Mat* out) {
+    *out = Mat{name, reinterpret_cast<uintptr_t>(p), 0, 0, 0};
+    if (rows < 0 || cols < 0) return fail(TIDE_ERR_INVALID_ARG, "%s has a negative size", name);
+    if (rows == 0 || cols == 0) return TIDE_OK;
+    if (stride < cols)
+        return fail(TIDE_ERR_INVALID_ARG, "%s: row stride %lld < %lld columns", name,
+                    (long long)stride, (long long)cols);
+    int64_t bytes;
+    if (__builtin_mul_overflow(rows, stride, &bytes) || __builtin_mul_overflow(bytes, size, &bytes))
+        return fail(TIDE_ERR_OVERFLOW, "%s: its extent overflows int64", name);
+    if (!p) return fail(TIDE_ERR_INVALID_ARG, "%s is NULL", name);
+    if (out->base & (uintptr_t)(size - 1))
+        return fail(TIDE_ERR_ALIGNMENT, "%s is not %d-byte aligned", name, size);
+    out->rows = rows;
+    out->width = cols * size;
+    out->stride = stride * size;
+    return TIDE_OK;
+}
+
+namespace {
+bool share(const Mat& a, const Mat& b) {
+    if (a.rows == 0 || b.rows == 0) return false;
+    const uintptr_t ae = a.base + (uintptr_t)((a.rows - 1) * a.stride + a.width);
+    const uintptr_t be = b.base + (uintptr_t)((b.rows - 1) * b.stride + b.width);
+    if (ae <= b.base || be <= a.base) return false;
+    if (a.stride != b.stride) return true;
+    const int64_t d = (int64_t)((b.base > a.base ? b.base - a.base : a.base - b.base) %
+                                (uintptr_t)a.stride);
+    const int64_t first = b.base > a.base ? a.width : b.width;
+    const int64_t second = b.base > a.base ? b.width : a.width;
+    return d < first || d + second > a.stride;
+}
+}  // namespace
+
+tide_status no_overlap(const Mat* written, int nw, const Mat* read, int nr) {
+    for (int i = 0; i < nw; ++i) {
+        for (int j = 0; j < i; ++j)
+            if (share(written[i], written[j]))
+                return fail(TIDE_ERR_INVALID_ARG, "%s overlaps %s", written[i].name, written[j].name);
+        for (int j = 0; j < nr; ++j)
+            if (share(written[i], read[j]))
+                return fail(TIDE_ERR_INVALID_ARG, "%s overlaps %s", written[i].name, read[j].name);
+    }
+    return TIDE_OK;
+}
+
+}  // namespace tide
+
+namespace {
 
 // Defaults of the CU-budgeted mode: 16 summing + 4 landing blocks (page 1
 // "Why does a communication kernel slow a matrix multiply by 69%?"; page 3
@@ -357,17 +391,6 @@ int64_t count_launches(const tide_plan* plan, int op, const tide_launch& l, int6
     const int64_t blocks = op == 0 ? l.reduce_blocks : l.place_blocks;
     const int64_t per_launch = blocks * budget_tiles_per_block(plan, op, l);
     return (ntiles + per_launch - 1) / per_launch;
-}
-
-tide_status stream_device(hipStream_t stream, int* dev) {
-    if (stream) {
-        hipError_t e = hipStreamGetDevice(stream, dev);
-        if (e != hipSuccess) return hip_fail(e, "hipStreamGetDevice");
-        return TIDE_OK;
-    }
-    hipError_t e = hipGetDevice(dev);
-    if (e != hipSuccess) return hip_fail(e, "hipGetDevice");
-    return TIDE_OK;
 }
 
 // Device state of `plan` on `dev` (created on first use). Caller holds plan->mu.

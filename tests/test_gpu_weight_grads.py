@@ -1,0 +1,209 @@
+"""Weight gradients, from bf16 activations and from checkpoints, for one expert
+and for many, against the definition in 64 bits on the CPU."""
+import pytest
+import torch
+
+import layer_reference as ref
+from gpu_util import dev, say
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def tide():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    import mixed_precision_rs_amd as t
+    return t
+
+
+def window(t, pad):
+    b = torch.full((t.shape[0], t.shape[1] + pad), float("nan"), dtype=torch.float32).to(t.dtype).to(dev())
+    w = b[:, pad // 2: pad // 2 + t.shape[1]]
+    w.copy_(t.to(dev()))
+    return w
+
+
+def window_bytes(t, pad):
+    """The same of an 8-bit type, with 0xFF (NaN) around it."""
+    b = torch.full((t.shape[0], t.shape[1] + pad), 0xFF, dtype=torch.uint8, device=dev())
+    b[:, pad // 2: pad // 2 + t.shape[1]] = t.view(torch.uint8).to(dev())
+    return b.view(t.dtype)[:, pad // 2: pad // 2 + t.shape[1]]
+
+
+def bound(want, mag, rows):
+    """One bf16 rounding of the result, and `rows` additions in the matrix unit
+    (and one for the old value), each off by at most a step, 2^-23, of the
+    magnitudes' sum."""
+    return 2.0 ** -8 * want.abs() + (rows + 2) * 2.0 ** -23 * mag
+
+
+def check(tide, dy, x, saved, offsets, tokens, pad=0, old=None):
+    n, O = dy.shape
+    I = x.shape[1]
+    xin = x
+    if saved:
+        s = ref.saved_of(x)
+        xv = ref.unpack(*s)
+        xin = (window_bytes(s[0], pad), window_bytes(s[1], pad))
+    else:
+        xv = x
+        xin = window(x, pad)
+    E = 1 if offsets is None else len(offsets) - 1
+    off = torch.tensor([0, n]) if offsets is None else offsets
+    want, mag, cnt = ref.weight_grads(dy, xv, off, tokens)
+    grads = torch.full((E + 2, O, I), 5.0, dtype=torch.bfloat16, device=dev())     # a guard on each side
+    if old is not None:
+        grads[1:-1] = old.to(dev())
+        want = want + old.double()
+        mag = mag + old.double().abs()
+    tide.weight_grads_bf16(window(dy, pad), xin, grads[1:-1],
+                           offsets=None if offsets is None else offsets.int().to(dev()),
+                           token_of_row=None if tokens is None else tokens.int().to(dev()),
+                           accumulate=old is not None)
+    for e in range(E):
+        ref.close(grads[1 + e], want[e], bound(want[e], mag[e], cnt[e]), "expert %d" % e)
+    assert (grads[0].cpu() == 5.0).all() and (grads[-1].cpu() == 5.0).all()
+    return grads[1:-1]
+
+
+DENSE = [(1, 1, 1), (1, 64, 64), (2, 7, 130), (15, 64, 32), (16, 65, 96), (17, 128, 128), (31, 256, 256),
+         (32, 257, 40), (33, 40, 513), (64, 300, 300), (100, 512, 2048), (129, 130, 1), (127, 1, 260),
+         (1000, 512, 160), (4097, 128, 136), (0, 16, 48), (300, 768, 264)]
+
+
+@pytest.mark.parametrize("saved", [False, True])
+@pytest.mark.parametrize("pad", [0, 8, 3])
+@pytest.mark.parametrize("n,O,I", DENSE)
+def test_one_parameter(tide, n, O, I, pad, saved):
+    say("weight_grads", n, O, I, pad, saved)
+    check(tide, ref.normal((n, O), torch.bfloat16, seed=n), ref.normal((n, I), torch.bfloat16, seed=I),
+          saved, None, None, pad)
+
+
+GROUPED = [  # tokens, k, experts, out, in, masked
+    (1, 1, 2, 64, 64, 0), (1, 8, 128, 40, 48, 0), (50, 2, 8, 96, 128, 0.2), (200, 3, 5, 257, 130, 0),
+    (300, 8, 16, 128, 256, 0.1), (97, 4, 60, 72, 33, 0.5), (30, 2, 300, 33, 64, 0), (1500, 2, 3, 264, 520, 0),
+]
+
+
+@pytest.mark.parametrize("saved", [False, True])
+@pytest.mark.parametrize("pad", [0, 3])
+@pytest.mark.parametrize("T,k,E,O,I,masked", GROUPED)
+def test_many_experts(tide, T, k, E, O, I, masked, pad, saved):
+    say("weight_grads", T, k, E, O, I, masked, pad, saved)
+    off, tok, _ = ref.route(ref.experts(T, k, E, seed=T, masked=masked).numpy(), E)
+    tokens = torch.full((T * k,), -1, dtype=torch.int64)
+    tokens[: len(tok)] = torch.from_numpy(tok)
+    dy = ref.normal((T * k, O), torch.bfloat16, seed=1)
+    dy[len(tok):] = float("nan")                        # rows behind the last: in no sum
+    check(tide, dy, ref.normal((T, I), torch.bfloat16, seed=2), saved, torch.from_numpy(off), tokens, pad)
+
+
+@pytest.mark.parametrize("saved", [False, True])
+def test_segments_without_a_sort(tide, saved):
+    """Offsets with empty experts, rows in no expert at both ends, x by row."""
+    off = torch.tensor([3, 3, 20, 20, 53, 54, 54, 90])
+    dy, x = ref.normal((100, 72), torch.bfloat16, seed=3), ref.normal((100, 80), torch.bfloat16, seed=4)
+    dy[:3] = dy[90:] = float("nan")
+    x[:3] = x[90:] = float("nan")
+    check(tide, dy, x, saved, off, None)
+
+
+@pytest.mark.parametrize("saved", [False, True])
+@pytest.mark.parametrize("E", [1, 4])
+def test_accumulate(tide, E, saved):
+    n, O, I = 200, 136, 96
+    off = None if E == 1 else torch.tensor([0, 60, 60, 130, 200])
+    check(tide, ref.normal((n, O), torch.bfloat16, seed=1), ref.normal((n, I), torch.bfloat16, seed=2), saved,
+          off, None, old=ref.normal((E, O, I), torch.bfloat16, seed=3, scale=10.0))
+
+
+def test_lists_and_tables_of_gradients(tide):
+    n, O, I, E = 150, 64, 72, 3
+    off = torch.tensor([0, 40, 90, 150], dtype=torch.int32, device=dev())
+    dy = ref.normal((n, O), torch.bfloat16, seed=1).to(dev())
+    x = ref.normal((n, I), torch.bfloat16, seed=2).to(dev())
+    whole = torch.empty(E, O, I, dtype=torch.bfloat16, device=dev())
+    tide.weight_grads_bf16(dy, x, whole, offsets=off)
+    parts = [torch.empty(O, I, dtype=torch.bfloat16, device=dev()) for _ in range(E)]
+    tide.weight_grads_bf16(dy, x, parts[::-1], offsets=off)
+    assert all(torch.equal(p, w) for p, w in zip(parts[::-1], whole))
+    again = [torch.empty_like(p) for p in parts]
+    tide.weight_grads_bf16(dy, x, tide.PointerTable(again), offsets=off)
+    assert all(torch.equal(p, w) for p, w in zip(again, whole))
+
+
+def test_not_finite_values_stay_in_their_rows_and_columns(tide):
+    n, O, I = 100, 72, 96
+    dy, x = ref.normal((n, O), torch.bfloat16, seed=5), ref.normal((n, I), torch.bfloat16, seed=6)
+    dy[4, 11] = float("nan")
+    x[50, 70] = float("inf")
+    for saved in (False, True):
+        g = torch.empty(1, O, I, dtype=torch.bfloat16, device=dev())
+        xin = x.to(dev())
+        if saved:
+            s = tuple(t.to(dev()) for t in ref.saved_of(x))
+            xin = s
+        tide.weight_grads_bf16(dy.to(dev()), xin, g)
+        bad = ~torch.isfinite(g[0].cpu().float())
+        want = torch.zeros(O, I, dtype=torch.bool)
+        want[11] = True
+        want[:, 70] = True
+        assert torch.equal(bad, want)
+
+
+def test_tokens_out_of_range_add_nothing(tide):
+    n, O, I = 90, 40, 64
+    tokens = torch.arange(n) % 50
+    tokens[[3, 40, 77]] = torch.tensor([-1, 50, 2 ** 31 - 1])
+    for saved in (False, True):
+        check(tide, ref.normal((n, O), torch.bfloat16, seed=1), ref.normal((50, I), torch.bfloat16, seed=2), saved,
+              torch.tensor([0, 44, 90]), tokens)
+
+
+def test_offsets_past_the_rows_are_clamped(tide):
+    n, O, I = 70, 40, 64
+    dy, x = ref.normal((n, O), torch.bfloat16, seed=1).to(dev()), ref.normal((n, I), torch.bfloat16, seed=2).to(dev())
+    a, b = (torch.empty(2, O, I, dtype=torch.bfloat16, device=dev()) for _ in range(2))
+    tide.weight_grads_bf16(dy, x, a, offsets=torch.tensor([-5, 30, 900], dtype=torch.int32, device=dev()))
+    tide.weight_grads_bf16(dy, x, b, offsets=torch.tensor([0, 30, 70], dtype=torch.int32, device=dev()))
+    assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("saved", [False, True])
+def test_same_bits_every_time(tide, saved):
+    n, O, I = 3001, 264, 520
+    dy, x = ref.normal((n, O), torch.bfloat16, seed=1).to(dev()), ref.normal((n, I), torch.bfloat16, seed=2)
+    xin = tuple(t.to(dev()) for t in ref.saved_of(x)) if saved else x.to(dev())
+    first = torch.empty(1, O, I, dtype=torch.bfloat16, device=dev())
+    tide.weight_grads_bf16(dy, xin, first)
+    for _ in range(5):
+        g = torch.full_like(first, 9.0)
+        tide.weight_grads_bf16(dy, xin, g)
+        assert torch.equal(g, first)
+
+
+@pytest.mark.parametrize("saved", [False, True])
+def test_rows_past_32_bit_offsets(tide, saved):
+    n, O, I, stride = 2200, 40, 48, 1 << 21
+    if torch.cuda.mem_get_info()[0] < 30 << 30:
+        pytest.skip("needs 30 GiB of GPU memory")
+    dy, x = ref.normal((n, O), torch.bfloat16, seed=1), ref.normal((n, I), torch.bfloat16, seed=2)
+    far = torch.empty(n, stride, dtype=torch.bfloat16, device=dev())
+    d = far[:, 16: 16 + O]
+    d.copy_(dy.to(dev()))
+    if saved:
+        s = ref.saved_of(x)
+        c = torch.empty(n, stride, dtype=torch.uint8, device=dev())
+        c[:, 32: 32 + I] = s[0].view(torch.uint8).to(dev())
+        xin = (c.view(torch.float8_e4m3fn)[:, 32: 32 + I], s[1].to(dev()))
+        xv = ref.unpack(*s)
+    else:
+        xin = torch.empty(n, stride, dtype=torch.bfloat16, device=dev())[:, 16: 16 + I]
+        xin.copy_(x.to(dev()))
+        xv = x
+    g = torch.empty(1, O, I, dtype=torch.bfloat16, device=dev())
+    tide.weight_grads_bf16(d, xin, g)
+    want, mag, cnt = ref.weight_grads(dy, xv, torch.tensor([0, n]), None)
+    ref.close(g[0], want[0], bound(want[0], mag[0], cnt[0]))
