@@ -3,6 +3,7 @@
 // straight into the parameter's gradient tensor.
 #include <algorithm>
 #include <climits>
+#include <cstdio>
 #include <new>
 #include <vector>
 
@@ -29,18 +30,339 @@ struct Args {
     const int32_t* tokens;             // row of x of each row of dy, or NULL: its own
     int64_t dy_stride, x_stride, codes_stride, scales_stride;
     int64_t n, x_rows, O, I;
-    int32_t accumulate, tiles_o, tiles_i, first;
+    int32_t accumulate, tiles_o, tiles_i, first, count;
 };
 
+typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
-constexpr int kTile = 64, kDepth = 16, kPitch = kTile + 2;
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+#define TIDE_LDS __attribute__((address_space(3)))
 
-__global__ __launch_bounds__(256) void weight_grads(Args a, GradPtrs g) {
-    __shared__ uint16_t A[kDepth * kPitch], B[kDepth * kPitch];
+constexpr int kDepth = 64;             // rows (tokens) of one stage
+constexpr uint32_t kBufferWord = 0x00020000;      // raw buffer, bounds checked in bytes
+constexpr uint32_t kOutside = 0xFFFFFFF0u;        // past every buffer: loads read 0
+
+// Position of 16-byte chunk c (8 elements) of row t in a staged row: rows t,
+// t + 1, t + 2, t + 3 place one column 64 bytes apart, so the four rows that a
+// transposing read takes at once come from different banks.
+__device__ __forceinline__ int chunk_at(int t, int c) { return c ^ ((t & 3) << 2); }
+
+__device__ __forceinline__ u32x4 buffer16(__amdgpu_buffer_rsrc_t r, uint32_t at) {
+    return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, (int)at, 0, 0));
+}
+
+// Sixteen e4m3 codes with one scale as two chunks of bf16 (exact).
+__device__ __forceinline__ void decode16(u32x4 c, float scale, u32x4& lo, u32x4& hi) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t a = __builtin_bit_cast(
+            uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((int)c[i], scale, false));
+        const uint32_t b = __builtin_bit_cast(
+            uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((int)c[i], scale, true));
+        u32x4& d = i < 2 ? lo : hi;
+        d[2 * (i & 1)] = a;
+        d[2 * (i & 1) + 1] = b;
+    }
+}
+
+__device__ __forceinline__ u32x4 codes16(const uint8_t* p, int n) {
+    if (n >= 16) return *gbl<u32x4_a1>(p);
+    u32x4 c = {0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < 15; ++i)
+        if (i < n) c[i / 4] |= (uint32_t)*gbl<uint8_t>(p + i) << (8 * (i & 3));
+    return c;
+}
+
+// A kTile x kTile tile of one expert's gradient. Rows of dy and x are staged in
+// LDS as bf16, kDepth at a time, and read back transposed
+// (ds_read_b64_tr_b16), since the matrix instruction wants the summed index
+// (the row) inside a lane; products are 32x32x16 bf16 with fp32 sums. The 256
+// tile has 8 waves of 128 x 64 (128 sums a lane, two waves a SIMD: 4 waves of
+// 128 x 128 leave every wait exposed and reach 1060 instead of 1200 TFLOP/s on
+// 8192 x 8192 x 8192), the 128 tile 4 of 64 x 64.
+// kSaved: x is a checkpoint, decoded on its way into LDS (exact, and free:
+// both forms run at 1150 TFLOP/s). kWide: every row starts on 16 bytes and
+// holds whole loads, which are bounds-checked buffer loads; otherwise any
+// alignment, one row at a time.
+template <int kTile, int kThreads, bool kSaved, bool kWide>
+struct Tile {
+    static constexpr int TO = kTile, TI = kTile;
+    static constexpr int WO = 2, WI = kThreads / 64 / WO;      // waves over the tile
+    static constexpr int FO = TO / WO / 32, FI = TI / WI / 32;  // 32 x 32 blocks of a wave
+    static constexpr int kSteps = kDepth / 16;                 // matrix steps of a stage
+    static constexpr int kParts = 2;                           // steps that move a stage's chunks
+    static constexpr int CO = TO / 8;                          // chunks of a staged row of dy
+    static constexpr int NO = kDepth * CO / kThreads;          // chunks of dy a thread stages
+    static constexpr int CI = TI / (kSaved ? 16 : 8);          // 16-byte loads of a row of x
+    static constexpr int NI = kDepth * CI / kThreads;
+    static_assert(kSteps == 4, "the steps of sum()");
+    static constexpr int kStage = kDepth * (TO + TI);          // elements of one stage
+    static constexpr int kLds = 2 * kStage * 2 > TO * TI * 2 ? 2 * kStage * 2 : TO * TI * 2;
+
+    const Args& a;
+    uint16_t* lds;
+    int64_t lo, hi, o0, i0;
+    int tid, lane, wave;
+    // what the next stage's chunks were loaded from and hold
+    u32x4 ro[NO], ri[NI];
+    uint32_t rs[kSaved ? NI : 1];
+    int32_t tok[NI];
+
+    __device__ __forceinline__ uint16_t* stage_o(int b) { return lds + b * kStage; }
+    __device__ __forceinline__ uint16_t* stage_i(int b) { return lds + b * kStage + kDepth * TO; }
+
+    // Rows of x of the stage that starts at t0 (0 without token indices and
+    // past the last row: no load uses those).
+    __device__ __forceinline__ void load_tokens(int64_t t0) {
+        const int64_t left = hi - t0 < 0 ? 0 : hi - t0;
+        const int rows = left < kDepth ? (int)left : kDepth;
+        const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(
+            (void*)(a.tokens + t0), (short)0, a.tokens ? rows * 4 : 0, (int)kBufferWord);
+#pragma unroll
+        for (int j = 0; j < NI; ++j) {
+            const int t = j * (kThreads / CI) + tid / CI;
+            tok[j] = __builtin_amdgcn_raw_buffer_load_b32(r, t * 4, 0, 0);
+        }
+    }
+
+    // Part kPart of kOf of the loads of the stage at t0.
+    template <int kPart, int kOf>
+    __device__ __forceinline__ void load(int64_t t0) {
+        const int64_t left = hi - t0 < 0 ? 0 : hi - t0;
+        const int rows = left < kDepth ? (int)left : kDepth;
+        if constexpr (kWide) {
+            const __amdgpu_buffer_rsrc_t d = __builtin_amdgcn_make_buffer_rsrc(
+                (void*)(a.dy + t0 * a.dy_stride), (short)0, (int)(rows * (uint32_t)a.dy_stride * 2),
+                (int)kBufferWord);
+#pragma unroll
+            for (int j = kPart * NO / kOf; j < (kPart + 1) * NO / kOf; ++j) {
+                const int t = j * (kThreads / CO) + tid / CO, c = tid % CO;
+                const uint32_t out = o0 + c * 8 < a.O && t < rows ? 0 : kOutside;
+                ro[j] = buffer16(d, out | ((uint32_t)t * (uint32_t)a.dy_stride * 2 + (uint32_t)(o0 + c * 8) * 2));
+            }
+            // with token indices the whole of x is one buffer, without the stage's rows are
+            const uint32_t stride = (uint32_t)(kSaved ? a.codes_stride : a.x_stride * 2);
+            const uint8_t* base = kSaved ? a.codes : (const uint8_t*)a.x;
+            const uint32_t span = a.tokens ? (uint32_t)a.x_rows : (uint32_t)rows;
+            const int64_t first = a.tokens ? 0 : t0;
+            const __amdgpu_buffer_rsrc_t x = __builtin_amdgcn_make_buffer_rsrc(
+                (void*)(base + first * stride), (short)0, (int)(span * stride), (int)kBufferWord);
+            __amdgpu_buffer_rsrc_t s = x;
+            if constexpr (kSaved)
+                s = __builtin_amdgcn_make_buffer_rsrc((void*)(a.scales + first * a.scales_stride), (short)0,
+                                                      (int)(span * (uint32_t)a.scales_stride), (int)kBufferWord);
+#pragma unroll
+            for (int j = kPart * NI / kOf; j < (kPart + 1) * NI / kOf; ++j) {
+                const int t = j * (kThreads / CI) + tid / CI, c = tid % CI;
+                const uint32_t row = a.tokens ? (uint32_t)tok[j] : (uint32_t)t;
+                const int64_t col = i0 + c * (kSaved ? 16 : 8);
+                // or'ed in rather than selected, so that no branch guards the products
+                const uint32_t out = row < span && t < rows && col < a.I ? 0 : kOutside;
+                ri[j] = buffer16(x, out | (row * stride + (uint32_t)col * (kSaved ? 1 : 2)));
+                if constexpr (kSaved)
+                    rs[j] = __builtin_amdgcn_raw_buffer_load_b8(
+                        s, (int)(out | (row * (uint32_t)a.scales_stride + (uint32_t)col / kBlock)), 0, 0);
+            }
+        } else {
+#pragma unroll
+            for (int j = kPart * NO / kOf; j < (kPart + 1) * NO / kOf; ++j) {
+                const int t = j * (kThreads / CO) + tid / CO, c = tid % CO;
+                const int64_t n = a.O - o0 - c * 8;
+                ro[j] = u32x4{};
+                if (n > 0 && t < rows)
+                    ro[j] = load8(a.dy + (t0 + t) * a.dy_stride + o0 + c * 8, (int)(n < 8 ? n : 8)).a;
+            }
+#pragma unroll
+            for (int j = kPart * NI / kOf; j < (kPart + 1) * NI / kOf; ++j) {
+                const int t = j * (kThreads / CI) + tid / CI, c = tid % CI;
+                const int64_t row = t >= rows ? -1 : a.tokens ? tok[j] : t0 + t;
+                const int64_t col = i0 + c * (kSaved ? 16 : 8), n = a.I - col;
+                ri[j] = u32x4{};
+                if constexpr (kSaved) rs[j] = 0;
+                if (n > 0 && row >= 0 && row < a.x_rows) {
+                    if constexpr (kSaved) {
+                        ri[j] = codes16(a.codes + row * a.codes_stride + col, (int)(n < 16 ? n : 16));
+                        rs[j] = *gbl<uint8_t>(a.scales + row * a.scales_stride + col / kBlock);
+                    } else {
+                        ri[j] = load8(a.x + row * a.x_stride + col, (int)(n < 8 ? n : 8)).a;
+                    }
+                }
+            }
+        }
+    }
+
+    // Part of the loaded chunks into LDS buffer b.
+    template <int kPart, int kOf>
+    __device__ __forceinline__ void store(int b) {
+#pragma unroll
+        for (int j = kPart * NO / kOf; j < (kPart + 1) * NO / kOf; ++j) {
+            const int t = j * (kThreads / CO) + tid / CO, c = tid % CO;
+            *(u32x4*)(stage_o(b) + t * TO + chunk_at(t, c) * 8) = ro[j];
+        }
+#pragma unroll
+        for (int j = kPart * NI / kOf; j < (kPart + 1) * NI / kOf; ++j) {
+            const int t = j * (kThreads / CI) + tid / CI, c = tid % CI;
+            if constexpr (kSaved) {
+                u32x4 p, q;
+                decode16(ri[j], __uint_as_float(rs[j] << 23), p, q);
+                u32x4* d = (u32x4*)(stage_i(b) + t * TI + chunk_at(t, 2 * c) * 8);
+                d[0] = p;
+                d[1] = q;
+            } else {
+                *(u32x4*)(stage_i(b) + t * TI + chunk_at(t, c) * 8) = ri[j];
+            }
+        }
+    }
+
+    // A 32-column block of 16 staged rows as a matrix operand: lane l holds
+    // column l % 32, rows (l / 32) * 8 + 0 .. 7. Each transposing read gives a
+    // lane four rows of one column out of the 4 x 16 blocks that 16 lanes name.
+    __device__ __forceinline__ bf16x8 operand(const uint16_t* rows, int width, int step, int col) {
+        const int t = step * 16 + (lane >> 5) * 8 + ((lane & 15) >> 2);
+        const int c = (col >> 3) + ((lane >> 4) & 1) * 2 + ((lane & 3) >> 1);
+        const uint16_t* p = rows + t * width + chunk_at(t, c) * 8 + (lane & 1) * 4;
+        const s16x4 u = __builtin_amdgcn_ds_read_tr16_b64_v4i16((TIDE_LDS s16x4*)p);
+        const s16x4 v = __builtin_amdgcn_ds_read_tr16_b64_v4i16((TIDE_LDS s16x4*)(p + 4 * width));
+        const bf16x4 x = __builtin_bit_cast(bf16x4, u), y = __builtin_bit_cast(bf16x4, v);
+        return __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7);
+    }
+    __device__ __forceinline__ void operands(int b, int step, bf16x8 (&fo)[FO], bf16x8 (&fi)[FI]) {
+#pragma unroll
+        for (int f = 0; f < FO; ++f) fo[f] = operand(stage_o(b), TO, step, (wave / WI) * (TO / WO) + f * 32);
+#pragma unroll
+        for (int f = 0; f < FI; ++f) fi[f] = operand(stage_i(b), TI, step, (wave % WI) * (TI / WI) + f * 32);
+    }
+
+    // Asks the scheduler to spread a step's LDS and memory instructions over
+    // its matrix instructions, each of which leaves 32 cycles to issue others.
+    template <int kStep, int kAt = 0>
+    __device__ __forceinline__ void interleave() {
+        constexpr int kMatrix = 0x8, kRead = 0x100, kWrite = 0x200, kLoad = 0x20, kVector = 0x2;
+        constexpr int M = FO * FI, R = 2 * (FO + FI);
+        constexpr bool moves = kStep < kParts;
+        constexpr int W = moves ? (NO + (kSaved ? 2 : 1) * NI) / kParts : 0;
+        constexpr int L = moves ? (NO + (kSaved ? 2 : 1) * NI) / kParts : kStep == kParts ? NI : 0;
+        if constexpr (kAt < M) {
+            constexpr int r = (kAt + 1) * R / M - kAt * R / M, w = (kAt + 1) * W / M - kAt * W / M;
+            constexpr int l = (kAt + 1) * L / M - kAt * L / M;
+            __builtin_amdgcn_sched_group_barrier(kMatrix, 1, 0);
+            if constexpr (r > 0) __builtin_amdgcn_sched_group_barrier(kRead, r, 0);
+            if constexpr (moves) __builtin_amdgcn_sched_group_barrier(kVector, 3, 0);
+            if constexpr (w > 0) __builtin_amdgcn_sched_group_barrier(kWrite, w, 0);
+            if constexpr (l > 0) __builtin_amdgcn_sched_group_barrier(kLoad, l, 0);
+            interleave<kStep, kAt + 1>();
+        }
+    }
+
+    template <int kStep>
+    __device__ __forceinline__ void step(int64_t t0, int b, bf16x8 (&fo)[2][FO], bf16x8 (&fi)[2][FI],
+                                         f32x16 (&acc)[FO][FI]) {
+        constexpr int now = kStep & 1, next = now ^ 1;
+        if constexpr (kStep < kSteps - 1) {
+            operands(b, kStep + 1, fo[next], fi[next]);
+        } else {
+            __syncthreads();
+            operands(b ^ 1, 0, fo[next], fi[next]);
+        }
+        if constexpr (kStep < kParts) {
+            store<kStep, kParts>(b ^ 1);
+            load<kStep, kParts>(t0 + 2 * kDepth);
+        }
+        if constexpr (kStep == kParts) load_tokens(t0 + 3 * kDepth);
+#pragma unroll
+        for (int x = 0; x < FO; ++x)
+#pragma unroll
+            for (int y = 0; y < FI; ++y)
+                acc[x][y] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fi[now][y], fo[now][x], acc[x][y], 0, 0, 0);
+        if constexpr (kWide) interleave<kStep>();
+    }
+
+    // The sum over rows [lo, hi). A step's operands are read while the step
+    // before is multiplied; a stage is loaded two ahead and written to LDS
+    // one ahead, in the shadow of the matrix instructions; one barrier a
+    // stage, before its last step, by when nothing of it is left to read.
+    __device__ __forceinline__ void sum(f32x16 (&acc)[FO][FI]) {
+        if (lo >= hi) return;
+        load_tokens(lo);
+        load<0, 1>(lo);
+        load_tokens(lo + kDepth);
+        store<0, 1>(0);
+        load<0, 1>(lo + kDepth);
+        load_tokens(lo + 2 * kDepth);
+        __syncthreads();
+        bf16x8 fo[2][FO], fi[2][FI];
+        operands(0, 0, fo[0], fi[0]);
+        int b = 0;
+        for (int64_t t0 = lo; t0 < hi; t0 += kDepth, b ^= 1) {
+            step<0>(t0, b, fo, fi, acc);
+            step<1>(t0, b, fo, fi, acc);
+            step<2>(t0, b, fo, fi, acc);
+            step<3>(t0, b, fo, fi, acc);
+        }
+        __syncthreads();
+    }
+
+    // acc[x][y]: lane l holds out row (o) l % 32 of the block, and for each
+    // group of four registers four consecutive in columns (i). The tile goes
+    // through LDS so that whole rows are stored; chunks are placed by row so
+    // that neither side meets a bank twice.
+    __device__ __forceinline__ void finish(f32x16 (&acc)[FO][FI], uint16_t* out) {
+        constexpr int C = TI / 8;
+#pragma unroll
+        for (int x = 0; x < FO; ++x) {
+            const int o = (wave / WI) * (TO / WO) + x * 32 + (lane & 31);
+#pragma unroll
+            for (int y = 0; y < FI; ++y) {
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int i = (wave % WI) * (TI / WI) + y * 32 + r * 8 + (lane >> 5) * 4;
+                    float v[4];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        v[q] = acc[x][y][r * 4 + q];
+                        if (a.accumulate && o0 + o < a.O && i0 + i + q < a.I)
+                            v[q] += lo_bf16(*gbl<uint16_t>(out + (o0 + o) * a.I + i0 + i + q));
+                    }
+                    const u32x2 p = {pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
+                    *(u32x2*)(lds + o * TI + ((i >> 3) ^ (o & (C - 1))) * 8 + (i & 4)) = p;
+                }
+            }
+        }
+        __syncthreads();
+        for (int j = tid; j < TO * C; j += kThreads) {
+            const int o = j / C, c = (j % C) ^ (o & (C - 1));
+            const int64_t n = a.I - i0 - c * 8;
+            if (o0 + o >= a.O || n <= 0) continue;
+            const u32x4 v = *(const u32x4*)(lds + j * 8);
+            uint16_t* d = out + (o0 + o) * a.I + i0 + c * 8;
+            if (n >= 8) {
+                *gbl_mut<u32x4_a2>(d) = v;
+            } else {
+#pragma unroll
+                for (int q = 0; q < 7; ++q)
+                    if (q < n) *gbl_mut<uint16_t>(d + q) = (uint16_t)(v[q / 2] >> (16 * (q & 1)));
+            }
+        }
+    }
+};
+
+template <int kTile, int kThreads, bool kSaved, bool kWide>
+__global__ __launch_bounds__(kThreads, 2) void weight_grads(Args a, GradPtrs g) {
+    using K = Tile<kTile, kThreads, kSaved, kWide>;
+    __shared__ __attribute__((aligned(1024))) uint16_t lds[K::kLds / 2];
+    // Workgroups go round robin over the XCDs: each XCD gets one run of tiles,
+    // so that tiles that share rows share an L2.
+    const int per = gridDim.x / 8, at = (int)(blockIdx.x % 8) * per + (int)(blockIdx.x / 8);
     const int tiles = a.tiles_o * a.tiles_i;
-    const int e = blockIdx.x / tiles, tile = blockIdx.x - e * tiles;
-    const int64_t o0 = (int64_t)(tile / a.tiles_i) * kTile, i0 = (int64_t)(tile % a.tiles_i) * kTile;
+    if (at >= a.count * tiles) return;
+    const int e = at / tiles;
+    int tile = at - e * tiles;
+    // within an expert, bands of 8 tile rows, walked column by column
+    const int band = tile / (8 * a.tiles_i), high = min(8, a.tiles_o - band * 8);
+    tile -= band * 8 * a.tiles_i;
+    const int to = band * 8 + tile % high, ti = tile / high;
     int64_t lo = 0, hi = a.n;
     if (a.offsets) {
         lo = a.offsets[a.first + e];
@@ -48,54 +370,38 @@ __global__ __launch_bounds__(256) void weight_grads(Args a, GradPtrs g) {
         lo = lo < 0 ? 0 : lo > a.n ? a.n : lo;
         hi = hi < lo ? lo : hi > a.n ? a.n : hi;
     }
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int m0 = (wave >> 1) * 32, n0 = (wave & 1) * 32;
-    f32x16 acc = {};
-    for (int64_t t0 = lo; t0 < hi; t0 += kDepth) {
-        for (int i = threadIdx.x; i < kDepth * kTile; i += 256) {
-            const int t = i / kTile, c = i % kTile;
-            const int64_t row = t0 + t;
-            uint16_t va = 0, vb = 0;
-            if (row < hi) {
-                if (o0 + c < a.O) va = a.dy[row * a.dy_stride + o0 + c];
-                const int64_t xr = a.tokens ? a.tokens[row] : row;
-                if (i0 + c < a.I && xr >= 0 && xr < a.x_rows) {
-                    if (a.x) {
-                        vb = a.x[xr * a.x_stride + i0 + c];
-                    } else {
-                        const float v = __builtin_amdgcn_cvt_f32_fp8(
-                            a.codes[xr * a.codes_stride + i0 + c], 0);
-                        const float s = __uint_as_float(
-                            (uint32_t)a.scales[xr * a.scales_stride + (i0 + c) / kBlock] << 23);
-                        vb = (uint16_t)pack_bf16(v * s, 0.0f);
-                    }
-                }
-            }
-            A[t * kPitch + c] = va;
-            B[t * kPitch + c] = vb;
-        }
-        __syncthreads();
-        bf16x8 fa, fb;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const int t = (lane >> 5) * 8 + j;
-            fa[j] = __builtin_bit_cast(__bf16, A[t * kPitch + m0 + (lane & 31)]);
-            fb[j] = __builtin_bit_cast(__bf16, B[t * kPitch + n0 + (lane & 31)]);
-        }
-        acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa, fb, acc, 0, 0, 0);
-        __syncthreads();
+    K k{a, lds, lo, hi, (int64_t)to * kTile, (int64_t)ti * kTile, (int)threadIdx.x, (int)threadIdx.x & 63,
+        (int)threadIdx.x >> 6, {}, {}, {}, {}};
+    f32x16 acc[K::FO][K::FI] = {};
+    k.sum(acc);
+    k.finish(acc, g.p[e]);
+}
+
+template <int kTile, int kThreads>
+hipError_t launch_tiles(Args a, const GradPtrs& g, bool wide, hipStream_t stream) {
+    const int64_t groups = (int64_t)a.count * a.tiles_o * a.tiles_i;
+    const dim3 grid((uint32_t)((groups + 7) / 8 * 8));
+    if (a.codes) {
+        if (wide) weight_grads<kTile, kThreads, true, true><<<grid, dim3(kThreads), 0, stream>>>(a, g);
+        else weight_grads<kTile, kThreads, true, false><<<grid, dim3(kThreads), 0, stream>>>(a, g);
+    } else {
+        if (wide) weight_grads<kTile, kThreads, false, true><<<grid, dim3(kThreads), 0, stream>>>(a, g);
+        else weight_grads<kTile, kThreads, false, false><<<grid, dim3(kThreads), 0, stream>>>(a, g);
     }
-    uint16_t* out = g.p[e];
-#pragma unroll
-    for (int r = 0; r < 16; ++r) {
-        const int64_t o = o0 + m0 + (r & 3) + 8 * (r >> 2) + 4 * (lane >> 5);
-        const int64_t i = i0 + n0 + (lane & 31);
-        if (o < a.O && i < a.I) {
-            float v = acc[r];
-            if (a.accumulate) v += lo_bf16(out[o * a.I + i]);
-            out[o * a.I + i] = (uint16_t)pack_bf16(v, 0.0f);
-        }
-    }
+    return hipGetLastError();
+}
+
+// Whether every load can be a 16-byte bounds-checked buffer load: rows start
+// on 16 bytes and hold whole loads, and 32-bit byte offsets reach a stage of
+// dy and, with token indices, all of x.
+bool wide_loads(const Args& a) {
+    const int64_t step = a.codes ? 16 : 8, xs = a.codes ? a.codes_stride : a.x_stride * 2;
+    const uintptr_t base = a.codes ? (uintptr_t)a.codes : (uintptr_t)a.x;
+    const int64_t rows = a.tokens ? a.x_rows : kDepth;
+    const int64_t lim = (int64_t)0xF0000000;
+    return a.O % 8 == 0 && a.I % step == 0 && ((uintptr_t)a.dy & 15) == 0 && a.dy_stride % 8 == 0 &&
+           (base & 15) == 0 && xs % 16 == 0 && a.dy_stride <= lim / 2 / kDepth && xs <= lim / rows &&
+           a.scales_stride <= lim / rows;
 }
 
 #define TIDE_TRY(expr)                        \
@@ -103,6 +409,16 @@ __global__ __launch_bounds__(256) void weight_grads(Args a, GradPtrs g) {
         tide_status s_ = (expr);              \
         if (s_ != TIDE_OK) return s_;         \
     } while (0)
+
+// Tile edge: 256 reuses each staged element 256 times and feeds the matrix
+// units best (1150 against 870 TFLOP/s on 28672 x 8192 from 4096 rows), once
+// there are tiles for most of the 256 CUs; with 128 tiles of 256 (1024 x 8192)
+// 512 of 128 are faster (178 against 193 us), with 192 (8 experts of 1984 x
+// 704) they are not (36 against 33 us).
+int choose_tile(const Args& a, int32_t experts) {
+    const int64_t big = ((a.O + 255) / 256) * ((a.I + 255) / 256);
+    return big > 160 / experts ? 256 : 128;
+}
 
 tide_status check_sizes(int64_t n, int64_t O, int64_t I, int32_t experts) {
     if (n < 0 || O < 0 || I < 0 || experts < 1)
@@ -198,7 +514,9 @@ tide_status tide_weight_grads_bf16(const uint16_t* dy, int64_t dy_stride, int64_
         a.O = out;
         a.I = in;
         a.accumulate = accumulate ? 1 : 0;
-        const int64_t to = (out + kTile - 1) / kTile, ti = (in + kTile - 1) / kTile;
+        if (x_rows == 0) a.n = 0;              // no row of x to add
+        const int tile = choose_tile(a, experts);
+        const int64_t to = (out + tile - 1) / tile, ti = (in + tile - 1) / tile;
         if (to > kMaxGroups / ti)
             return fail(TIDE_ERR_UNSUPPORTED, "gradients of %lld x %lld", (long long)out, (long long)in);
         a.tiles_o = (int32_t)to;
@@ -209,8 +527,11 @@ tide_status tide_weight_grads_bf16(const uint16_t* dy, int64_t dy_stride, int64_
             GradPtrs g{};
             for (int32_t e = 0; e < ne; ++e) g.p[e] = grads[e0 + e];
             a.first = e0;
-            weight_grads<<<dim3((uint32_t)(ne * to * ti)), dim3(256), 0, stream>>>(a, g);
-            TIDE_HIP_TRY(hipGetLastError());
+            a.count = ne;
+            const bool wide = wide_loads(a);
+            const hipError_t launched = tile == 256 ? launch_tiles<256, 512>(a, g, wide, stream)
+                                                    : launch_tiles<128, 256>(a, g, wide, stream);
+            if (launched != hipSuccess) return hip_fail(launched, "weight_grads");
         }
         return TIDE_OK;
     } catch (const std::bad_alloc&) {

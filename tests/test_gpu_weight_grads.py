@@ -101,6 +101,28 @@ def test_many_experts(tide, T, k, E, O, I, masked, pad, saved):
 
 
 @pytest.mark.parametrize("saved", [False, True])
+@pytest.mark.parametrize("pad", [0, 3])
+@pytest.mark.parametrize("n,O,I", [(1, 4096, 2816), (64, 4104, 2600), (100, 2570, 4611), (333, 4160, 2592)])
+def test_one_large_parameter(tide, n, O, I, pad, saved):
+    """Enough tiles for the large ones, ragged at both edges."""
+    say("weight_grads", n, O, I, pad, saved)
+    check(tide, ref.normal((n, O), torch.bfloat16, seed=n), ref.normal((n, I), torch.bfloat16, seed=I),
+          saved, None, None, pad)
+
+
+@pytest.mark.parametrize("saved", [False, True])
+@pytest.mark.parametrize("pad", [0, 3])
+@pytest.mark.parametrize("T,k,E,O,I", [(700, 4, 48, 512, 520), (333, 8, 64, 257, 513), (2000, 1, 170, 136, 48)])
+def test_many_experts_in_large_tiles(tide, T, k, E, O, I, pad, saved):
+    say("weight_grads", T, k, E, O, I, pad, saved)
+    off, tok, _ = ref.route(ref.experts(T, k, E, seed=T, masked=0.05).numpy(), E)
+    tokens = torch.full((T * k,), -1, dtype=torch.int64)
+    tokens[: len(tok)] = torch.from_numpy(tok)
+    check(tide, ref.normal((T * k, O), torch.bfloat16, seed=1), ref.normal((T, I), torch.bfloat16, seed=2), saved,
+          torch.from_numpy(off), tokens, pad)
+
+
+@pytest.mark.parametrize("saved", [False, True])
 def test_segments_without_a_sort(tide, saved):
     """Offsets with empty experts, rows in no expert at both ends, x by row."""
     off = torch.tensor([3, 3, 20, 20, 53, 54, 54, 90])
