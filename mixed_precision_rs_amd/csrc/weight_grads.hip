@@ -40,6 +40,11 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 #define TIDE_LDS __attribute__((address_space(3)))
 
 constexpr int kDepth = 64;             // rows (tokens) of one stage
+// How rows are read. Buffers: every row starts on 16 bytes and holds whole
+// 16-byte loads, which are bounds-checked buffer loads. Vectors: any alignment
+// and length from one load on; a row's last load ends at its end and is
+// shifted into place. Elements: rows shorter than a load.
+enum Access { kBuffers, kVectors, kElements };
 constexpr uint32_t kBufferWord = 0x00020000;      // raw buffer, bounds checked in bytes
 constexpr uint32_t kOutside = 0xFFFFFFF0u;        // past every buffer: loads read 0
 
@@ -75,6 +80,17 @@ __device__ __forceinline__ u32x4 codes16(const uint8_t* p, int n) {
     return c;
 }
 
+// v moved down by n bytes, n < 16.
+__device__ __forceinline__ u32x4 shift_down(u32x4 v, int n) {
+    if (n & 8) v = u32x4{v[2], v[3], 0, 0};
+    if (n & 4) v = u32x4{v[1], v[2], v[3], 0};
+    const int b = (n & 3) * 8;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        v[i] = (uint32_t)(((uint64_t)(i < 3 ? v[i + 1] : 0) << 32 | v[i]) >> b);
+    return v;
+}
+
 // A kTile x kTile tile of one expert's gradient. Rows of dy and x are staged in
 // LDS as bf16, kDepth at a time, and read back transposed
 // (ds_read_b64_tr_b16), since the matrix instruction wants the summed index
@@ -83,10 +99,8 @@ __device__ __forceinline__ u32x4 codes16(const uint8_t* p, int n) {
 // 128 x 128 leave every wait exposed and reach 1060 instead of 1200 TFLOP/s on
 // 8192 x 8192 x 8192), the 128 tile 4 of 64 x 64.
 // kSaved: x is a checkpoint, decoded on its way into LDS (exact, and free:
-// both forms run at 1150 TFLOP/s). kWide: every row starts on 16 bytes and
-// holds whole loads, which are bounds-checked buffer loads; otherwise any
-// alignment, one row at a time.
-template <int kTile, int kThreads, bool kSaved, bool kWide>
+// both forms run at 1150 TFLOP/s).
+template <int kTile, int kThreads, bool kSaved, int kAccess>
 struct Tile {
     static constexpr int TO = kTile, TI = kTile;
     static constexpr int WO = 2, WI = kThreads / 64 / WO;      // waves over the tile
@@ -108,6 +122,7 @@ struct Tile {
     // what the next stage's chunks were loaded from and hold
     u32x4 ro[NO], ri[NI];
     uint32_t rs[kSaved ? NI : 1];
+    uint32_t none;                     // Vectors: bit j: ro[j], bit 16 + j: ri[j] is of no row
     int32_t tok[NI];
 
     __device__ __forceinline__ uint16_t* stage_o(int b) { return lds + b * kStage; }
@@ -132,7 +147,7 @@ struct Tile {
     __device__ __forceinline__ void load(int64_t t0) {
         const int64_t left = hi - t0 < 0 ? 0 : hi - t0;
         const int rows = left < kDepth ? (int)left : kDepth;
-        if constexpr (kWide) {
+        if constexpr (kAccess == kBuffers) {
             const __amdgpu_buffer_rsrc_t d = __builtin_amdgcn_make_buffer_rsrc(
                 (void*)(a.dy + t0 * a.dy_stride), (short)0, (int)(rows * (uint32_t)a.dy_stride * 2),
                 (int)kBufferWord);
@@ -165,6 +180,30 @@ struct Tile {
                     rs[j] = __builtin_amdgcn_raw_buffer_load_b8(
                         s, (int)(out | (row * (uint32_t)a.scales_stride + (uint32_t)col / kBlock)), 0, 0);
             }
+        } else if constexpr (kAccess == kVectors) {
+            const int64_t last = hi - 1;
+            const int64_t co = min(o0 + tid % CO * 8, a.O - 8);
+#pragma unroll
+            for (int j = kPart * NO / kOf; j < (kPart + 1) * NO / kOf; ++j) {
+                const int t = j * (kThreads / CO) + tid / CO;
+                none = (none & ~(1u << j)) | (t < rows ? 0 : 1u << j);
+                ro[j] = *gbl<u32x4_a2>(a.dy + min(t0 + t, last) * a.dy_stride + co);
+            }
+            const int64_t col = i0 + tid % CI * (kSaved ? 16 : 8), ci = min(col, a.I - (kSaved ? 16 : 8));
+#pragma unroll
+            for (int j = kPart * NI / kOf; j < (kPart + 1) * NI / kOf; ++j) {
+                const int t = j * (kThreads / CI) + tid / CI;
+                int64_t row = a.tokens ? tok[j] : t0 + t;
+                const bool in = t < rows && (uint64_t)row < (uint64_t)a.x_rows;
+                none = (none & ~(0x10000u << j)) | (in ? 0 : 0x10000u << j);
+                row = in ? row : 0;
+                if constexpr (kSaved) {
+                    ri[j] = *gbl<u32x4_a1>(a.codes + row * a.codes_stride + ci);
+                    rs[j] = *gbl<uint8_t>(a.scales + row * a.scales_stride + min(col, a.I - 1) / kBlock);
+                } else {
+                    ri[j] = *gbl<u32x4_a2>(a.x + row * a.x_stride + ci);
+                }
+            }
         } else {
 #pragma unroll
             for (int j = kPart * NO / kOf; j < (kPart + 1) * NO / kOf; ++j) {
@@ -193,17 +232,33 @@ struct Tile {
         }
     }
 
+    // Elements of a load that lie before its column; a load past the row has
+    // no column that is stored, whatever it holds.
+    static __device__ __forceinline__ int tail(int64_t col, int64_t last) {
+        return col > last ? (int)(col - last) & (kSaved ? 15 : 7) : 0;
+    }
+
     // Part of the loaded chunks into LDS buffer b.
     template <int kPart, int kOf>
     __device__ __forceinline__ void store(int b) {
 #pragma unroll
         for (int j = kPart * NO / kOf; j < (kPart + 1) * NO / kOf; ++j) {
             const int t = j * (kThreads / CO) + tid / CO, c = tid % CO;
+            if constexpr (kAccess == kVectors) {
+                if (o0 + TO > a.O) ro[j] = shift_down(ro[j], tail(o0 + c * 8, a.O - 8) * 2);
+                if (none >> j & 1) ro[j] = u32x4{};
+            }
             *(u32x4*)(stage_o(b) + t * TO + chunk_at(t, c) * 8) = ro[j];
         }
 #pragma unroll
         for (int j = kPart * NI / kOf; j < (kPart + 1) * NI / kOf; ++j) {
             const int t = j * (kThreads / CI) + tid / CI, c = tid % CI;
+            if constexpr (kAccess == kVectors) {
+                if (i0 + TI > a.I)
+                    ri[j] = kSaved ? shift_down(ri[j], tail(i0 + c * 16, a.I - 16))
+                                   : shift_down(ri[j], tail(i0 + c * 8, a.I - 8) * 2);
+                if (none >> (16 + j) & 1) ri[j] = u32x4{};
+            }
             if constexpr (kSaved) {
                 u32x4 p, q;
                 decode16(ri[j], __uint_as_float(rs[j] << 23), p, q);
@@ -276,7 +331,7 @@ struct Tile {
 #pragma unroll
             for (int y = 0; y < FI; ++y)
                 acc[x][y] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fi[now][y], fo[now][x], acc[x][y], 0, 0, 0);
-        if constexpr (kWide) interleave<kStep>();
+        if constexpr (kAccess != kElements) interleave<kStep>();
     }
 
     // The sum over rows [lo, hi). A step's operands are read while the step
@@ -348,9 +403,9 @@ struct Tile {
     }
 };
 
-template <int kTile, int kThreads, bool kSaved, bool kWide>
+template <int kTile, int kThreads, bool kSaved, int kAccess>
 __global__ __launch_bounds__(kThreads, 2) void weight_grads(Args a, GradPtrs g) {
-    using K = Tile<kTile, kThreads, kSaved, kWide>;
+    using K = Tile<kTile, kThreads, kSaved, kAccess>;
     __shared__ __attribute__((aligned(1024))) uint16_t lds[K::kLds / 2];
     // Workgroups go round robin over the XCDs: each XCD gets one run of tiles,
     // so that tiles that share rows share an L2.
@@ -371,37 +426,41 @@ __global__ __launch_bounds__(kThreads, 2) void weight_grads(Args a, GradPtrs g) 
         hi = hi < lo ? lo : hi > a.n ? a.n : hi;
     }
     K k{a, lds, lo, hi, (int64_t)to * kTile, (int64_t)ti * kTile, (int)threadIdx.x, (int)threadIdx.x & 63,
-        (int)threadIdx.x >> 6, {}, {}, {}, {}};
+        (int)threadIdx.x >> 6, {}, {}, {}, 0, {}};
     f32x16 acc[K::FO][K::FI] = {};
     k.sum(acc);
     k.finish(acc, g.p[e]);
 }
 
 template <int kTile, int kThreads>
-hipError_t launch_tiles(Args a, const GradPtrs& g, bool wide, hipStream_t stream) {
+hipError_t launch_tiles(Args a, const GradPtrs& g, Access how, hipStream_t stream) {
     const int64_t groups = (int64_t)a.count * a.tiles_o * a.tiles_i;
     const dim3 grid((uint32_t)((groups + 7) / 8 * 8));
     if (a.codes) {
-        if (wide) weight_grads<kTile, kThreads, true, true><<<grid, dim3(kThreads), 0, stream>>>(a, g);
-        else weight_grads<kTile, kThreads, true, false><<<grid, dim3(kThreads), 0, stream>>>(a, g);
+        if (how == kBuffers) weight_grads<kTile, kThreads, true, kBuffers><<<grid, dim3(kThreads), 0, stream>>>(a, g);
+        else if (how == kVectors) weight_grads<kTile, kThreads, true, kVectors><<<grid, dim3(kThreads), 0, stream>>>(a, g);
+        else if constexpr (kTile == 128) weight_grads<kTile, kThreads, true, kElements><<<grid, dim3(kThreads), 0, stream>>>(a, g);
     } else {
-        if (wide) weight_grads<kTile, kThreads, false, true><<<grid, dim3(kThreads), 0, stream>>>(a, g);
-        else weight_grads<kTile, kThreads, false, false><<<grid, dim3(kThreads), 0, stream>>>(a, g);
+        if (how == kBuffers) weight_grads<kTile, kThreads, false, kBuffers><<<grid, dim3(kThreads), 0, stream>>>(a, g);
+        else if (how == kVectors) weight_grads<kTile, kThreads, false, kVectors><<<grid, dim3(kThreads), 0, stream>>>(a, g);
+        else if constexpr (kTile == 128) weight_grads<kTile, kThreads, false, kElements><<<grid, dim3(kThreads), 0, stream>>>(a, g);
     }
     return hipGetLastError();
 }
 
-// Whether every load can be a 16-byte bounds-checked buffer load: rows start
-// on 16 bytes and hold whole loads, and 32-bit byte offsets reach a stage of
-// dy and, with token indices, all of x.
-bool wide_loads(const Args& a) {
+// The buffers' 32-bit byte offsets have to reach a stage of dy and, with token
+// indices, all of x.
+Access how_to_read(const Args& a) {
     const int64_t step = a.codes ? 16 : 8, xs = a.codes ? a.codes_stride : a.x_stride * 2;
     const uintptr_t base = a.codes ? (uintptr_t)a.codes : (uintptr_t)a.x;
     const int64_t rows = a.tokens ? a.x_rows : kDepth;
     const int64_t lim = (int64_t)0xF0000000;
-    return a.O % 8 == 0 && a.I % step == 0 && ((uintptr_t)a.dy & 15) == 0 && a.dy_stride % 8 == 0 &&
-           (base & 15) == 0 && xs % 16 == 0 && a.dy_stride <= lim / 2 / kDepth && xs <= lim / rows &&
-           a.scales_stride <= lim / rows;
+    if (a.O < 8 || a.I < step) return kElements;
+    if (a.O % 8 == 0 && a.I % step == 0 && ((uintptr_t)a.dy & 15) == 0 && a.dy_stride % 8 == 0 &&
+        (base & 15) == 0 && xs % 16 == 0 && a.dy_stride <= lim / 2 / kDepth && (rows == 0 || xs <= lim / rows) &&
+        (rows == 0 || a.scales_stride <= lim / rows))
+        return kBuffers;
+    return kVectors;
 }
 
 #define TIDE_TRY(expr)                        \
@@ -515,7 +574,8 @@ tide_status tide_weight_grads_bf16(const uint16_t* dy, int64_t dy_stride, int64_
         a.I = in;
         a.accumulate = accumulate ? 1 : 0;
         if (x_rows == 0) a.n = 0;              // no row of x to add
-        const int tile = choose_tile(a, experts);
+        const Access how = how_to_read(a);
+        const int tile = how == kElements ? 128 : choose_tile(a, experts);
         const int64_t to = (out + tile - 1) / tile, ti = (in + tile - 1) / tile;
         if (to > kMaxGroups / ti)
             return fail(TIDE_ERR_UNSUPPORTED, "gradients of %lld x %lld", (long long)out, (long long)in);
@@ -528,9 +588,8 @@ tide_status tide_weight_grads_bf16(const uint16_t* dy, int64_t dy_stride, int64_
             for (int32_t e = 0; e < ne; ++e) g.p[e] = grads[e0 + e];
             a.first = e0;
             a.count = ne;
-            const bool wide = wide_loads(a);
-            const hipError_t launched = tile == 256 ? launch_tiles<256, 512>(a, g, wide, stream)
-                                                    : launch_tiles<128, 256>(a, g, wide, stream);
+            const hipError_t launched = tile == 256 ? launch_tiles<256, 512>(a, g, how, stream)
+                                                    : launch_tiles<128, 256>(a, g, how, stream);
             if (launched != hipSuccess) return hip_fail(launched, "weight_grads");
         }
         return TIDE_OK;
