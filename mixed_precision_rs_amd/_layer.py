@@ -12,7 +12,7 @@ from typing import Optional, Sequence, Tuple, Union
 
 from ._lib import PointerTable, _check, _check_many, _load, _ptr, _record, _stream_handle
 
-_DTYPES = None           # torch dtype -> tide_dtype, filled when torch is first needed
+_DTYPES = {}             # torch dtype -> tide_dtype, filled when torch is first needed
 SCALE_BLOCK = 32         # consecutive elements of a row that share a checkpoint scale
 
 
@@ -54,10 +54,9 @@ def _fn(name: str):
 
 
 def _dtype_code(t, what: str) -> int:
-    global _DTYPES
-    if _DTYPES is None:
+    if not _DTYPES:
         import torch
-        _DTYPES = {torch.bfloat16: 0, torch.float32: 1}
+        _DTYPES.update({torch.bfloat16: 0, torch.float32: 1})
     code = _DTYPES.get(t.dtype)
     if code is None:
         raise TypeError("%s has dtype %s, expected torch.bfloat16 or torch.float32" % (what, t.dtype))
@@ -113,11 +112,36 @@ def _saved(saved, what: str, rows: Optional[int], cols: Optional[int], dev):
     return Saved(cp, sp, cs, ss), r, c
 
 
-def _on(stream):
-    """(handle, stream object or None, device or None): None when the handle is
-    a raw integer, whose device only the library can tell."""
+def _on(stream, t):
+    """(handle, stream object or None, device or None) of a call whose first
+    tensor is t. Without a stream: the current one of t's device, which need
+    not be the current device. The object is there when the tensors have to be
+    recorded on the stream, the device is None when the handle is a raw integer,
+    whose device only the library can tell."""
+    if stream is None:
+        import torch
+        dev = t.get_device()
+        if dev < 0:
+            return 0, None, None           # refused by the checks that follow
+        h = torch._C._cuda_getCurrentRawStream(dev)
+        return h, None if h == 0 else torch.cuda.current_stream(dev), dev
     h, obj = _stream_handle(stream)
     return h, obj, None if obj is None else obj.device.index
+
+
+def _run(name: str, args, dev: Optional[int], refs, sobj) -> None:
+    """Calls the library with `dev` current (the null stream is the current
+    device's) and records the tensors on the stream."""
+    import torch
+    if dev is None or dev == torch._C._cuda_getDevice():
+        st = _fn(name)(*args)
+    else:
+        with torch.cuda.device(dev):
+            st = _fn(name)(*args)
+    if st:
+        _check(st, name)
+    if sobj is not None:
+        _record(refs, sobj)
 
 
 def _workspace(need: int, workspace, stream, dev):
@@ -132,7 +156,7 @@ def _workspace(need: int, workspace, stream, dev):
     if need == 0:
         return 0, 0, None
     if stream is None:
-        w = torch.empty(need, dtype=torch.uint8, device="cuda")
+        w = torch.empty(need, dtype=torch.uint8, device=dev)
     else:
         s = torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream
         with torch.cuda.stream(s):
@@ -157,7 +181,7 @@ def route_tokens(experts, num_experts: int, offsets, token_of_row, slots, worksp
     pair has no row. workspace: uint8 tensor of route_workspace_bytes(), by
     default allocated for the call."""
     import torch
-    sh, sobj, dev = _on(stream)
+    sh, sobj, dev = _on(stream, experts)
     if experts.dim() != 2:
         raise ValueError("experts has %d dimensions, expected 2" % experts.dim())
     T, k = experts.shape
@@ -169,9 +193,8 @@ def route_tokens(experts, num_experts: int, offsets, token_of_row, slots, worksp
     sp = _flat(slots, "slots", torch.int32, (T, k), dev)
     need = route_workspace_bytes(T, k, num_experts)
     wp, wn, w = _workspace(need, workspace, stream, dev)
-    _check(_fn("tide_route_tokens")(ep, experts.element_size(), T, k, num_experts, op, tp, sp, wp,
-                                    wn, sh), "tide_route_tokens")
-    _record([experts, offsets, token_of_row, slots, w], sobj)
+    _run("tide_route_tokens", (ep, experts.element_size(), T, k, num_experts, op, tp, sp, wp,
+         wn, sh), dev, [experts, offsets, token_of_row, slots, w], sobj)
 
 
 def dispatch_tokens(x, slots, rows, stream=None) -> None:
@@ -179,23 +202,22 @@ def dispatch_tokens(x, slots, rows, stream=None) -> None:
     rows (capacity, width) bf16 or fp32, slots (tokens, k) from route_tokens.
     Its gradient is combine_tokens of the rows' gradients without weights."""
     import torch
-    sh, sobj, dev = _on(stream)
+    sh, sobj, dev = _on(stream, x)
     code = _dtype_code(x, "x")
     xp, xs = _mat(x, "x", x.dtype, None, None, dev)
     T, D = x.shape
     k = slots.shape[-1]
     sp = _flat(slots, "slots", torch.int32, (T, k), dev)
     rp, rs = _mat(rows, "rows", x.dtype, None, D, dev)
-    _check(_fn("tide_dispatch_tokens")(code, xp, xs, T, D, sp, k, rp, rs, rows.shape[0], sh),
-           "tide_dispatch_tokens")
-    _record([x, slots, rows], sobj)
+    _run("tide_dispatch_tokens", (code, xp, xs, T, D, sp, k, rp, rs, rows.shape[0], sh), dev,
+         [x, slots, rows], sobj)
 
 
 def combine_tokens(rows, slots, out, weights=None, stream=None) -> None:
     """out[t] = sum over j of weights[t, j] * rows[slots[t, j]] in fp32, rounded
     once (tide_combine_tokens); weights (tokens, k) fp32, or None for ones."""
     import torch
-    sh, sobj, dev = _on(stream)
+    sh, sobj, dev = _on(stream, rows)
     code = _dtype_code(rows, "rows")
     rp, rs = _mat(rows, "rows", rows.dtype, None, None, dev)
     n, D = rows.shape
@@ -203,9 +225,8 @@ def combine_tokens(rows, slots, out, weights=None, stream=None) -> None:
     T, k = out.shape[0], slots.shape[-1]
     sp = _flat(slots, "slots", torch.int32, (T, k), dev)
     wp = 0 if weights is None else _flat(weights, "weights", torch.float32, (T, k), dev)
-    _check(_fn("tide_combine_tokens")(code, rp, rs, n, D, sp, wp, T, k, op, os_, sh),
-           "tide_combine_tokens")
-    _record([rows, slots, out, weights], sobj)
+    _run("tide_combine_tokens", (code, rp, rs, n, D, sp, wp, T, k, op, os_, sh), dev, [rows,
+         slots, out, weights], sobj)
 
 
 def combine_tokens_grad(dout, rows, slots, weights, drows, dweights, stream=None) -> None:
@@ -214,7 +235,7 @@ def combine_tokens_grad(dout, rows, slots, weights, drows, dweights, stream=None
     weights may be None (ones); with dweights None rows is not read and may be
     None."""
     import torch
-    sh, sobj, dev = _on(stream)
+    sh, sobj, dev = _on(stream, dout)
     code = _dtype_code(dout, "dout")
     dp, ds = _mat(dout, "dout", dout.dtype, None, None, dev)
     T, D = dout.shape
@@ -227,42 +248,38 @@ def combine_tokens_grad(dout, rows, slots, weights, drows, dweights, stream=None
     rp, rs = (0, D) if rows is None else _mat(rows, "rows", dout.dtype, n, D, dev)
     wp = 0 if weights is None else _flat(weights, "weights", torch.float32, (T, k), dev)
     qp = 0 if dweights is None else _flat(dweights, "dweights", torch.float32, (T, k), dev)
-    _check(_fn("tide_combine_tokens_grad")(code, dp, ds, rp, rs, n, D, sp, wp, T, k, gp, gs, qp,
-                                           sh), "tide_combine_tokens_grad")
-    _record([dout, rows, slots, weights, drows, dweights], sobj)
+    _run("tide_combine_tokens_grad", (code, dp, ds, rp, rs, n, D, sp, wp, T, k, gp, gs, qp,
+         sh), dev, [dout, rows, slots, weights, drows, dweights], sobj)
 
 
 def checkpoint_pack(x, saved, stream=None) -> None:
     """Packs x (rows, width), bf16 or fp32, into saved = (codes, scales): codes
     (rows, width) torch.float8_e4m3fn, scales (rows, ceil(width / 32))
     torch.float8_e8m0fnu (tide_checkpoint_pack)."""
-    sh, sobj, dev = _on(stream)
+    sh, sobj, dev = _on(stream, x)
     code = _dtype_code(x, "x")
     xp, xs = _mat(x, "x", x.dtype, None, None, dev)
     n, D = x.shape
     s, _, _ = _saved(saved, "saved", n, D, dev)
-    _check(_fn("tide_checkpoint_pack")(code, xp, xs, n, D, ctypes.byref(s), sh),
-           "tide_checkpoint_pack")
-    _record([x, *saved], sobj)
+    _run("tide_checkpoint_pack", (code, xp, xs, n, D, ctypes.byref(s), sh), dev, [x, *saved], sobj)
 
 
 def checkpoint_unpack(saved, out, stream=None) -> None:
     """The values a checkpoint stands for, in bf16 or fp32, exactly
     (tide_checkpoint_unpack)."""
-    sh, sobj, dev = _on(stream)
+    sh, sobj, dev = _on(stream, out)
     code = _dtype_code(out, "out")
     op, os_ = _mat(out, "out", out.dtype, None, None, dev)
     n, D = out.shape
     s, _, _ = _saved(saved, "saved", n, D, dev)
-    _check(_fn("tide_checkpoint_unpack")(code, ctypes.byref(s), n, D, op, os_, sh),
-           "tide_checkpoint_unpack")
-    _record([out, *saved], sobj)
+    _run("tide_checkpoint_unpack", (code, ctypes.byref(s), n, D, op, os_, sh), dev, [out,
+         *saved], sobj)
 
 
 def gated_silu(gate, up, out, gate_saved=None, up_saved=None, stream=None) -> None:
     """out = silu(gate) * up and, where they are given, the checkpoints of gate
     and up, in one pass (tide_gated_silu)."""
-    sh, sobj, dev = _on(stream)
+    sh, sobj, dev = _on(stream, gate)
     code = _dtype_code(gate, "gate")
     gp, gs = _mat(gate, "gate", gate.dtype, None, None, dev)
     n, D = gate.shape
@@ -270,15 +287,14 @@ def gated_silu(gate, up, out, gate_saved=None, up_saved=None, stream=None) -> No
     op, os_ = _mat(out, "out", gate.dtype, n, D, dev)
     a = None if gate_saved is None else _saved(gate_saved, "gate_saved", n, D, dev)[0]
     b = None if up_saved is None else _saved(up_saved, "up_saved", n, D, dev)[0]
-    _check(_fn("tide_gated_silu")(code, gp, gs, up_, us, n, D, op, os_, a, b, sh),
-           "tide_gated_silu")
-    _record([gate, up, out, *(gate_saved or ()), *(up_saved or ())], sobj)
+    _run("tide_gated_silu", (code, gp, gs, up_, us, n, D, op, os_, a, b, sh), dev, [gate, up,
+         out, *(gate_saved or ()), *(up_saved or ())], sobj)
 
 
 def gated_silu_grad(dout, gate_saved, up_saved, dgate, dup, out=None, stream=None) -> None:
     """Gradient of gated_silu at the checkpoints' values; out, when given,
     receives the activation recomputed from them (tide_gated_silu_grad)."""
-    sh, sobj, dev = _on(stream)
+    sh, sobj, dev = _on(stream, dout)
     code = _dtype_code(dout, "dout")
     dp, ds = _mat(dout, "dout", dout.dtype, None, None, dev)
     n, D = dout.shape
@@ -287,9 +303,8 @@ def gated_silu_grad(dout, gate_saved, up_saved, dgate, dup, out=None, stream=Non
     gp, gs = _mat(dgate, "dgate", dout.dtype, n, D, dev)
     up_, us = _mat(dup, "dup", dout.dtype, n, D, dev)
     op, os_ = (0, D) if out is None else _mat(out, "out", dout.dtype, n, D, dev)
-    _check(_fn("tide_gated_silu_grad")(code, dp, ds, a, b, n, D, gp, gs, up_, us, op, os_, sh),
-           "tide_gated_silu_grad")
-    _record([dout, *gate_saved, *up_saved, dgate, dup, out], sobj)
+    _run("tide_gated_silu_grad", (code, dp, ds, a, b, n, D, gp, gs, up_, us, op, os_, sh), dev,
+         [dout, *gate_saved, *up_saved, dgate, dup, out], sobj)
 
 
 def weight_grads_workspace_bytes(rows: int, out: int, in_: int, num_experts: int = 1) -> int:
@@ -313,7 +328,7 @@ def weight_grads_bf16(dy, x, grads: Union[object, Sequence[object], PointerTable
     accumulate: add to what grads holds. workspace: uint8 tensor of
     weight_grads_workspace_bytes(), by default allocated for the call."""
     import torch
-    sh, sobj, dev = _on(stream)
+    sh, sobj, dev = _on(stream, dy)
     dp, ds = _mat(dy, "dy", torch.bfloat16, None, None, dev)
     n, O = dy.shape
     keep = [dy, offsets, token_of_row]
@@ -348,7 +363,5 @@ def weight_grads_bf16(dy, x, grads: Union[object, Sequence[object], PointerTable
     need = weight_grads_workspace_bytes(n, O, I, E)
     wp, wn, w = _workspace(need, workspace, stream, dev)
     keep.append(w)
-    _check(_fn("tide_weight_grads_bf16")(dp, ds, n, O, xp, xs, s, xr, I, op, tp, E, arr,
-                                         1 if accumulate else 0, wp, wn, sh),
-           "tide_weight_grads_bf16")
-    _record(keep, sobj)
+    _run("tide_weight_grads_bf16", (dp, ds, n, O, xp, xs, s, xr, I, op, tp, E, arr, 1 if
+         accumulate else 0, wp, wn, sh), dev, keep, sobj)

@@ -14,6 +14,7 @@ using namespace tide;
 
 namespace {
 
+typedef uint32_t u32x2_a2 __attribute__((ext_vector_type(2), aligned(2)));
 constexpr int kBlock = 32;             // elements that share a scale
 constexpr int kMaxGrads = 256;         // gradient pointers in one launch's arguments
 constexpr int64_t kMaxGroups = 1 << 23;   // workgroups of a launch (2^32 work-items a dimension)
@@ -30,7 +31,8 @@ struct Args {
     const int32_t* tokens;             // row of x of each row of dy, or NULL: its own
     int64_t dy_stride, x_stride, codes_stride, scales_stride;
     int64_t n, x_rows, O, I;
-    int32_t accumulate, tiles_o, tiles_i, first, count;
+    float* partial;                    // with splits > 1: the sums of each split of each tile
+    int32_t accumulate, tiles_o, tiles_i, first, count, splits;
 };
 
 typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
@@ -46,12 +48,18 @@ constexpr int kDepth = 64;             // rows (tokens) of one stage
 // shifted into place. Elements: rows shorter than a load.
 enum Access { kBuffers, kVectors, kElements };
 constexpr uint32_t kBufferWord = 0x00020000;      // raw buffer, bounds checked in bytes
-constexpr uint32_t kOutside = 0xFFFFFFF0u;        // past every buffer: loads read 0
+constexpr uint32_t kOutside = 0x80000000u;        // past every buffer, also with a stage's offsets added: loads read 0
+constexpr int64_t kMostBytes = 0x7F000000;        // of a buffer
 
-// Position of 16-byte chunk c (8 elements) of row t in a staged row: rows t,
-// t + 1, t + 2, t + 3 place one column 64 bytes apart, so the four rows that a
-// transposing read takes at once come from different banks.
-__device__ __forceinline__ int chunk_at(int t, int c) { return c ^ ((t & 3) << 2); }
+// Position of 16-byte chunk c (8 elements) of row t in a staged row of kWidth
+// elements: rows t, t + 1, t + 2, t + 3 place one column 64 bytes apart (modulo
+// the 256 bytes of all banks), so the four rows that a transposing read takes
+// at once come from different banks.
+template <int kWidth>
+__device__ __forceinline__ int chunk_at(int t, int c) {
+    static_assert(kWidth == 64 || kWidth % 128 == 0, "bank pattern of a row");
+    return kWidth == 64 ? c ^ ((t & 2) << 1) : c ^ ((t & 3) << 2);
+}
 
 __device__ __forceinline__ u32x4 buffer16(__amdgpu_buffer_rsrc_t r, uint32_t at) {
     return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, (int)at, 0, 0));
@@ -91,19 +99,43 @@ __device__ __forceinline__ u32x4 shift_down(u32x4 v, int n) {
     return v;
 }
 
+// Four columns of a gradient from column i of row o on, as far as they are in it.
+__device__ __forceinline__ void store4(const Args& a, uint16_t* out, int64_t o, int64_t i, float v[4]) {
+    if (o >= a.O || i >= a.I) return;
+    out += o * a.I + i;
+    if (a.accumulate) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+            if (i + q < a.I) v[q] += lo_bf16(*gbl<uint16_t>(out + q));
+    }
+    const u32x2 p = {pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
+    if (i + 4 <= a.I) {
+        *gbl_mut<u32x2_a2>(out) = p;
+    } else {
+#pragma unroll
+        for (int q = 0; q < 3; ++q)
+            if (i + q < a.I) *gbl_mut<uint16_t>(out + q) = (uint16_t)(p[q / 2] >> (16 * (q & 1)));
+    }
+}
+
 // A kTile x kTile tile of one expert's gradient. Rows of dy and x are staged in
 // LDS as bf16, kDepth at a time, and read back transposed
 // (ds_read_b64_tr_b16), since the matrix instruction wants the summed index
 // (the row) inside a lane; products are 32x32x16 bf16 with fp32 sums. The 256
 // tile has 8 waves of 128 x 64 (128 sums a lane, two waves a SIMD: 4 waves of
 // 128 x 128 leave every wait exposed and reach 1060 instead of 1200 TFLOP/s on
-// 8192 x 8192 x 8192), the 128 tile 4 of 64 x 64.
+// 8192 x 8192 x 8192), the 128 tile 4 of 64 x 64. The 64 tile is for few
+// tiles: its 4 waves are teams of one, each with the whole tile, stages of its
+// own and a quarter of the rows, joined at the end through LDS; nothing but
+// that join waits on another wave.
 // kSaved: x is a checkpoint, decoded on its way into LDS (exact, and free:
 // both forms run at 1150 TFLOP/s).
-template <int kTile, int kThreads, bool kSaved, int kAccess>
+template <int kTile, bool kSaved, int kAccess>
 struct Tile {
     static constexpr int TO = kTile, TI = kTile;
-    static constexpr int WO = 2, WI = kThreads / 64 / WO;      // waves over the tile
+    static constexpr int kThreads = kTile == 256 ? 512 : kTile == 128 ? 256 : 64;      // of a team
+    static constexpr int kTeams = kTile == 64 ? 4 : 1;
+    static constexpr int WO = kTile == 64 ? 1 : 2, WI = kThreads / 64 / WO;    // waves over the tile
     static constexpr int FO = TO / WO / 32, FI = TI / WI / 32;  // 32 x 32 blocks of a wave
     static constexpr int kSteps = kDepth / 16;                 // matrix steps of a stage
     static constexpr int kParts = 2;                           // steps that move a stage's chunks
@@ -119,18 +151,25 @@ struct Tile {
     uint16_t* lds;
     int64_t lo, hi, o0, i0;
     int tid, lane, wave;
-    // what the next stage's chunks were loaded from and hold
-    u32x4 ro[NO], ri[NI];
-    uint32_t rs[kSaved ? NI : 1];
-    uint32_t none;                     // Vectors: bit j: ro[j], bit 16 + j: ri[j] is of no row
-    int32_t tok[NI];
+    // A stage on its way into LDS.
+    struct Moving {
+        u32x4 o[NO], i[NI];
+        uint32_t s[kSaved ? NI : 1];
+        uint32_t none;                 // Vectors: bit j: o[j], bit 16 + j: i[j] is of no row
+        int32_t tok[NI];               // the next one's rows of x
+    };
 
+    // A team of one wave needs no barrier: its LDS accesses run in order.
+    __device__ __forceinline__ void sync() {
+        if constexpr (kThreads == 64) __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        else __syncthreads();
+    }
     __device__ __forceinline__ uint16_t* stage_o(int b) { return lds + b * kStage; }
     __device__ __forceinline__ uint16_t* stage_i(int b) { return lds + b * kStage + kDepth * TO; }
 
     // Rows of x of the stage that starts at t0 (0 without token indices and
     // past the last row: no load uses those).
-    __device__ __forceinline__ void load_tokens(int64_t t0) {
+    __device__ __forceinline__ void load_tokens(Moving& m, int64_t t0) {
         const int64_t left = hi - t0 < 0 ? 0 : hi - t0;
         const int rows = left < kDepth ? (int)left : kDepth;
         const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(
@@ -138,25 +177,25 @@ struct Tile {
 #pragma unroll
         for (int j = 0; j < NI; ++j) {
             const int t = j * (kThreads / CI) + tid / CI;
-            tok[j] = __builtin_amdgcn_raw_buffer_load_b32(r, t * 4, 0, 0);
+            m.tok[j] = __builtin_amdgcn_raw_buffer_load_b32(r, t * 4, 0, 0);
         }
     }
 
     // Part kPart of kOf of the loads of the stage at t0.
     template <int kPart, int kOf>
-    __device__ __forceinline__ void load(int64_t t0) {
+    __device__ __forceinline__ void load(Moving& m, int64_t t0) {
         const int64_t left = hi - t0 < 0 ? 0 : hi - t0;
         const int rows = left < kDepth ? (int)left : kDepth;
         if constexpr (kAccess == kBuffers) {
             const __amdgpu_buffer_rsrc_t d = __builtin_amdgcn_make_buffer_rsrc(
                 (void*)(a.dy + t0 * a.dy_stride), (short)0, (int)(rows * (uint32_t)a.dy_stride * 2),
                 (int)kBufferWord);
+            // rows past the last lie past the buffer by themselves
+            const uint32_t at = (o0 + tid % CO * 8 < a.O ? 0 : kOutside) +
+                                (uint32_t)(tid / CO) * (uint32_t)a.dy_stride * 2 + (uint32_t)(o0 + tid % CO * 8) * 2;
 #pragma unroll
-            for (int j = kPart * NO / kOf; j < (kPart + 1) * NO / kOf; ++j) {
-                const int t = j * (kThreads / CO) + tid / CO, c = tid % CO;
-                const uint32_t out = o0 + c * 8 < a.O && t < rows ? 0 : kOutside;
-                ro[j] = buffer16(d, out | ((uint32_t)t * (uint32_t)a.dy_stride * 2 + (uint32_t)(o0 + c * 8) * 2));
-            }
+            for (int j = kPart * NO / kOf; j < (kPart + 1) * NO / kOf; ++j)
+                m.o[j] = buffer16(d, at + (uint32_t)(j * (kThreads / CO)) * (uint32_t)a.dy_stride * 2);
             // with token indices the whole of x is one buffer, without the stage's rows are
             const uint32_t stride = (uint32_t)(kSaved ? a.codes_stride : a.x_stride * 2);
             const uint8_t* base = kSaved ? a.codes : (const uint8_t*)a.x;
@@ -171,13 +210,13 @@ struct Tile {
 #pragma unroll
             for (int j = kPart * NI / kOf; j < (kPart + 1) * NI / kOf; ++j) {
                 const int t = j * (kThreads / CI) + tid / CI, c = tid % CI;
-                const uint32_t row = a.tokens ? (uint32_t)tok[j] : (uint32_t)t;
+                const uint32_t row = a.tokens ? (uint32_t)m.tok[j] : (uint32_t)t;
                 const int64_t col = i0 + c * (kSaved ? 16 : 8);
                 // or'ed in rather than selected, so that no branch guards the products
                 const uint32_t out = row < span && t < rows && col < a.I ? 0 : kOutside;
-                ri[j] = buffer16(x, out | (row * stride + (uint32_t)col * (kSaved ? 1 : 2)));
+                m.i[j] = buffer16(x, out | (row * stride + (uint32_t)col * (kSaved ? 1 : 2)));
                 if constexpr (kSaved)
-                    rs[j] = __builtin_amdgcn_raw_buffer_load_b8(
+                    m.s[j] = __builtin_amdgcn_raw_buffer_load_b8(
                         s, (int)(out | (row * (uint32_t)a.scales_stride + (uint32_t)col / kBlock)), 0, 0);
             }
         } else if constexpr (kAccess == kVectors) {
@@ -186,22 +225,22 @@ struct Tile {
 #pragma unroll
             for (int j = kPart * NO / kOf; j < (kPart + 1) * NO / kOf; ++j) {
                 const int t = j * (kThreads / CO) + tid / CO;
-                none = (none & ~(1u << j)) | (t < rows ? 0 : 1u << j);
-                ro[j] = *gbl<u32x4_a2>(a.dy + min(t0 + t, last) * a.dy_stride + co);
+                m.none = (m.none & ~(1u << j)) | (t < rows ? 0 : 1u << j);
+                m.o[j] = *gbl<u32x4_a2>(a.dy + min(t0 + t, last) * a.dy_stride + co);
             }
             const int64_t col = i0 + tid % CI * (kSaved ? 16 : 8), ci = min(col, a.I - (kSaved ? 16 : 8));
 #pragma unroll
             for (int j = kPart * NI / kOf; j < (kPart + 1) * NI / kOf; ++j) {
                 const int t = j * (kThreads / CI) + tid / CI;
-                int64_t row = a.tokens ? tok[j] : t0 + t;
+                int64_t row = a.tokens ? m.tok[j] : t0 + t;
                 const bool in = t < rows && (uint64_t)row < (uint64_t)a.x_rows;
-                none = (none & ~(0x10000u << j)) | (in ? 0 : 0x10000u << j);
+                m.none = (m.none & ~(0x10000u << j)) | (in ? 0 : 0x10000u << j);
                 row = in ? row : 0;
                 if constexpr (kSaved) {
-                    ri[j] = *gbl<u32x4_a1>(a.codes + row * a.codes_stride + ci);
-                    rs[j] = *gbl<uint8_t>(a.scales + row * a.scales_stride + min(col, a.I - 1) / kBlock);
+                    m.i[j] = *gbl<u32x4_a1>(a.codes + row * a.codes_stride + ci);
+                    m.s[j] = *gbl<uint8_t>(a.scales + row * a.scales_stride + min(col, a.I - 1) / kBlock);
                 } else {
-                    ri[j] = *gbl<u32x4_a2>(a.x + row * a.x_stride + ci);
+                    m.i[j] = *gbl<u32x4_a2>(a.x + row * a.x_stride + ci);
                 }
             }
         } else {
@@ -209,23 +248,23 @@ struct Tile {
             for (int j = kPart * NO / kOf; j < (kPart + 1) * NO / kOf; ++j) {
                 const int t = j * (kThreads / CO) + tid / CO, c = tid % CO;
                 const int64_t n = a.O - o0 - c * 8;
-                ro[j] = u32x4{};
+                m.o[j] = u32x4{};
                 if (n > 0 && t < rows)
-                    ro[j] = load8(a.dy + (t0 + t) * a.dy_stride + o0 + c * 8, (int)(n < 8 ? n : 8)).a;
+                    m.o[j] = load8(a.dy + (t0 + t) * a.dy_stride + o0 + c * 8, (int)(n < 8 ? n : 8)).a;
             }
 #pragma unroll
             for (int j = kPart * NI / kOf; j < (kPart + 1) * NI / kOf; ++j) {
                 const int t = j * (kThreads / CI) + tid / CI, c = tid % CI;
-                const int64_t row = t >= rows ? -1 : a.tokens ? tok[j] : t0 + t;
+                const int64_t row = t >= rows ? -1 : a.tokens ? m.tok[j] : t0 + t;
                 const int64_t col = i0 + c * (kSaved ? 16 : 8), n = a.I - col;
-                ri[j] = u32x4{};
-                if constexpr (kSaved) rs[j] = 0;
+                m.i[j] = u32x4{};
+                if constexpr (kSaved) m.s[j] = 0;
                 if (n > 0 && row >= 0 && row < a.x_rows) {
                     if constexpr (kSaved) {
-                        ri[j] = codes16(a.codes + row * a.codes_stride + col, (int)(n < 16 ? n : 16));
-                        rs[j] = *gbl<uint8_t>(a.scales + row * a.scales_stride + col / kBlock);
+                        m.i[j] = codes16(a.codes + row * a.codes_stride + col, (int)(n < 16 ? n : 16));
+                        m.s[j] = *gbl<uint8_t>(a.scales + row * a.scales_stride + col / kBlock);
                     } else {
-                        ri[j] = load8(a.x + row * a.x_stride + col, (int)(n < 8 ? n : 8)).a;
+                        m.i[j] = load8(a.x + row * a.x_stride + col, (int)(n < 8 ? n : 8)).a;
                     }
                 }
             }
@@ -240,33 +279,33 @@ struct Tile {
 
     // Part of the loaded chunks into LDS buffer b.
     template <int kPart, int kOf>
-    __device__ __forceinline__ void store(int b) {
+    __device__ __forceinline__ void store(Moving& m, int b) {
 #pragma unroll
         for (int j = kPart * NO / kOf; j < (kPart + 1) * NO / kOf; ++j) {
             const int t = j * (kThreads / CO) + tid / CO, c = tid % CO;
             if constexpr (kAccess == kVectors) {
-                if (o0 + TO > a.O) ro[j] = shift_down(ro[j], tail(o0 + c * 8, a.O - 8) * 2);
-                if (none >> j & 1) ro[j] = u32x4{};
+                if (o0 + TO > a.O) m.o[j] = shift_down(m.o[j], tail(o0 + c * 8, a.O - 8) * 2);
+                if (m.none >> j & 1) m.o[j] = u32x4{};
             }
-            *(u32x4*)(stage_o(b) + t * TO + chunk_at(t, c) * 8) = ro[j];
+            *(u32x4*)(stage_o(b) + t * TO + chunk_at<TO>(t, c) * 8) = m.o[j];
         }
 #pragma unroll
         for (int j = kPart * NI / kOf; j < (kPart + 1) * NI / kOf; ++j) {
             const int t = j * (kThreads / CI) + tid / CI, c = tid % CI;
             if constexpr (kAccess == kVectors) {
                 if (i0 + TI > a.I)
-                    ri[j] = kSaved ? shift_down(ri[j], tail(i0 + c * 16, a.I - 16))
-                                   : shift_down(ri[j], tail(i0 + c * 8, a.I - 8) * 2);
-                if (none >> (16 + j) & 1) ri[j] = u32x4{};
+                    m.i[j] = kSaved ? shift_down(m.i[j], tail(i0 + c * 16, a.I - 16))
+                                   : shift_down(m.i[j], tail(i0 + c * 8, a.I - 8) * 2);
+                if (m.none >> (16 + j) & 1) m.i[j] = u32x4{};
             }
             if constexpr (kSaved) {
                 u32x4 p, q;
-                decode16(ri[j], __uint_as_float(rs[j] << 23), p, q);
-                u32x4* d = (u32x4*)(stage_i(b) + t * TI + chunk_at(t, 2 * c) * 8);
+                decode16(m.i[j], __uint_as_float(m.s[j] << 23), p, q);
+                u32x4* d = (u32x4*)(stage_i(b) + t * TI + chunk_at<TI>(t, 2 * c) * 8);
                 d[0] = p;
                 d[1] = q;
             } else {
-                *(u32x4*)(stage_i(b) + t * TI + chunk_at(t, c) * 8) = ri[j];
+                *(u32x4*)(stage_i(b) + t * TI + chunk_at<TI>(t, c) * 8) = m.i[j];
             }
         }
     }
@@ -274,20 +313,21 @@ struct Tile {
     // A 32-column block of 16 staged rows as a matrix operand: lane l holds
     // column l % 32, rows (l / 32) * 8 + 0 .. 7. Each transposing read gives a
     // lane four rows of one column out of the 4 x 16 blocks that 16 lanes name.
-    __device__ __forceinline__ bf16x8 operand(const uint16_t* rows, int width, int step, int col) {
+    static_assert(TO == TI, "one width");
+    __device__ __forceinline__ bf16x8 operand(const uint16_t* rows, int step, int col) {
         const int t = step * 16 + (lane >> 5) * 8 + ((lane & 15) >> 2);
         const int c = (col >> 3) + ((lane >> 4) & 1) * 2 + ((lane & 3) >> 1);
-        const uint16_t* p = rows + t * width + chunk_at(t, c) * 8 + (lane & 1) * 4;
+        const uint16_t* p = rows + t * TI + chunk_at<TI>(t, c) * 8 + (lane & 1) * 4;
         const s16x4 u = __builtin_amdgcn_ds_read_tr16_b64_v4i16((TIDE_LDS s16x4*)p);
-        const s16x4 v = __builtin_amdgcn_ds_read_tr16_b64_v4i16((TIDE_LDS s16x4*)(p + 4 * width));
+        const s16x4 v = __builtin_amdgcn_ds_read_tr16_b64_v4i16((TIDE_LDS s16x4*)(p + 4 * TI));
         const bf16x4 x = __builtin_bit_cast(bf16x4, u), y = __builtin_bit_cast(bf16x4, v);
         return __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7);
     }
     __device__ __forceinline__ void operands(int b, int step, bf16x8 (&fo)[FO], bf16x8 (&fi)[FI]) {
 #pragma unroll
-        for (int f = 0; f < FO; ++f) fo[f] = operand(stage_o(b), TO, step, (wave / WI) * (TO / WO) + f * 32);
+        for (int f = 0; f < FO; ++f) fo[f] = operand(stage_o(b), step, (wave / WI) * (TO / WO) + f * 32);
 #pragma unroll
-        for (int f = 0; f < FI; ++f) fi[f] = operand(stage_i(b), TI, step, (wave % WI) * (TI / WI) + f * 32);
+        for (int f = 0; f < FI; ++f) fi[f] = operand(stage_i(b), step, (wave % WI) * (TI / WI) + f * 32);
     }
 
     // Asks the scheduler to spread a step's LDS and memory instructions over
@@ -304,7 +344,7 @@ struct Tile {
             constexpr int l = (kAt + 1) * L / M - kAt * L / M;
             __builtin_amdgcn_sched_group_barrier(kMatrix, 1, 0);
             if constexpr (r > 0) __builtin_amdgcn_sched_group_barrier(kRead, r, 0);
-            if constexpr (moves) __builtin_amdgcn_sched_group_barrier(kVector, 3, 0);
+            if constexpr (moves) __builtin_amdgcn_sched_group_barrier(kVector, 1, 0);
             if constexpr (w > 0) __builtin_amdgcn_sched_group_barrier(kWrite, w, 0);
             if constexpr (l > 0) __builtin_amdgcn_sched_group_barrier(kLoad, l, 0);
             interleave<kStep, kAt + 1>();
@@ -312,20 +352,20 @@ struct Tile {
     }
 
     template <int kStep>
-    __device__ __forceinline__ void step(int64_t t0, int b, bf16x8 (&fo)[2][FO], bf16x8 (&fi)[2][FI],
+    __device__ __forceinline__ void step(int64_t t0, int b, Moving& m, bf16x8 (&fo)[2][FO], bf16x8 (&fi)[2][FI],
                                          f32x16 (&acc)[FO][FI]) {
         constexpr int now = kStep & 1, next = now ^ 1;
         if constexpr (kStep < kSteps - 1) {
             operands(b, kStep + 1, fo[next], fi[next]);
         } else {
-            __syncthreads();
+            sync();
             operands(b ^ 1, 0, fo[next], fi[next]);
         }
         if constexpr (kStep < kParts) {
-            store<kStep, kParts>(b ^ 1);
-            load<kStep, kParts>(t0 + 2 * kDepth);
+            store<kStep, kParts>(m, b ^ 1);
+            load<kStep, kParts>(m, t0 + 2 * kDepth);
         }
-        if constexpr (kStep == kParts) load_tokens(t0 + 3 * kDepth);
+        if constexpr (kStep == kParts) load_tokens(m, t0 + 3 * kDepth);
 #pragma unroll
         for (int x = 0; x < FO; ++x)
 #pragma unroll
@@ -335,44 +375,96 @@ struct Tile {
     }
 
     // The sum over rows [lo, hi). A step's operands are read while the step
-    // before is multiplied; a stage is loaded two ahead and written to LDS
-    // one ahead, in the shadow of the matrix instructions; one barrier a
-    // stage, before its last step, by when nothing of it is left to read.
+    // before is multiplied; a stage is loaded two stages before it is multiplied
+    // and written to LDS one before, in the shadow of the matrix instructions;
+    // one barrier a stage, before its last step, by when nothing of it is left
+    // to read.
     __device__ __forceinline__ void sum(f32x16 (&acc)[FO][FI]) {
         if (lo >= hi) return;
-        load_tokens(lo);
-        load<0, 1>(lo);
-        load_tokens(lo + kDepth);
-        store<0, 1>(0);
-        load<0, 1>(lo + kDepth);
-        load_tokens(lo + 2 * kDepth);
-        __syncthreads();
+        Moving first, m;
+        load_tokens(first, lo);
+        load_tokens(m, lo + kDepth);
+        load<0, 1>(first, lo);
+        load<0, 1>(m, lo + kDepth);
+        load_tokens(m, lo + 2 * kDepth);
+        store<0, 1>(first, 0);
+        sync();
         bf16x8 fo[2][FO], fi[2][FI];
         operands(0, 0, fo[0], fi[0]);
-        int b = 0;
-        for (int64_t t0 = lo; t0 < hi; t0 += kDepth, b ^= 1) {
-            step<0>(t0, b, fo, fi, acc);
-            step<1>(t0, b, fo, fi, acc);
-            step<2>(t0, b, fo, fi, acc);
-            step<3>(t0, b, fo, fi, acc);
+        // two stages a turn, so that the buffer is known when compiling (4% faster)
+        for (int64_t t0 = lo; t0 < hi; t0 += 2 * kDepth) {
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                const int64_t t = t0 + b * kDepth;
+                if (b > 0 && t >= hi) break;
+                step<0>(t, b, m, fo, fi, acc);
+                step<1>(t, b, m, fo, fi, acc);
+                step<2>(t, b, m, fo, fi, acc);
+                step<3>(t, b, m, fo, fi, acc);
+            }
         }
-        __syncthreads();
+        sync();
     }
 
     // acc[x][y]: lane l holds out row (o) l % 32 of the block, and for each
-    // group of four registers four consecutive in columns (i). The tile goes
-    // through LDS so that whole rows are stored; chunks are placed by row so
-    // that neither side meets a bank twice.
+    // group of four registers four consecutive in columns (i).
+    static __device__ __forceinline__ int row_of(int wave, int lane, int x) {
+        return wave / WI * (TO / WO) + x * 32 + (lane & 31);
+    }
+    static __device__ __forceinline__ int column_of(int wave, int lane, int y, int r) {
+        return wave % WI * (TI / WI) + y * 32 + r * 8 + (lane >> 5) * 4;
+    }
+
+    // The 64 tile: each team's sums go to LDS, four columns a 16-byte chunk,
+    // placed by row for the banks, and are added in the teams' order; the whole
+    // workgroup stores them, or keeps them in fp32 for join_splits.
+    __device__ __forceinline__ void finish_teams(f32x16 (&acc)[FO][FI], uint16_t* all, int team, uint16_t* out,
+                                                 float* partial) {
+        constexpr int C = TI / 4;
+        __syncthreads();
+        float* mine = (float*)all + team * TO * TI;
+#pragma unroll
+        for (int x = 0; x < FO; ++x)
+#pragma unroll
+            for (int y = 0; y < FI; ++y)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int o = row_of(wave, lane, x), i = column_of(wave, lane, y, r);
+                    u32x4 v;
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) v[q] = __float_as_uint(acc[x][y][r * 4 + q]);
+                    *(u32x4*)(mine + o * TI + ((i >> 2) ^ (o & (C - 1))) * 4) = v;
+                }
+        __syncthreads();
+        for (int j = threadIdx.x; j < TO * C; j += kThreads * kTeams) {
+            const int o = j / C, c = j % C;
+            float v[4] = {};
+            for (int k = 0; k < kTeams; ++k) {
+                const u32x4 w = *(const u32x4*)((const float*)all + k * TO * TI + o * TI + (c ^ (o & (C - 1))) * 4);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) v[q] += __uint_as_float(w[q]);
+            }
+            if (partial) {
+                *gbl_mut<u32x4>(partial + j * 4) = u32x4{__float_as_uint(v[0]), __float_as_uint(v[1]),
+                                                         __float_as_uint(v[2]), __float_as_uint(v[3])};
+            } else {
+                store4(a, out, o0 + o, i0 + c * 4, v);
+            }
+        }
+    }
+
+    // The tile goes through LDS so that whole rows are stored; chunks are
+    // placed by row so that neither side meets a bank twice.
     __device__ __forceinline__ void finish(f32x16 (&acc)[FO][FI], uint16_t* out) {
         constexpr int C = TI / 8;
 #pragma unroll
         for (int x = 0; x < FO; ++x) {
-            const int o = (wave / WI) * (TO / WO) + x * 32 + (lane & 31);
+            const int o = row_of(wave, lane, x);
 #pragma unroll
             for (int y = 0; y < FI; ++y) {
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
-                    const int i = (wave % WI) * (TI / WI) + y * 32 + r * 8 + (lane >> 5) * 4;
+                    const int i = column_of(wave, lane, y, r);
                     float v[4];
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
@@ -403,17 +495,17 @@ struct Tile {
     }
 };
 
-template <int kTile, int kThreads, bool kSaved, int kAccess>
-__global__ __launch_bounds__(kThreads, 2) void weight_grads(Args a, GradPtrs g) {
-    using K = Tile<kTile, kThreads, kSaved, kAccess>;
-    __shared__ __attribute__((aligned(1024))) uint16_t lds[K::kLds / 2];
+template <int kTile, bool kSaved, int kAccess>
+__global__ __launch_bounds__(kTile == 256 ? 512 : 256, kTile == 64 ? 1 : 2) void weight_grads(Args a, GradPtrs g) {
+    using K = Tile<kTile, kSaved, kAccess>;
+    __shared__ __attribute__((aligned(1024))) uint16_t lds[K::kTeams * K::kLds / 2];
     // Workgroups go round robin over the XCDs: each XCD gets one run of tiles,
     // so that tiles that share rows share an L2.
     const int per = gridDim.x / 8, at = (int)(blockIdx.x % 8) * per + (int)(blockIdx.x / 8);
     const int tiles = a.tiles_o * a.tiles_i;
-    if (at >= a.count * tiles) return;
-    const int e = at / tiles;
-    int tile = at - e * tiles;
+    if (at >= a.count * a.splits * tiles) return;
+    const int part = at / tiles, e = part / a.splits, split = part - e * a.splits;
+    int tile = at - part * tiles;
     // within an expert, bands of 8 tile rows, walked column by column
     const int band = tile / (8 * a.tiles_i), high = min(8, a.tiles_o - band * 8);
     tile -= band * 8 * a.tiles_i;
@@ -425,26 +517,64 @@ __global__ __launch_bounds__(kThreads, 2) void weight_grads(Args a, GradPtrs g) 
         lo = lo < 0 ? 0 : lo > a.n ? a.n : lo;
         hi = hi < lo ? lo : hi > a.n ? a.n : hi;
     }
-    K k{a, lds, lo, hi, (int64_t)to * kTile, (int64_t)ti * kTile, (int)threadIdx.x, (int)threadIdx.x & 63,
-        (int)threadIdx.x >> 6, {}, {}, {}, 0, {}};
+    const int team = kTile == 64 ? __builtin_amdgcn_readfirstlane(threadIdx.x / K::kThreads) : 0;
+    if (kTile == 64) {                 // whole stages to each team of each split
+        const int64_t parts = a.splits * K::kTeams, stages = (hi - lo + kDepth - 1) / kDepth;
+        const int64_t each = (stages + parts - 1) / parts * kDepth;
+        lo = min(lo + (split * K::kTeams + team) * each, hi);
+        hi = min(lo + each, hi);
+    }
+    const int tid = threadIdx.x % K::kThreads;
+    K k{a, lds + team * (K::kLds / 2), lo, hi, (int64_t)to * kTile, (int64_t)ti * kTile, tid, tid & 63, tid >> 6};
     f32x16 acc[K::FO][K::FI] = {};
     k.sum(acc);
-    k.finish(acc, g.p[e]);
+    if constexpr (kTile == 64)
+        k.finish_teams(acc, lds, team, g.p[e],
+                       a.splits > 1 ? a.partial + ((int64_t)part * tiles + to * a.tiles_i + ti) * (kTile * kTile)
+                                    : nullptr);
+    else
+        k.finish(acc, g.p[e]);
 }
 
-template <int kTile, int kThreads>
-hipError_t launch_tiles(Args a, const GradPtrs& g, Access how, hipStream_t stream) {
-    const int64_t groups = (int64_t)a.count * a.tiles_o * a.tiles_i;
-    const dim3 grid((uint32_t)((groups + 7) / 8 * 8));
-    if (a.codes) {
-        if (how == kBuffers) weight_grads<kTile, kThreads, true, kBuffers><<<grid, dim3(kThreads), 0, stream>>>(a, g);
-        else if (how == kVectors) weight_grads<kTile, kThreads, true, kVectors><<<grid, dim3(kThreads), 0, stream>>>(a, g);
-        else if constexpr (kTile == 128) weight_grads<kTile, kThreads, true, kElements><<<grid, dim3(kThreads), 0, stream>>>(a, g);
-    } else {
-        if (how == kBuffers) weight_grads<kTile, kThreads, false, kBuffers><<<grid, dim3(kThreads), 0, stream>>>(a, g);
-        else if (how == kVectors) weight_grads<kTile, kThreads, false, kVectors><<<grid, dim3(kThreads), 0, stream>>>(a, g);
-        else if constexpr (kTile == 128) weight_grads<kTile, kThreads, false, kElements><<<grid, dim3(kThreads), 0, stream>>>(a, g);
+// Joins the splits of 64 tiles, in order: four columns a lane.
+__global__ __launch_bounds__(256) void join_splits(Args a, GradPtrs g) {
+    constexpr int kTile = 64, kPer = kTile * kTile / 4 / 256;      // workgroups a tile
+    const int tiles = a.tiles_o * a.tiles_i;
+    const int j = blockIdx.x % kPer * 256 + threadIdx.x, tile = blockIdx.x / kPer % tiles;
+    const int e = blockIdx.x / kPer / tiles;
+    const int64_t apart = (int64_t)tiles * (kTile * kTile);
+    const float* p = a.partial + (int64_t)e * a.splits * apart + (int64_t)tile * (kTile * kTile) + j * 4;
+    float v[4] = {};
+    for (int s = 0; s < a.splits; s += 8) {
+        u32x4 w[8];
+#pragma unroll
+        for (int c = 0; c < 8; ++c) w[c] = *gbl<u32x4>(p + min(s + c, a.splits - 1) * apart);
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) v[q] += s + c < a.splits ? __uint_as_float(w[c][q]) : 0.0f;
     }
+    store4(a, g.p[e], (int64_t)(tile / a.tiles_i) * kTile + j / (kTile / 4),
+           (int64_t)(tile % a.tiles_i) * kTile + j % (kTile / 4) * 4, v);
+}
+
+template <int kTile>
+hipError_t launch_tiles(const Args& a, const GradPtrs& g, Access how, hipStream_t stream) {
+    const int64_t groups = (int64_t)a.count * a.splits * a.tiles_o * a.tiles_i;
+    const dim3 grid((uint32_t)((groups + 7) / 8 * 8)), threads(kTile == 256 ? 512 : 256);
+    if (a.codes) {
+        if (how == kBuffers) weight_grads<kTile, true, kBuffers><<<grid, threads, 0, stream>>>(a, g);
+        else if (how == kVectors) weight_grads<kTile, true, kVectors><<<grid, threads, 0, stream>>>(a, g);
+        else if constexpr (kTile == 64) weight_grads<kTile, true, kElements><<<grid, threads, 0, stream>>>(a, g);
+    } else {
+        if (how == kBuffers) weight_grads<kTile, false, kBuffers><<<grid, threads, 0, stream>>>(a, g);
+        else if (how == kVectors) weight_grads<kTile, false, kVectors><<<grid, threads, 0, stream>>>(a, g);
+        else if constexpr (kTile == 64) weight_grads<kTile, false, kElements><<<grid, threads, 0, stream>>>(a, g);
+    }
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess || a.splits == 1) return e;
+    const int64_t blocks = (int64_t)a.count * a.tiles_o * a.tiles_i * (64 * 64 / 4 / 256);
+    join_splits<<<dim3((uint32_t)blocks), dim3(256), 0, stream>>>(a, g);
     return hipGetLastError();
 }
 
@@ -454,7 +584,7 @@ Access how_to_read(const Args& a) {
     const int64_t step = a.codes ? 16 : 8, xs = a.codes ? a.codes_stride : a.x_stride * 2;
     const uintptr_t base = a.codes ? (uintptr_t)a.codes : (uintptr_t)a.x;
     const int64_t rows = a.tokens ? a.x_rows : kDepth;
-    const int64_t lim = (int64_t)0xF0000000;
+    const int64_t lim = kMostBytes;
     if (a.O < 8 || a.I < step) return kElements;
     if (a.O % 8 == 0 && a.I % step == 0 && ((uintptr_t)a.dy & 15) == 0 && a.dy_stride % 8 == 0 &&
         (base & 15) == 0 && xs % 16 == 0 && a.dy_stride <= lim / 2 / kDepth && (rows == 0 || xs <= lim / rows) &&
@@ -469,14 +599,49 @@ Access how_to_read(const Args& a) {
         if (s_ != TIDE_OK) return s_;         \
     } while (0)
 
-// Tile edge: 256 reuses each staged element 256 times and feeds the matrix
-// units best (1150 against 870 TFLOP/s on 28672 x 8192 from 4096 rows), once
-// there are tiles for most of the 256 CUs; with 128 tiles of 256 (1024 x 8192)
-// 512 of 128 are faster (178 against 193 us), with 192 (8 experts of 1984 x
-// 704) they are not (36 against 33 us).
-int choose_tile(const Args& a, int32_t experts) {
-    const int64_t big = ((a.O + 255) / 256) * ((a.I + 255) / 256);
-    return big > 160 / experts ? 256 : 128;
+// Tile edge and splits. A large tile reuses each staged element more (1180,
+// 870 and 410 TFLOP/s on long sums, edges 256, 128 and 64), a small one leaves
+// fewer CUs idle and, with its teams, waits less. The costs below, in us, are
+// fits to measured times: a round of workgroups has a part that does not
+// depend on the rows, and each stage of 64 rows adds to it. Both sides where
+// the choice turns: 1024 x 8192 from 8192 rows 193 us with 128 tiles of 256,
+// 180 with 512 of 128; 8 experts of 1984 x 704 33 us (192 of 256) and 40 (768
+// of 128); 512 x 2048 from 1000 rows 18.4 us (64 of 128) and 13.5 (256 of 64);
+// 2048 x 2048 from 64 rows 15 us (256 of 128) and 22 (1024 of 64).
+// Splits: where even tiles of 64 leave CUs idle, the rows of each are divided
+// among several workgroups, whose fp32 sums a second kernel adds in order:
+// 128 x 2048 from 8192 rows 37 us with one, 20 with four.
+struct Plan {
+    int64_t tiles_o, tiles_i;
+    int tile, splits;
+};
+Plan plan_tiles(int64_t n, int64_t O, int64_t I, int32_t experts) {
+    const int64_t cap = 1 << 20, stages = (n / experts + kDepth - 1) / kDepth;
+    const auto tiles = [&](int64_t edge) {
+        return std::min((O + edge - 1) / edge, cap) * std::min((I + edge - 1) / edge, cap) * experts;
+    };
+    const auto rounds = [](int64_t groups, int64_t at_once) { return (double)((groups + at_once - 1) / at_once); };
+    const int64_t small = tiles(64);
+    Plan p{0, 0, 64, 1};
+    double best = 0;
+    for (int64_t s = 1; s == 1 || (s * small <= 256 && s * 4 <= stages); s *= 2) {
+        const double us = rounds(s * small, 256) * (6 + 0.75 * (double)((stages + 4 * s - 1) / (4 * s))) +
+                          (s > 1 ? 5 + 0.01 * (double)(s * small) : 0);
+        if (s == 1 || us < best) {
+            best = us;
+            p.splits = (int)s;
+        }
+    }
+    if (O >= 16 && I >= 16) {
+        const int64_t mid = tiles(128), big = tiles(256);
+        const double mid_us = mid <= 256 ? 6 + 0.75 * stages : rounds(mid, 512) * (7 + 1.35 * stages);
+        const double big_us = rounds(big, 256) * (8 + 1.6 * stages);
+        if (mid_us < best) p.tile = 128, p.splits = 1, best = mid_us;
+        if (big_us < best) p.tile = 256, p.splits = 1;
+    }
+    p.tiles_o = (O + p.tile - 1) / p.tile;
+    p.tiles_i = (I + p.tile - 1) / p.tile;
+    return p;
 }
 
 tide_status check_sizes(int64_t n, int64_t O, int64_t I, int32_t experts) {
@@ -498,7 +663,8 @@ tide_status tide_weight_grads_workspace(int64_t rows, int64_t out, int64_t in, i
                                         int64_t* bytes) {
     if (!bytes) return fail(TIDE_ERR_INVALID_ARG, "bytes is NULL");
     TIDE_TRY(check_sizes(rows, out, in, experts));
-    *bytes = 0;
+    const Plan p = plan_tiles(rows, out, in, experts);
+    *bytes = p.splits > 1 ? p.splits * experts * p.tiles_o * p.tiles_i * p.tile * p.tile * 4 : 0;
     return TIDE_OK;
 }
 
@@ -523,7 +689,7 @@ tide_status tide_weight_grads_bf16(const uint16_t* dy, int64_t dy_stride, int64_
                         (long long)rows);
         if ((x != nullptr) == (saved != nullptr) && rows > 0 && in > 0)
             return fail(TIDE_ERR_INVALID_ARG, "need either x or saved");
-        Mat rd[5], wr;
+        Mat rd[5], wr, ws;
         TIDE_TRY(matrix("dy", dy, rows, out, dy_stride, 2, &rd[0]));
         if (saved) {
             TIDE_TRY(matrix("saved", saved->codes, x_rows, in, saved->codes_stride, 1, &rd[1]));
@@ -536,6 +702,9 @@ tide_status tide_weight_grads_bf16(const uint16_t* dy, int64_t dy_stride, int64_
         TIDE_TRY(matrix("offsets", offsets, offsets ? 1 : 0, (int64_t)experts + 1,
                         (int64_t)experts + 1, 4, &rd[3]));
         TIDE_TRY(matrix("token_of_row", token_of_row, token_of_row ? 1 : 0, rows, rows, 4, &rd[4]));
+        TIDE_TRY(matrix("workspace", workspace, 1, need / 4, need / 4, 4, &ws));
+        if (ws.base & 15) return fail(TIDE_ERR_ALIGNMENT, "workspace is not 16-byte aligned");
+        TIDE_TRY(no_overlap(&ws, 1, rd, 5));
         if (out == 0 || in == 0) return TIDE_OK;
         if (!grads) return fail(TIDE_ERR_INVALID_ARG, "grads is NULL");
         std::vector<uintptr_t> at(experts);
@@ -544,6 +713,7 @@ tide_status tide_weight_grads_bf16(const uint16_t* dy, int64_t dy_stride, int64_
             snprintf(name, sizeof name, "grads[%d]", e);
             TIDE_TRY(matrix(name, grads[e], 1, out * in, out * in, 2, &wr));
             TIDE_TRY(no_overlap(&wr, 1, rd, 5));
+            TIDE_TRY(no_overlap(&wr, 1, &ws, 1));
             at[e] = wr.base;
         }
         if (!std::is_sorted(at.begin(), at.end())) std::sort(at.begin(), at.end());
@@ -575,21 +745,24 @@ tide_status tide_weight_grads_bf16(const uint16_t* dy, int64_t dy_stride, int64_
         a.accumulate = accumulate ? 1 : 0;
         if (x_rows == 0) a.n = 0;              // no row of x to add
         const Access how = how_to_read(a);
-        const int tile = how == kElements ? 128 : choose_tile(a, experts);
-        const int64_t to = (out + tile - 1) / tile, ti = (in + tile - 1) / tile;
-        if (to > kMaxGroups / ti)
+        const Plan p = plan_tiles(rows, out, in, experts);
+        if (p.tiles_o > kMaxGroups / p.tiles_i)
             return fail(TIDE_ERR_UNSUPPORTED, "gradients of %lld x %lld", (long long)out, (long long)in);
-        a.tiles_o = (int32_t)to;
-        a.tiles_i = (int32_t)ti;
-        const int32_t most = (int32_t)std::min<int64_t>(kMaxGrads, kMaxGroups / (to * ti));
+        const int64_t tiles = p.tiles_o * p.tiles_i;
+        a.tiles_o = (int32_t)p.tiles_o;
+        a.tiles_i = (int32_t)p.tiles_i;
+        a.splits = p.splits;
+        const int32_t most = (int32_t)std::min<int64_t>(kMaxGrads, kMaxGroups / (tiles * p.splits));
         for (int32_t e0 = 0; e0 < experts; e0 += most) {
             const int32_t ne = std::min(experts - e0, most);
             GradPtrs g{};
             for (int32_t e = 0; e < ne; ++e) g.p[e] = grads[e0 + e];
             a.first = e0;
             a.count = ne;
-            const hipError_t launched = tile == 256 ? launch_tiles<256, 512>(a, g, how, stream)
-                                                    : launch_tiles<128, 256>(a, g, how, stream);
+            a.partial = (float*)workspace + (int64_t)e0 * p.splits * tiles * p.tile * p.tile;
+            const hipError_t launched = p.tile == 256   ? launch_tiles<256>(a, g, how, stream)
+                                        : p.tile == 128 ? launch_tiles<128>(a, g, how, stream)
+                                                        : launch_tiles<64>(a, g, how, stream);
             if (launched != hipSuccess) return hip_fail(launched, "weight_grads");
         }
         return TIDE_OK;

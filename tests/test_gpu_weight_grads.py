@@ -123,6 +123,33 @@ def test_many_experts_in_large_tiles(tide, T, k, E, O, I, pad, saved):
 
 
 @pytest.mark.parametrize("saved", [False, True])
+@pytest.mark.parametrize("pad", [0, 3])
+@pytest.mark.parametrize("n,O,I", [(2100, 128, 512), (5000, 96, 97), (1500, 61, 64), (9001, 64, 40), (700, 8, 16),
+                                   (6000, 128, 512)])
+def test_few_tiles_and_many_rows(tide, n, O, I, pad, saved):
+    """Rows divided among waves and, the longest, among workgroups."""
+    say("weight_grads", n, O, I, pad, saved)
+    dy, x = ref.normal((n, O), torch.bfloat16, seed=n), ref.normal((n, I), torch.bfloat16, seed=I)
+    check(tide, dy, x, saved, None, None, pad)
+    check(tide, dy, x, saved, None, None, pad, old=ref.normal((1, O, I), torch.bfloat16, seed=3, scale=10.0))
+    half = n // 3
+    check(tide, dy, x, saved, torch.tensor([5, 5, half, n - 1]), None, pad)
+
+
+def test_workspace_of_the_caller(tide):
+    n, O, I = 3000, 128, 256
+    dy, x = ref.normal((n, O), torch.bfloat16, seed=1).to(dev()), ref.normal((n, I), torch.bfloat16, seed=2).to(dev())
+    need = tide.weight_grads_workspace_bytes(n, O, I)
+    ws = torch.full((need,), 0xFF, dtype=torch.uint8, device=dev())       # whatever it holds
+    a, b = (torch.empty(1, O, I, dtype=torch.bfloat16, device=dev()) for _ in range(2))
+    tide.weight_grads_bf16(dy, x, a, workspace=ws)
+    tide.weight_grads_bf16(dy, x, b)
+    assert torch.equal(a, b)
+    with pytest.raises(tide.TideError, match="INVALID_ARG"):
+        tide.weight_grads_bf16(dy, x, a, workspace=ws[: need - 1])
+
+
+@pytest.mark.parametrize("saved", [False, True])
 def test_segments_without_a_sort(tide, saved):
     """Offsets with empty experts, rows in no expert at both ends, x by row."""
     off = torch.tensor([3, 3, 20, 20, 53, 54, 54, 90])

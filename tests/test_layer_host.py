@@ -36,6 +36,9 @@ def test_workspaces(tide):
     many = tide.route_workspace_bytes(1 << 20, 8, 512)
     assert 0 < many <= 1 << 20
     assert tide.weight_grads_workspace_bytes(0, 64, 64) == 0
+    assert tide.weight_grads_workspace_bytes(4096, 28672, 8192) == 0
+    split = tide.weight_grads_workspace_bytes(8192, 128, 2048)         # few tiles, a long sum
+    assert split >= 2 * 128 * 2048 * 4 and split % (128 * 2048 * 4) == 0
     for bad in [(-1, 1, 1), (1, 0, 1), (1, 1, 0)]:
         with pytest.raises(tide.TideError, match="INVALID_ARG"):
             tide.route_workspace_bytes(*bad)
