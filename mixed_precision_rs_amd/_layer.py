@@ -327,6 +327,7 @@ def weight_grads_bf16(dy, x, grads: Union[object, Sequence[object], PointerTable
     route_tokens; without offsets there is one expert, with every row.
     accumulate: add to what grads holds. workspace: uint8 tensor of
     weight_grads_workspace_bytes(), by default allocated for the call."""
+    import numpy as np
     import torch
     sh, sobj, dev = _on(stream, dy)
     dp, ds = _mat(dy, "dy", torch.bfloat16, None, None, dev)
@@ -355,8 +356,8 @@ def weight_grads_bf16(dy, x, grads: Union[object, Sequence[object], PointerTable
     else:
         E = grads.shape[0] if grads.dim() == 3 else -1
         base = _flat(grads, "grads", torch.bfloat16, (E, O, I), dev)
-        step = O * I * 2
-        arr = (ctypes.c_void_p * max(E, 1))(*[base + e * step for e in range(E)])
+        table = np.arange(E, dtype=np.uint64) * (O * I * 2) + np.uint64(base)
+        arr = table.ctypes.data
         keep.append(grads)
     op = 0 if offsets is None else _flat(offsets, "offsets", torch.int32, (E + 1,), dev)
     tp = 0 if token_of_row is None else _flat(token_of_row, "token_of_row", torch.int32, (n,), dev)

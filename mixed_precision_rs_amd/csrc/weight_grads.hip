@@ -334,7 +334,7 @@ struct Tile {
     // its matrix instructions, each of which leaves 32 cycles to issue others.
     template <int kStep, int kAt = 0>
     __device__ __forceinline__ void interleave() {
-        constexpr int kMatrix = 0x8, kRead = 0x100, kWrite = 0x200, kLoad = 0x20, kVector = 0x2;
+        constexpr int kMatrix = 0x8, kRead = 0x100, kWrite = 0x200, kLoad = 0x20;
         constexpr int M = FO * FI, R = 2 * (FO + FI);
         constexpr bool moves = kStep < kParts;
         constexpr int W = moves ? (NO + (kSaved ? 2 : 1) * NI) / kParts : 0;
@@ -344,7 +344,6 @@ struct Tile {
             constexpr int l = (kAt + 1) * L / M - kAt * L / M;
             __builtin_amdgcn_sched_group_barrier(kMatrix, 1, 0);
             if constexpr (r > 0) __builtin_amdgcn_sched_group_barrier(kRead, r, 0);
-            if constexpr (moves) __builtin_amdgcn_sched_group_barrier(kVector, 1, 0);
             if constexpr (w > 0) __builtin_amdgcn_sched_group_barrier(kWrite, w, 0);
             if constexpr (l > 0) __builtin_amdgcn_sched_group_barrier(kLoad, l, 0);
             interleave<kStep, kAt + 1>();
@@ -453,10 +452,26 @@ struct Tile {
         }
     }
 
-    // The tile goes through LDS so that whole rows are stored; chunks are
-    // placed by row so that neither side meets a bank twice.
+    // The sums start with what the gradient holds.
+    __device__ __forceinline__ void add_to(f32x16 (&acc)[FO][FI], const uint16_t* out) {
+#pragma unroll
+        for (int x = 0; x < FO; ++x) {
+            const int64_t o = o0 + row_of(wave, lane, x);
+#pragma unroll
+            for (int y = 0; y < FI; ++y)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) {
+                    const int64_t i = i0 + column_of(wave, lane, y, r / 4) + r % 4;
+                    if (o < a.O && i < a.I) acc[x][y][r] = lo_bf16(*gbl<uint16_t>(out + o * a.I + i));
+                }
+        }
+    }
+
+    // The tile goes through LDS so that whole rows are stored: row o's 16-byte
+    // chunk c lies at c ^ o, its halves swapped in every other 16 rows, so that
+    // neither the 8-byte writes nor the reads meet a bank twice.
     __device__ __forceinline__ void finish(f32x16 (&acc)[FO][FI], uint16_t* out) {
-        constexpr int C = TI / 8;
+        constexpr int C = TI / 8, N = TO * C / kThreads;
 #pragma unroll
         for (int x = 0; x < FO; ++x) {
             const int o = row_of(wave, lane, x);
@@ -465,31 +480,32 @@ struct Tile {
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                     const int i = column_of(wave, lane, y, r);
-                    float v[4];
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        v[q] = acc[x][y][r * 4 + q];
-                        if (a.accumulate && o0 + o < a.O && i0 + i + q < a.I)
-                            v[q] += lo_bf16(*gbl<uint16_t>(out + (o0 + o) * a.I + i0 + i + q));
-                    }
-                    const u32x2 p = {pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
-                    *(u32x2*)(lds + o * TI + ((i >> 3) ^ (o & (C - 1))) * 8 + (i & 4)) = p;
+                    const u32x2 p = {pack_bf16(acc[x][y][r * 4], acc[x][y][r * 4 + 1]),
+                                     pack_bf16(acc[x][y][r * 4 + 2], acc[x][y][r * 4 + 3])};
+                    *(u32x2*)(lds + o * TI + ((i >> 3) ^ (o & (C - 1))) * 8 + ((i & 4) ^ ((o >> 2) & 4))) = p;
                 }
             }
         }
         __syncthreads();
-        for (int j = tid; j < TO * C; j += kThreads) {
-            const int o = j / C, c = (j % C) ^ (o & (C - 1));
-            const int64_t n = a.I - i0 - c * 8;
-            if (o0 + o >= a.O || n <= 0) continue;
-            const u32x4 v = *(const u32x4*)(lds + j * 8);
-            uint16_t* d = out + (o0 + o) * a.I + i0 + c * 8;
-            if (n >= 8) {
-                *gbl_mut<u32x4_a2>(d) = v;
-            } else {
+        const bool whole = o0 + TO <= a.O && i0 + TI <= a.I;
 #pragma unroll
-                for (int q = 0; q < 7; ++q)
-                    if (q < n) *gbl_mut<uint16_t>(d + q) = (uint16_t)(v[q / 2] >> (16 * (q & 1)));
+        for (int j0 = 0; j0 < N; j0 += 4) {
+            u32x4 v[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[j] = *(const u32x4*)(lds + (tid + (j0 + j) * kThreads) * 8);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int at = tid + (j0 + j) * kThreads, o = at / C, c = (at % C) ^ (o & (C - 1));
+                if (o & 16) v[j] = u32x4{v[j][2], v[j][3], v[j][0], v[j][1]};
+                uint16_t* d = out + (o0 + o) * a.I + i0 + c * 8;
+                const int64_t n = whole ? 8 : o0 + o < a.O ? a.I - i0 - c * 8 : 0;
+                if (n >= 8) {
+                    __builtin_nontemporal_store(v[j], gbl_mut<u32x4_a2>(d));
+                } else {
+#pragma unroll
+                    for (int q = 0; q < 7; ++q)
+                        if (q < n) *gbl_mut<uint16_t>(d + q) = (uint16_t)(v[j][q / 2] >> (16 * (q & 1)));
+                }
             }
         }
     }
@@ -527,6 +543,7 @@ __global__ __launch_bounds__(kTile == 256 ? 512 : 256, kTile == 64 ? 1 : 2) void
     const int tid = threadIdx.x % K::kThreads;
     K k{a, lds + team * (K::kLds / 2), lo, hi, (int64_t)to * kTile, (int64_t)ti * kTile, tid, tid & 63, tid >> 6};
     f32x16 acc[K::FO][K::FI] = {};
+    if (kTile != 64 && a.accumulate) k.add_to(acc, g.p[e]);
     k.sum(acc);
     if constexpr (kTile == 64)
         k.finish_teams(acc, lds, team, g.p[e],
@@ -689,7 +706,7 @@ tide_status tide_weight_grads_bf16(const uint16_t* dy, int64_t dy_stride, int64_
                         (long long)rows);
         if ((x != nullptr) == (saved != nullptr) && rows > 0 && in > 0)
             return fail(TIDE_ERR_INVALID_ARG, "need either x or saved");
-        Mat rd[5], wr, ws;
+        Mat rd[6];                     // dy, x or codes, scales, offsets, token_of_row, workspace
         TIDE_TRY(matrix("dy", dy, rows, out, dy_stride, 2, &rd[0]));
         if (saved) {
             TIDE_TRY(matrix("saved", saved->codes, x_rows, in, saved->codes_stride, 1, &rd[1]));
@@ -702,23 +719,24 @@ tide_status tide_weight_grads_bf16(const uint16_t* dy, int64_t dy_stride, int64_
         TIDE_TRY(matrix("offsets", offsets, offsets ? 1 : 0, (int64_t)experts + 1,
                         (int64_t)experts + 1, 4, &rd[3]));
         TIDE_TRY(matrix("token_of_row", token_of_row, token_of_row ? 1 : 0, rows, rows, 4, &rd[4]));
-        TIDE_TRY(matrix("workspace", workspace, 1, need / 4, need / 4, 4, &ws));
-        if (ws.base & 15) return fail(TIDE_ERR_ALIGNMENT, "workspace is not 16-byte aligned");
-        TIDE_TRY(no_overlap(&ws, 1, rd, 5));
+        TIDE_TRY(matrix("workspace", workspace, 1, need / 4, need / 4, 4, &rd[5]));
+        if (need > 0 && (rd[5].base & 15))
+            return fail(TIDE_ERR_ALIGNMENT, "workspace is not 16-byte aligned");
+        TIDE_TRY(no_overlap(&rd[5], 1, rd, 5));
         if (out == 0 || in == 0) return TIDE_OK;
         if (!grads) return fail(TIDE_ERR_INVALID_ARG, "grads is NULL");
         std::vector<uintptr_t> at(experts);
+        const uintptr_t bytes = (uintptr_t)(out * in) * 2;
         for (int32_t e = 0; e < experts; ++e) {
-            char name[32];
-            snprintf(name, sizeof name, "grads[%d]", e);
-            TIDE_TRY(matrix(name, grads[e], 1, out * in, out * in, 2, &wr));
-            TIDE_TRY(no_overlap(&wr, 1, rd, 5));
-            TIDE_TRY(no_overlap(&wr, 1, &ws, 1));
-            at[e] = wr.base;
+            at[e] = (uintptr_t)grads[e];
+            if (!at[e]) return fail(TIDE_ERR_INVALID_ARG, "grads[%d] is NULL", e);
+            if (at[e] & 1) return fail(TIDE_ERR_ALIGNMENT, "grads[%d] is not 2-byte aligned", e);
+            const Mat m{"one of the grads", at[e], 1, (int64_t)bytes, (int64_t)bytes};
+            TIDE_TRY(no_overlap(&m, 1, rd, 6));
         }
         if (!std::is_sorted(at.begin(), at.end())) std::sort(at.begin(), at.end());
         for (int32_t e = 1; e < experts; ++e)
-            if (at[e] - at[e - 1] < (uintptr_t)(out * in) * 2)
+            if (at[e] - at[e - 1] < bytes)
                 return fail(TIDE_ERR_INVALID_ARG, "two of the grads overlap");
         hipStream_t stream = reinterpret_cast<hipStream_t>(stream_v);
         int dev = 0;
