@@ -6,8 +6,8 @@
 // consecutive elements of a row. The scale is a power of two, so neither the
 // division before the rounding nor the product after it rounds: a code is off
 // by half a step of e4m3 (2^-4 of its value) and nothing else, and decoding
-// to bf16 is exact. Four lanes share a block and join its maximum with two
-// DPP steps. All four kernels are HBM streams that touch each byte once.
+// to bf16 is exact. Four lanes (bf16, eight with fp32) share a block and join its
+// maximum with DPP steps. All four kernels are HBM streams that touch each byte once.
 #include "device.hpp"
 #include "host.hpp"
 
@@ -15,76 +15,44 @@ using namespace tide;
 
 namespace {
 
+typedef uint32_t u32_a1 __attribute__((aligned(1)));
 constexpr int kBlock = 32;
-constexpr int kQuad = kBlock / 8;    // lanes that share a scale
 
-__device__ __forceinline__ float quad_max(float v) {
-    const int x1 = __builtin_amdgcn_mov_dpp(__float_as_int(v), 0xB1, 0xF, 0xF, true);  // lane ^ 1
-    v = fmaxf(v, __int_as_float(x1));
-    const int x2 = __builtin_amdgcn_mov_dpp(__float_as_int(v), 0x4E, 0xF, 0xF, true);  // lane ^ 2
-    return fmaxf(v, __int_as_float(x2));
+// The largest of the kLanes (4 or 8) lanes that share a scale.
+template <int kLanes>
+__device__ __forceinline__ uint32_t block_max(uint32_t v) {
+    v = max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0xB1, 0xF, 0xF, true));       // lane ^ 1
+    v = max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x4E, 0xF, 0xF, true));       // lane ^ 2
+    if (kLanes == 8) v = max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x141, 0xF, 0xF, true));  // lane ^ 7
+    return v;
 }
-
-__device__ __forceinline__ bool finite(float v) { return fabsf(v) < __builtin_inff(); }
+__device__ __forceinline__ uint32_t magnitude(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
+constexpr uint32_t kInfinity = 0x7F800000u, kLargest = 0x7F600000u;   // 448 * 2^119
 
 // The scale byte (exponent + 127) of a block: the least 2^e with amax <= 448 *
 // 2^e. 448 = 1.75 * 2^8, so e is amax's exponent - 8, one more where its
 // mantissa passes 1.75. Bytes stop at 10 (the smallest code, 2^-9, then
 // stands for 2^-126, the smallest normal bf16) and at 246 (448 * 2^119 is the
 // largest value that does not pass bf16's range after rounding).
-__device__ __forceinline__ uint32_t scale_byte(float amax) {
-    const uint32_t b = __float_as_uint(amax);
+__device__ __forceinline__ uint32_t scale_byte(uint32_t b) {
     const int e = (int)(b >> 23) - 8 + ((b & 0x7FFFFFu) > 0x600000u ? 1 : 0);
     return (uint32_t)(e < 10 ? 10 : e > 246 ? 246 : e);
 }
 __device__ __forceinline__ float scale_of(uint32_t byte) { return __uint_as_float(byte << 23); }
 
-// Eight values of a block with scale byte `byte` as codes; what is not finite
-// becomes the NaN code.
-__device__ __forceinline__ u32x2 encode8(const float v[8], uint32_t byte) {
-    const float inv = scale_of(254 - byte);
-    float q[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-        q[i] = finite(v[i]) ? fminf(fmaxf(v[i] * inv, -448.0f), 448.0f) : __builtin_nanf("");
-    u32x2 c;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        int w = __builtin_amdgcn_cvt_pk_fp8_f32(q[4 * i], q[4 * i + 1], 0, false);
-        c[i] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(q[4 * i + 2], q[4 * i + 3], w, true);
-    }
-    return c;
+// Four values within 448 (or NaN) as codes.
+__device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d) {
+    const int w = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
+    return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c, d, w, true);
 }
-
-__device__ __forceinline__ void decode8(u32x2 c, uint32_t byte, float v[8]) {
+__device__ __forceinline__ void decode4(uint32_t c, uint32_t byte, float* v) {
     const float s = scale_of(byte);
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const f32x2 lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)c[i], false);
-        const f32x2 hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)c[i], true);
-        v[4 * i] = lo[0] * s;
-        v[4 * i + 1] = lo[1] * s;
-        v[4 * i + 2] = hi[0] * s;
-        v[4 * i + 3] = hi[1] * s;
-    }
-}
-
-__device__ __forceinline__ u32x2 load_codes(const uint8_t* p, int n) {
-    if (n >= 8) return *gbl<u32x2_a1>(p);
-    u32x2 c = {0, 0};
-#pragma unroll
-    for (int i = 0; i < 7; ++i)
-        if (i < n) c[i / 4] |= (uint32_t)*gbl<uint8_t>(p + i) << (8 * (i & 3));
-    return c;
-}
-__device__ __forceinline__ void store_codes(uint8_t* p, int n, u32x2 c) {
-    if (n >= 8) {
-        *gbl_mut<u32x2_a1>(p) = c;
-    } else {
-#pragma unroll
-        for (int i = 0; i < 7; ++i)
-            if (i < n) *gbl_mut<uint8_t>(p + i) = (uint8_t)(c[i / 4] >> (8 * (i & 3)));
-    }
+    const f32x2 lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)c, false);
+    const f32x2 hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)c, true);
+    v[0] = lo[0] * s;
+    v[1] = lo[1] * s;
+    v[2] = hi[0] * s;
+    v[3] = hi[1] * s;
 }
 
 struct Saved {
@@ -93,37 +61,99 @@ struct Saved {
     int64_t codes_stride, scales_stride;
 };
 
-// Packs this lane's eight values (n of them in the row; lanes past the row
-// have n <= 0 and zeros, and take part in the maximum all the same).
-__device__ __forceinline__ void pack8(const Saved& s, int64_t r, int64_t u, int n,
-                                      const float v[8]) {
-    float m = 0.0f;
+// A lane's V codes, n of them in the row.
+template <int V>
+struct Codes {
+    uint32_t w[V / 4];
+};
+template <int V>
+__device__ __forceinline__ Codes<V> load_codes(const uint8_t* p, int n) {
+    Codes<V> c{};
+    if (n >= V) {
+        if constexpr (V == 8) {
+            const u32x2 v = *gbl<u32x2_a1>(p);
+            c.w[0] = v[0];
+            c.w[1] = v[1];
+        } else {
+            c.w[0] = *gbl<u32_a1>(p);
+        }
+    } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) m = fmaxf(m, finite(v[i]) ? fabsf(v[i]) : 0.0f);
-    const uint32_t byte = scale_byte(quad_max(m));
-    if (n <= 0) return;
-    store_codes(s.codes + r * s.codes_stride + u * 8, n, encode8(v, byte));
-    if ((u & (kQuad - 1)) == 0)
-        *gbl_mut<uint8_t>(s.scales + r * s.scales_stride + u / kQuad) = (uint8_t)byte;
+        for (int i = 0; i < V - 1; ++i)
+            if (i < n) c.w[i / 4] |= (uint32_t)*gbl<uint8_t>(p + i) << (8 * (i & 3));
+    }
+    return c;
 }
-__device__ __forceinline__ void unpack8(const Saved& s, int64_t r, int64_t u, int n, float v[8]) {
-    const u32x2 c = load_codes(s.codes + r * s.codes_stride + u * 8, n);
-    decode8(c, *gbl<uint8_t>(s.scales + r * s.scales_stride + u / kQuad), v);
+template <int V>
+__device__ __forceinline__ void store_codes(uint8_t* p, int n, const Codes<V>& c) {
+    if (n >= V) {
+        if constexpr (V == 8) {
+            const u32x2 v = {c.w[0], c.w[1]};
+            __builtin_nontemporal_store(v, gbl_mut<u32x2_a1>(p));
+        } else {
+            __builtin_nontemporal_store(c.w[0], gbl_mut<u32_a1>(p));
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < V - 1; ++i)
+            if (i < n) *gbl_mut<uint8_t>(p + i) = (uint8_t)(c.w[i / 4] >> (8 * (i & 3)));
+    }
+}
+
+// Packs this lane's values (n of them in the row; lanes past the row have n <=
+// 0 and zeros, and take part in the maximum all the same). Magnitudes are
+// compared as integers, in which infinities and NaN are the largest: only a
+// block with one of them, or with a value past the largest scale, takes a
+// second look at each element.
+template <int V>
+__device__ __forceinline__ void pack_row(const Saved& s, int64_t r, int64_t u, int n, float (&v)[V]) {
+    constexpr int kLanes = kBlock / V;
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < V; ++i) m = max(m, magnitude(v[i]));
+    m = block_max<kLanes>(m);
+    if (m > kLargest) {
+        m = 0;
+#pragma unroll
+        for (int i = 0; i < V; ++i) m = max(m, magnitude(v[i]) < kInfinity ? magnitude(v[i]) : 0u);
+        m = block_max<kLanes>(m);
+        const float most = 448.0f * scale_of(scale_byte(m));
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            v[i] = magnitude(v[i]) < kInfinity ? fminf(fmaxf(v[i], -most), most) : __builtin_nanf("");
+    }
+    const uint32_t byte = scale_byte(m);
+    if (n <= 0) return;
+    const float inv = scale_of(254 - byte);
+    Codes<V> c;
+#pragma unroll
+    for (int i = 0; i < V / 4; ++i)
+        c.w[i] = encode4(v[4 * i] * inv, v[4 * i + 1] * inv, v[4 * i + 2] * inv, v[4 * i + 3] * inv);
+    store_codes<V>(s.codes + r * s.codes_stride + u * V, n, c);
+    if ((u & (kLanes - 1)) == 0)
+        *gbl_mut<uint8_t>(s.scales + r * s.scales_stride + u / kLanes) = (uint8_t)byte;
+}
+template <int V>
+__device__ __forceinline__ void unpack_row(const Saved& s, int64_t r, int64_t u, int n, float (&v)[V]) {
+    const Codes<V> c = load_codes<V>(s.codes + r * s.codes_stride + u * V, n);
+    const uint32_t byte = *gbl<uint8_t>(s.scales + r * s.scales_stride + u / (kBlock / V));
+#pragma unroll
+    for (int i = 0; i < V / 4; ++i) decode4(c.w[i], byte, v + 4 * i);
 }
 
 // Calls f(row, vector, elements left) for this lane's share; with kWhole the
-// four lanes of a block always run together, some of them with nothing left.
-template <bool kWhole, class F>
+// lanes of a block always run together, some of them with nothing left.
+template <int V, bool kWhole, class F>
 __device__ __forceinline__ void each_vector(int64_t n, int64_t width, int lane_log2, F&& f) {
     const int lanes = 1 << lane_log2;
-    int64_t units = (width + 7) / 8;
-    if (kWhole) units = (units + kQuad - 1) / kQuad * kQuad;
+    int64_t units = (width + V - 1) / V;
+    if (kWhole) units = (width + kBlock - 1) / kBlock * (kBlock / V);
     for (int64_t r = (int64_t)blockIdx.x * (kRowThreads >> lane_log2) + (threadIdx.x >> lane_log2);
          r < n; r += (int64_t)gridDim.x * (kRowThreads >> lane_log2)) {
         for (int64_t u = (int64_t)blockIdx.y * lanes + (threadIdx.x & (lanes - 1)); u < units;
              u += (int64_t)gridDim.y * lanes) {
-            const int64_t left = width - u * 8;
-            f(r, u, (int)(left > 8 ? 8 : left));
+            const int64_t left = width - u * V;
+            f(r, u, (int)(left > V ? V : left));
         }
     }
 }
@@ -131,10 +161,11 @@ __device__ __forceinline__ void each_vector(int64_t n, int64_t width, int lane_l
 template <class T>
 __global__ __launch_bounds__(kRowThreads) void pack_rows(const T* x, int64_t x_stride, int64_t n,
                                                          int64_t width, Saved to, int lane_log2) {
-    each_vector<true>(n, width, lane_log2, [&](int64_t r, int64_t u, int left) {
-        float v[8] = {};
-        if (left > 0) widen8(load8(x + r * x_stride + u * 8, left), v);
-        pack8(to, r, u, left, v);
+    constexpr int V = kVecOf<T>;
+    each_vector<V, true>(n, width, lane_log2, [&](int64_t r, int64_t u, int left) {
+        float v[V] = {};
+        if (left > 0) widen(load_row(x + r * x_stride + u * V, left), v);
+        pack_row<V>(to, r, u, left, v);
     });
 }
 
@@ -142,19 +173,37 @@ template <class T>
 __global__ __launch_bounds__(kRowThreads) void unpack_rows(Saved from, int64_t n, int64_t width,
                                                            T* out, int64_t out_stride,
                                                            int lane_log2) {
-    each_vector<false>(n, width, lane_log2, [&](int64_t r, int64_t u, int left) {
-        float v[8];
-        unpack8(from, r, u, left, v);
-        store8(out + r * out_stride + u * 8, left, v);
+    constexpr int V = kVecOf<T>;
+    each_vector<V, false>(n, width, lane_log2, [&](int64_t r, int64_t u, int left) {
+        float v[V];
+        unpack_row<V>(from, r, u, left, v);
+        store_row(out + r * out_stride + u * V, left, narrow(v));
     });
 }
 
-// sigmoid(g) and sigmoid(-g), neither by a difference that cancels.
+// sigmoid(g) and sigmoid(-g), neither by a difference that cancels: with e =
+// exp(-|g|) they are 1 / (1 + e) and e / (1 + e). e = 2^p, p = -|g| log2(e) in
+// two floats (the rounding of one alone would be off by |g| 2^-24 of e), past
+// the range of normal results taken 2^64 too large and brought back; the
+// reciprocal is refined once. 20 instructions instead of 45 of the library's
+// expf and division, which bounded the forward pass (210 -> GATED us at 4096 x
+// 28672).
 __device__ __forceinline__ void sigmoids(float g, float& s, float& c) {
-    const float e = expf(-fabsf(g));
-    const float big = 1.0f / (1.0f + e), small = e * big;
-    s = g >= 0.0f ? big : g < 0.0f ? small : g;      // NaN stays
-    c = g >= 0.0f ? small : g < 0.0f ? big : g;
+    const float a = fmaxf(-fabsf(g), -200.0f);     // exp(-200) is 0; a NaN comes back with the factor g
+    const float kLog2e = 0x1.715476p+0f, kRest = 0x1.4ae0cp-26f;
+    float p = a * kLog2e;
+    const float rest = __builtin_fmaf(a, kRest, __builtin_fmaf(a, kLog2e, -p));
+    const bool far = p < -120.0f;
+    p = far ? p + 64.0f : p;
+    float e = __builtin_amdgcn_exp2f(p);
+    e = __builtin_fmaf(e, rest * 0x1.62e43p-1f, e);
+    e = far ? e * 0x1p-64f : e;
+    const float d = 1.0f + e;
+    float big = __builtin_amdgcn_rcpf(d);
+    big = __builtin_fmaf(__builtin_fmaf(-d, big, 1.0f), big, big);
+    const float small = e * big;
+    s = g >= 0.0f ? big : small;
+    c = g >= 0.0f ? small : big;
 }
 
 template <class T>
@@ -163,23 +212,24 @@ __global__ __launch_bounds__(kRowThreads) void gated_rows(const T* gate, int64_t
                                                           int64_t n, int64_t width, T* out,
                                                           int64_t out_stride, Saved gate_to,
                                                           Saved up_to, int lane_log2) {
-    each_vector<true>(n, width, lane_log2, [&](int64_t r, int64_t u, int left) {
-        float g[8] = {}, v[8] = {}, h[8];
+    constexpr int V = kVecOf<T>;
+    each_vector<V, true>(n, width, lane_log2, [&](int64_t r, int64_t u, int left) {
+        float g[V] = {}, v[V] = {}, h[V];
         if (left > 0) {
-            const Raw8<T> a = load8(gate + r * gate_stride + u * 8, left);
-            const Raw8<T> b = load8(up + r * up_stride + u * 8, left);
-            widen8(a, g);
-            widen8(b, v);
+            const u32x4 a = load_row(gate + r * gate_stride + u * V, left);
+            const u32x4 b = load_row(up + r * up_stride + u * V, left);
+            widen(a, g);
+            widen(b, v);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
+            for (int i = 0; i < V; ++i) {
                 float s, c;
                 sigmoids(g[i], s, c);
                 h[i] = g[i] * s * v[i];
             }
-            store8(out + r * out_stride + u * 8, left, h);
+            store_row(out + r * out_stride + u * V, left, narrow(h));
         }
-        if (gate_to.codes) pack8(gate_to, r, u, left, g);
-        if (up_to.codes) pack8(up_to, r, u, left, v);
+        if (gate_to.codes) pack_row<V>(gate_to, r, u, left, g);
+        if (up_to.codes) pack_row<V>(up_to, r, u, left, v);
     });
 }
 
@@ -190,13 +240,14 @@ __global__ __launch_bounds__(kRowThreads) void gated_rows_grad(const T* dout, in
                                                                int64_t dgate_stride, T* dup,
                                                                int64_t dup_stride, T* out,
                                                                int64_t out_stride, int lane_log2) {
-    each_vector<false>(n, width, lane_log2, [&](int64_t r, int64_t u, int left) {
-        float d[8], g[8], v[8], dg[8], du[8], h[8];
-        widen8(load8(dout + r * dout_stride + u * 8, left), d);
-        unpack8(gate, r, u, left, g);
-        unpack8(up, r, u, left, v);
+    constexpr int V = kVecOf<T>;
+    each_vector<V, false>(n, width, lane_log2, [&](int64_t r, int64_t u, int left) {
+        float d[V], g[V], v[V], dg[V], du[V], h[V];
+        widen(load_row(dout + r * dout_stride + u * V, left), d);
+        unpack_row<V>(gate, r, u, left, g);
+        unpack_row<V>(up, r, u, left, v);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < V; ++i) {
             float s, c;
             sigmoids(g[i], s, c);
             const float t = g[i] * s;
@@ -204,9 +255,9 @@ __global__ __launch_bounds__(kRowThreads) void gated_rows_grad(const T* dout, in
             du[i] = d[i] * t;
             h[i] = t * v[i];
         }
-        store8(dgate + r * dgate_stride + u * 8, left, dg);
-        store8(dup + r * dup_stride + u * 8, left, du);
-        if (out) store8(out + r * out_stride + u * 8, left, h);
+        store_row(dgate + r * dgate_stride + u * V, left, narrow(dg));
+        store_row(dup + r * dup_stride + u * V, left, narrow(du));
+        if (out) store_row(out + r * out_stride + u * V, left, narrow(h));
     });
 }
 
@@ -253,14 +304,14 @@ Saved device_of(const tide_saved* s) {
 
 // Runs `launch` (grid, stream) with the stream's device current.
 template <class F>
-tide_status over_rows(int64_t n, int64_t width, void* stream_v, F&& launch) {
+tide_status over_rows(int64_t n, int64_t width, int32_t size, void* stream_v, F&& launch) {
     if (n == 0 || width == 0) return TIDE_OK;
     hipStream_t stream = reinterpret_cast<hipStream_t>(stream_v);
     int dev = 0;
     TIDE_TRY(stream_device(stream, &dev));
     DeviceGuard guard(dev);
     if (guard.status() != hipSuccess) return hip_fail(guard.status(), "hipSetDevice");
-    launch(row_grid(n, (width + 7) / 8, 2), stream);
+    launch(row_grid(n, (width * size + 15) / 16, size == 2 ? 2 : 3), stream);
     const hipError_t e = hipGetLastError();
     return e == hipSuccess ? TIDE_OK : hip_fail(e, "kernel launch");
 }
@@ -277,7 +328,7 @@ tide_status tide_checkpoint_pack(int32_t dtype, const void* x, int64_t x_stride,
     TIDE_TRY(c.read("x", x, rows, width, x_stride, size));
     TIDE_TRY(c.write("saved", saved, rows, width));
     TIDE_TRY(c.done());
-    return over_rows(rows, width, stream, [&](RowGrid g, hipStream_t s) {
+    return over_rows(rows, width, size, stream, [&](RowGrid g, hipStream_t s) {
         if (size == 2)
             pack_rows<uint16_t><<<g.grid, dim3(kRowThreads), 0, s>>>(
                 (const uint16_t*)x, x_stride, rows, width, device_of(saved), g.lane_log2);
@@ -295,7 +346,7 @@ tide_status tide_checkpoint_unpack(int32_t dtype, const tide_saved* saved, int64
     TIDE_TRY(c.read("saved", saved, rows, width));
     TIDE_TRY(c.write("out", out, rows, width, out_stride, size));
     TIDE_TRY(c.done());
-    return over_rows(rows, width, stream, [&](RowGrid g, hipStream_t s) {
+    return over_rows(rows, width, size, stream, [&](RowGrid g, hipStream_t s) {
         if (size == 2)
             unpack_rows<uint16_t><<<g.grid, dim3(kRowThreads), 0, s>>>(
                 device_of(saved), rows, width, (uint16_t*)out, out_stride, g.lane_log2);
@@ -318,7 +369,7 @@ tide_status tide_gated_silu(int32_t dtype, const void* gate, int64_t gate_stride
     if (gate_saved) TIDE_TRY(c.write("gate_saved", gate_saved, rows, width));
     if (up_saved) TIDE_TRY(c.write("up_saved", up_saved, rows, width));
     TIDE_TRY(c.done());
-    return over_rows(rows, width, stream, [&](RowGrid g, hipStream_t s) {
+    return over_rows(rows, width, size, stream, [&](RowGrid g, hipStream_t s) {
         if (size == 2)
             gated_rows<uint16_t><<<g.grid, dim3(kRowThreads), 0, s>>>(
                 (const uint16_t*)gate, gate_stride, (const uint16_t*)up, up_stride, rows, width,
@@ -346,7 +397,7 @@ tide_status tide_gated_silu_grad(int32_t dtype, const void* dout, int64_t dout_s
     TIDE_TRY(c.write("dup", dup, rows, width, dup_stride, size));
     TIDE_TRY(c.write("out", out, out ? rows : 0, width, out_stride, size));
     TIDE_TRY(c.done());
-    return over_rows(rows, width, stream, [&](RowGrid g, hipStream_t s) {
+    return over_rows(rows, width, size, stream, [&](RowGrid g, hipStream_t s) {
         if (size == 2)
             gated_rows_grad<uint16_t><<<g.grid, dim3(kRowThreads), 0, s>>>(
                 (const uint16_t*)dout, dout_stride, device_of(gate_saved), device_of(up_saved),

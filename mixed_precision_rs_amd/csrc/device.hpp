@@ -1,6 +1,6 @@
 // Device helpers shared by the training-layer kernels (tokens.hip,
-// checkpoint.hip, weight_grads.hip): 8-element row vectors of bf16 or fp32 at
-// any element alignment, exact widening, rounding to nearest even.
+// checkpoint.hip, weight_grads.hip): 16-byte row vectors of bf16 or fp32 at any
+// element alignment, exact widening, rounding to nearest even.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -39,91 +39,93 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
     return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2));
 }
 
-// Eight consecutive elements as they lie in memory, and as fp32.
+// A lane's vector: 16 bytes of a row, 8 bf16 or 4 fp32, so that every load and
+// store of a wave covers 1 KiB without gaps (8 fp32 a lane in two stores of
+// half-covered lines wrote 40% slower once the stores were non-temporal).
 template <class T>
-struct Raw8;
-template <>
-struct Raw8<uint16_t> {
-    u32x4 a;
-};
-template <>
-struct Raw8<float> {
-    u32x4 a, b;
-};
+constexpr int kVecOf = 16 / sizeof(T);
 
-// n = elements left in the row, at least 1; a row's last vector goes element
-// by element so that nothing past the row is touched. Elements past n read 0.
-__device__ __forceinline__ Raw8<uint16_t> load8(const uint16_t* p, int n) {
-    Raw8<uint16_t> r;
-    if (n >= 8) {
-        r.a = *gbl<u32x4_a2>(p);
-    } else {
+// 16 bytes of elements of type T, at their alignment; the stores are
+// non-temporal, since no kernel here reads what it wrote (dispatch 123 -> 110
+// us, unpacking to bf16 40 -> 30 at 16384 tokens and 8192 x 8192).
+__device__ __forceinline__ u32x4 load16(const uint16_t* p) { return *gbl<u32x4_a2>(p); }
+__device__ __forceinline__ u32x4 load16(const float* p) { return *gbl<u32x4_a4>(p); }
+__device__ __forceinline__ u32x4 load16_once(const uint16_t* p) {
+    return __builtin_nontemporal_load(gbl<u32x4_a2>(p));
+}
+__device__ __forceinline__ u32x4 load16_once(const float* p) {
+    return __builtin_nontemporal_load(gbl<u32x4_a4>(p));
+}
+__device__ __forceinline__ void store16(uint16_t* p, u32x4 v) {
+    __builtin_nontemporal_store(v, gbl_mut<u32x4_a2>(p));
+}
+__device__ __forceinline__ void store16(float* p, u32x4 v) {
+    __builtin_nontemporal_store(v, gbl_mut<u32x4_a4>(p));
+}
+
+// A vector of a row with n >= 1 elements left: a row's last vector goes element
+// by element, so that nothing past the row is touched; elements past n read 0.
+template <bool kOnce = false>
+__device__ __forceinline__ u32x4 load_row(const uint16_t* p, int n) {
+    if (n >= 8) return kOnce ? load16_once(p) : load16(p);
+    u32x4 r;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            uint32_t lo = 2 * i < n ? *gbl<uint16_t>(p + 2 * i) : 0;
-            uint32_t hi = 2 * i + 1 < n ? *gbl<uint16_t>(p + 2 * i + 1) : 0;
-            r.a[i] = lo | (hi << 16);
-        }
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t lo = 2 * i < n ? *gbl<uint16_t>(p + 2 * i) : 0;
+        const uint32_t hi = 2 * i + 1 < n ? *gbl<uint16_t>(p + 2 * i + 1) : 0;
+        r[i] = lo | (hi << 16);
     }
     return r;
 }
-__device__ __forceinline__ Raw8<float> load8(const float* p, int n) {
-    Raw8<float> r;
-    if (n >= 8) {
-        r.a = *gbl<u32x4_a4>(p);
-        r.b = *gbl<u32x4_a4>(p + 4);
-    } else {
+template <bool kOnce = false>
+__device__ __forceinline__ u32x4 load_row(const float* p, int n) {
+    if (n >= 4) return kOnce ? load16_once(p) : load16(p);
+    u32x4 r;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            r.a[i] = i < n ? *gbl<uint32_t>(p + i) : 0;
-            r.b[i] = i + 4 < n ? *gbl<uint32_t>(p + i + 4) : 0;
-        }
-    }
+    for (int i = 0; i < 4; ++i) r[i] = i < n ? *gbl<uint32_t>(p + i) : 0;
     return r;
 }
-
-__device__ __forceinline__ void widen8(const Raw8<uint16_t>& r, float v[8]) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        v[2 * i] = lo_bf16(r.a[i]);
-        v[2 * i + 1] = hi_bf16(r.a[i]);
-    }
-}
-__device__ __forceinline__ void widen8(const Raw8<float>& r, float v[8]) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        v[i] = __uint_as_float(r.a[i]);
-        v[i + 4] = __uint_as_float(r.b[i]);
-    }
-}
-
-__device__ __forceinline__ void store8(uint16_t* p, int n, const float v[8]) {
-    u32x4 a;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) a[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
+__device__ __forceinline__ void store_row(uint16_t* p, int n, u32x4 v) {
     if (n >= 8) {
-        *gbl_mut<u32x4_a2>(p) = a;
+        store16(p, v);
     } else {
 #pragma unroll
         for (int i = 0; i < 7; ++i)
-            if (i < n) *gbl_mut<uint16_t>(p + i) = (uint16_t)(a[i / 2] >> (16 * (i & 1)));
+            if (i < n) *gbl_mut<uint16_t>(p + i) = (uint16_t)(v[i / 2] >> (16 * (i & 1)));
     }
 }
-__device__ __forceinline__ void store8(float* p, int n, const float v[8]) {
-    if (n >= 8) {
-        u32x4 a, b;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            a[i] = __float_as_uint(v[i]);
-            b[i] = __float_as_uint(v[i + 4]);
-        }
-        *gbl_mut<u32x4_a4>(p) = a;
-        *gbl_mut<u32x4_a4>(p + 4) = b;
+__device__ __forceinline__ void store_row(float* p, int n, u32x4 v) {
+    if (n >= 4) {
+        store16(p, v);
     } else {
 #pragma unroll
-        for (int i = 0; i < 7; ++i)
-            if (i < n) *gbl_mut<float>(p + i) = v[i];
+        for (int i = 0; i < 3; ++i)
+            if (i < n) *gbl_mut<uint32_t>(p + i) = v[i];
     }
+}
+
+__device__ __forceinline__ void widen(u32x4 r, float (&v)[8]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[2 * i] = lo_bf16(r[i]);
+        v[2 * i + 1] = hi_bf16(r[i]);
+    }
+}
+__device__ __forceinline__ void widen(u32x4 r, float (&v)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ u32x4 narrow(const float (&v)[8]) {
+    u32x4 r;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
+    return r;
+}
+__device__ __forceinline__ u32x4 narrow(const float (&v)[4]) {
+    u32x4 r;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r[i] = __float_as_uint(v[i]);
+    return r;
 }
 
 // Lanes of a 256-thread workgroup over rows of `units` vectors: 2^lane_log2

@@ -177,19 +177,10 @@ __global__ __launch_bounds__(kRowThreads) void dispatch_rows(
         for (int64_t u = (int64_t)blockIdx.y * lanes + (threadIdx.x & (lanes - 1)); u < units;
              u += (int64_t)gridDim.y * lanes) {
             const int left = (int)(width - u * 8 < 8 ? width - u * 8 : 8);
-            const Raw8<uint16_t> v = load8(x + t * x_stride + u * 8, left);
+            const u32x4 v = load_row(x + t * x_stride + u * 8, left);
             for (int32_t j = 0; j < k; ++j) {
                 const int32_t s = *gbl<int32_t>(slots + t * k + j);
-                if ((uint32_t)s >= nrows) continue;
-                uint16_t* d = rows + (int64_t)s * rows_stride + u * 8;
-                if (left == 8) {
-                    *gbl_mut<u32x4_a2>(d) = v.a;
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 7; ++i)
-                        if (i < left)
-                            *gbl_mut<uint16_t>(d + i) = (uint16_t)(v.a[i / 2] >> (16 * (i & 1)));
-                }
+                if ((uint32_t)s < nrows) store_row(rows + (int64_t)s * rows_stride + u * 8, left, v);
             }
         }
     }
@@ -201,95 +192,108 @@ template <class T, int KU>
 __global__ __launch_bounds__(kRowThreads) void combine_rows(
     const T* rows, int64_t rows_stride, uint32_t nrows, int64_t width, const int32_t* slots,
     const float* weights, int64_t tokens, int32_t k, T* out, int64_t out_stride, int lane_log2) {
+    constexpr int V = kVecOf<T>;
     const int lanes = 1 << lane_log2;
-    const int64_t units = (width + 7) / 8;
+    const int64_t units = (width + V - 1) / V;
     for (int64_t t = (int64_t)blockIdx.x * (kRowThreads >> lane_log2) + (threadIdx.x >> lane_log2);
          t < tokens; t += (int64_t)gridDim.x * (kRowThreads >> lane_log2)) {
         for (int64_t u = (int64_t)blockIdx.y * lanes + (threadIdx.x & (lanes - 1)); u < units;
              u += (int64_t)gridDim.y * lanes) {
-            const int left = (int)(width - u * 8 < 8 ? width - u * 8 : 8);
-            float acc[8] = {};
+            const int left = (int)(width - u * V < V ? width - u * V : V);
+            float acc[V] = {};
             for (int32_t j0 = 0; j0 < k; j0 += KU) {
-                Raw8<T> raw[KU];
+                u32x4 raw[KU];
                 float w[KU];
 #pragma unroll
                 for (int i = 0; i < KU; ++i) {
                     const int32_t s = j0 + i < k ? *gbl<int32_t>(slots + t * k + j0 + i) : -1;
-                    const bool there = (uint32_t)s < nrows;
-                    raw[i] = Raw8<T>{};
+                    raw[i] = u32x4{};
                     w[i] = 0.0f;
-                    if (there) {
-                        raw[i] = load8(rows + (int64_t)s * rows_stride + u * 8, left);
+                    if ((uint32_t)s < nrows) {
+                        raw[i] = load_row<true>(rows + (int64_t)s * rows_stride + u * V, left);
                         w[i] = weights ? *gbl<float>(weights + t * k + j0 + i) : 1.0f;
                     }
                 }
 #pragma unroll
                 for (int i = 0; i < KU; ++i) {
-                    float v[8];
-                    widen8(raw[i], v);
+                    float v[V];
+                    widen(raw[i], v);
 #pragma unroll
-                    for (int c = 0; c < 8; ++c) acc[c] = __builtin_fmaf(w[i], v[c], acc[c]);
+                    for (int c = 0; c < V; ++c) acc[c] = __builtin_fmaf(w[i], v[c], acc[c]);
                 }
             }
-            store8(out + t * out_stride + u * 8, left, acc);
+            store_row(out + t * out_stride + u * V, left, narrow(acc));
         }
     }
 }
 
 // drows[slots[t, j]] = weights[t, j] * dout[t] and dweights[t, j] = dout[t] .
-// rows[slots[t, j]]: one wave a token, KU rows at a time. Each lane sums its
-// vectors in order and the lanes are joined by a fixed tree.
+// rows[slots[t, j]], KU rows at a time. A token has 64 to 256 lanes, enough
+// for a row of 2048 bf16 in one pass: a wave's later loads wait for its
+// earlier stores, so a token's loads all come first. Each lane sums its
+// vectors in order, a fixed tree joins a wave's lanes and LDS the waves.
 template <class T, int KU>
 __global__ __launch_bounds__(kRowThreads) void combine_rows_grad(
     const T* dout, int64_t dout_stride, const T* rows, int64_t rows_stride, uint32_t nrows,
     int64_t width, const int32_t* slots, const float* weights, int64_t tokens, int32_t k,
-    T* drows, int64_t drows_stride, float* dweights) {
-    const int lane = threadIdx.x & 63;
-    const int64_t units = (width + 7) / 8;
-    for (int64_t t = (int64_t)blockIdx.x * (kRowThreads / 64) + (threadIdx.x >> 6); t < tokens;
-         t += (int64_t)gridDim.x * (kRowThreads / 64)) {
+    T* drows, int64_t drows_stride, float* dweights, int lane_log2) {
+    constexpr int V = kVecOf<T>;
+    __shared__ float dots[kRowThreads / 64][KU];
+    const int lanes = 1 << lane_log2, lane = threadIdx.x & (lanes - 1);
+    const int64_t units = (width + V - 1) / V;
+    const int64_t per = kRowThreads >> lane_log2;
+    for (int64_t t0 = (int64_t)blockIdx.x * per; t0 < tokens; t0 += (int64_t)gridDim.x * per) {
+        const int64_t t = t0 + (threadIdx.x >> lane_log2);
         for (int32_t j0 = 0; j0 < k; j0 += KU) {
             int32_t s[KU];
             float w[KU], dot[KU] = {};
 #pragma unroll
             for (int i = 0; i < KU; ++i) {
-                s[i] = j0 + i < k ? *gbl<int32_t>(slots + t * k + j0 + i) : -1;
+                s[i] = t < tokens && j0 + i < k ? *gbl<int32_t>(slots + t * k + j0 + i) : -1;
                 if ((uint32_t)s[i] >= nrows) s[i] = -1;
                 w[i] = s[i] >= 0 && weights ? *gbl<float>(weights + t * k + j0 + i) : 1.0f;
             }
-            for (int64_t u = lane; u < units; u += 64) {
-                const int left = (int)(width - u * 8 < 8 ? width - u * 8 : 8);
-                float d[8];
-                widen8(load8(dout + t * dout_stride + u * 8, left), d);
-                Raw8<T> raw[KU];
+            for (int64_t u = lane; t < tokens && u < units; u += lanes) {
+                const int left = (int)(width - u * V < V ? width - u * V : V);
+                float d[V];
+                widen(load_row(dout + t * dout_stride + u * V, left), d);
+                u32x4 raw[KU];
 #pragma unroll
                 for (int i = 0; i < KU; ++i) {
-                    raw[i] = Raw8<T>{};
+                    raw[i] = u32x4{};
                     if (s[i] >= 0 && dweights)
-                        raw[i] = load8(rows + (int64_t)s[i] * rows_stride + u * 8, left);
+                        raw[i] = load_row<true>(rows + (int64_t)s[i] * rows_stride + u * V, left);
+                }
+#pragma unroll
+                for (int i = 0; i < KU; ++i) {
+                    float v[V];
+                    widen(raw[i], v);
+#pragma unroll
+                    for (int c = 0; c < V; ++c) dot[i] = __builtin_fmaf(d[c], v[c], dot[i]);
                 }
 #pragma unroll
                 for (int i = 0; i < KU; ++i) {
                     if (s[i] < 0) continue;
-                    float v[8];
-                    widen8(raw[i], v);
+                    float v[V];
 #pragma unroll
-                    for (int c = 0; c < 8; ++c) dot[i] = __builtin_fmaf(d[c], v[c], dot[i]);
-#pragma unroll
-                    for (int c = 0; c < 8; ++c) v[c] = w[i] * d[c];
-                    store8(drows + (int64_t)s[i] * drows_stride + u * 8, left, v);
+                    for (int c = 0; c < V; ++c) v[c] = w[i] * d[c];
+                    store_row(drows + (int64_t)s[i] * drows_stride + u * V, left, narrow(v));
                 }
             }
-            if (dweights) {
+            if (!dweights) continue;
 #pragma unroll
-                for (int i = 0; i < KU; ++i) {
-                    float v = dot[i];
+            for (int i = 0; i < KU; ++i) {
 #pragma unroll
-                    for (int m = 32; m > 0; m >>= 1) v += __shfl_xor(v, m);
-                    if (lane == 0 && j0 + i < k)
-                        *gbl_mut<float>(dweights + t * k + j0 + i) = s[i] >= 0 ? v : 0.0f;
-                }
+                for (int m = 32; m > 0; m >>= 1) dot[i] += __shfl_xor(dot[i], m);
+                if ((threadIdx.x & 63) == 0) dots[threadIdx.x / 64][i] = s[i] >= 0 ? dot[i] : 0.0f;
             }
+            __syncthreads();
+            if (lane < KU && t < tokens && j0 + lane < k) {
+                float v = 0.0f;
+                for (int i = 0; i < lanes / 64; ++i) v += dots[threadIdx.x / 64 + i][lane];
+                *gbl_mut<float>(dweights + t * k + j0 + lane) = v;
+            }
+            __syncthreads();
         }
     }
 }
@@ -422,7 +426,7 @@ tide_status tide_combine_tokens(int32_t dtype, const void* rows, int64_t rows_st
     TIDE_TRY(no_overlap(&wr, 1, rd, 3));
     if (tokens == 0 || width == 0) return TIDE_OK;
     return on_stream(stream, [&](hipStream_t s) {
-        const RowGrid g = row_grid(tokens, (width + 7) / 8);
+        const RowGrid g = row_grid(tokens, (width * size + 15) / 16);
         with_ku(k, [&](auto ku) {
             if (size == 2)
                 combine_rows<uint16_t, ku.value><<<g.grid, dim3(kRowThreads), 0, s>>>(
@@ -454,19 +458,19 @@ tide_status tide_combine_tokens_grad(int32_t dtype, const void* dout, int64_t do
     TIDE_TRY(no_overlap(wr, 2, rd, 4));
     if (tokens == 0 || (width == 0 && !dweights)) return TIDE_OK;
     return on_stream(stream, [&](hipStream_t s) {
-        const int64_t per = kRowThreads / 64, gx = (tokens + per - 1) / per;
-        const dim3 grid((uint32_t)(gx < (1 << 23) ? gx : (1 << 23)));
+        const RowGrid g = row_grid(tokens, (width * size + 15) / 16, 6);
+        const dim3 grid(g.grid.x);
         with_ku(k, [&](auto ku) {
             if (size == 2)
                 combine_rows_grad<uint16_t, ku.value><<<grid, dim3(kRowThreads), 0, s>>>(
                     (const uint16_t*)dout, dout_stride, (const uint16_t*)rows, rows_stride,
                     (uint32_t)nrows, width, slots, weights, tokens, k, (uint16_t*)drows,
-                    drows_stride, dweights);
+                    drows_stride, dweights, g.lane_log2);
             else
                 combine_rows_grad<float, ku.value><<<grid, dim3(kRowThreads), 0, s>>>(
                     (const float*)dout, dout_stride, (const float*)rows, rows_stride,
                     (uint32_t)nrows, width, slots, weights, tokens, k, (float*)drows,
-                    drows_stride, dweights);
+                    drows_stride, dweights, g.lane_log2);
         });
         return hipGetLastError();
     });

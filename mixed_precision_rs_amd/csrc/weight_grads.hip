@@ -250,7 +250,7 @@ struct Tile {
                 const int64_t n = a.O - o0 - c * 8;
                 m.o[j] = u32x4{};
                 if (n > 0 && t < rows)
-                    m.o[j] = load8(a.dy + (t0 + t) * a.dy_stride + o0 + c * 8, (int)(n < 8 ? n : 8)).a;
+                    m.o[j] = load_row(a.dy + (t0 + t) * a.dy_stride + o0 + c * 8, (int)(n < 8 ? n : 8));
             }
 #pragma unroll
             for (int j = kPart * NI / kOf; j < (kPart + 1) * NI / kOf; ++j) {
@@ -264,7 +264,7 @@ struct Tile {
                         m.i[j] = codes16(a.codes + row * a.codes_stride + col, (int)(n < 16 ? n : 16));
                         m.s[j] = *gbl<uint8_t>(a.scales + row * a.scales_stride + col / kBlock);
                     } else {
-                        m.i[j] = load8(a.x + row * a.x_stride + col, (int)(n < 8 ? n : 8)).a;
+                        m.i[j] = load_row(a.x + row * a.x_stride + col, (int)(n < 8 ? n : 8));
                     }
                 }
             }

@@ -204,8 +204,9 @@ def test_gated_gradient_by_differences(tide):
 
 def test_gated_extremes(tide):
     """Large gates of both signs, infinities and NaN follow the formula."""
-    g = torch.tensor([[-1e4, -88.0, -90.0, 88.0, 1e4, 0.0, float("nan"), 2.0]])
-    u = torch.tensor([[1.0, 1.0, 2.0, 1.0, 3.0, 5.0, 1.0, float("inf")]])
+    inf = float("inf")
+    g = torch.tensor([[-1e4, -88.0, -90.0, 88.0, 1e4, 0.0, float("nan"), 2.0, inf, -inf, inf, 3e38, -3e38]])
+    u = torch.tensor([[1.0, 1.0, 2.0, 1.0, 3.0, 5.0, 1.0, inf, 2.0, 1.0, 0.0, 0.5, 1.0]])
     out = torch.empty_like(g, device=dev())
     tide.gated_silu(g.to(dev()), u.to(dev()), out)
     want = ref.gated(g, u)
