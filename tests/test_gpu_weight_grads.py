@@ -202,6 +202,20 @@ def test_not_finite_values_stay_in_their_rows_and_columns(tide):
         assert torch.equal(bad, want)
 
 
+@pytest.mark.parametrize("big", [-100, 100])
+def test_checkpoints_of_extreme_scales(tide, big):
+    """Values near both ends of the scales' range decode as unpacking does."""
+    n, O, I = 70, 24, 64
+    x = ref.normal((n, I), torch.float32, seed=8) * 2.0 ** big
+    x[:, ::5] *= 2.0 ** (-14 if big < 0 else 14)
+    dy = (ref.normal((n, O), torch.float32, seed=9) * 2.0 ** (60 if big < 0 else -60)).to(torch.bfloat16)
+    s = ref.saved_of(x)
+    g = torch.empty(1, O, I, dtype=torch.bfloat16, device=dev())
+    tide.weight_grads_bf16(dy.to(dev()), tuple(t.to(dev()) for t in s), g)
+    want, mag, cnt = ref.weight_grads(dy, ref.unpack(*s), torch.tensor([0, n]), None)
+    ref.close(g[0], want[0], bound(want[0], mag[0], cnt[0]))
+
+
 def test_tokens_out_of_range_add_nothing(tide):
     n, O, I = 90, 40, 64
     tokens = torch.arange(n) % 50
