@@ -41,7 +41,7 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 #define TIDE_LDS __attribute__((address_space(3)))
 
-constexpr int kDepth = 64;             // rows (tokens) of one stage
+constexpr int kMostDepth = 64;         // rows (tokens) of one stage, at most
 // How rows are read. Buffers: every row starts on 16 bytes and holds whole
 // 16-byte loads, which are bounds-checked buffer loads. Vectors: any alignment
 // and length from one load on; a row's last load ends at its end and is
@@ -118,32 +118,35 @@ __device__ __forceinline__ void store4(const Args& a, uint16_t* out, int64_t o, 
     }
 }
 
-// A kTile x kTile tile of one expert's gradient. Rows of dy and x are staged in
-// LDS as bf16, kDepth at a time, and read back transposed
+// A TO x TI tile of one expert's gradient. Rows of dy and x are staged in
+// LDS as bf16, 64 or 32 at a time, and read back transposed
 // (ds_read_b64_tr_b16), since the matrix instruction wants the summed index
 // (the row) inside a lane; products are 32x32x16 bf16 with fp32 sums. The 256
 // tile has 8 waves of 128 x 64 (128 sums a lane, two waves a SIMD: 4 waves of
 // 128 x 128 leave every wait exposed and reach 1060 instead of 1200 TFLOP/s on
-// 8192 x 8192 x 8192), the 128 tile 4 of 64 x 64. The 64 tile is for few
+// 8192 x 8192 x 8192), the 128 tile 4 of 64 x 64. The 256 x 128 tile has 4
+// waves of 128 x 64 and stages of 32 rows, so that two workgroups fit a CU: one
+// stores its tile while the other sums (128 experts of 768 x 2048, 32 rows
+// each: 77 us against 104 in tiles of 256). The 64 tile is for few
 // tiles: its 4 waves are teams of one, each with the whole tile, stages of its
 // own and a quarter of the rows, joined at the end through LDS; nothing but
 // that join waits on another wave.
 // kSaved: x is a checkpoint, decoded on its way into LDS (exact, and free:
 // both forms run at 1150 TFLOP/s).
-template <int kTile, bool kSaved, int kAccess>
+template <int TO, int TI, bool kSaved, int kAccess>
 struct Tile {
-    static constexpr int TO = kTile, TI = kTile;
-    static constexpr int kThreads = kTile == 256 ? 512 : kTile == 128 ? 256 : 64;      // of a team
-    static constexpr int kTeams = kTile == 64 ? 4 : 1;
-    static constexpr int WO = kTile == 64 ? 1 : 2, WI = kThreads / 64 / WO;    // waves over the tile
+    static constexpr int kTeams = TO == 64 ? 4 : 1;
+    static constexpr int kThreads = (TI == 256 ? 512 : 256) / kTeams;          // of a team
+    static constexpr int kDepth = TO == TI ? kMostDepth : kMostDepth / 2;      // rows of a stage
+    static constexpr int WO = TO == 64 ? 1 : 2, WI = kThreads / 64 / WO;       // waves over the tile
     static constexpr int FO = TO / WO / 32, FI = TI / WI / 32;  // 32 x 32 blocks of a wave
     static constexpr int kSteps = kDepth / 16;                 // matrix steps of a stage
-    static constexpr int kParts = 2;                           // steps that move a stage's chunks
+    static constexpr int kParts = kSteps / 2;                  // steps that move a stage's chunks
     static constexpr int CO = TO / 8;                          // chunks of a staged row of dy
     static constexpr int NO = kDepth * CO / kThreads;          // chunks of dy a thread stages
     static constexpr int CI = TI / (kSaved ? 16 : 8);          // 16-byte loads of a row of x
     static constexpr int NI = kDepth * CI / kThreads;
-    static_assert(kSteps == 4, "the steps of sum()");
+    static_assert(kSteps == 2 || kSteps == 4, "the steps of sum()");
     static constexpr int kStage = kDepth * (TO + TI);          // elements of one stage
     static constexpr int kLds = 2 * kStage * 2 > TO * TI * 2 ? 2 * kStage * 2 : TO * TI * 2;
 
@@ -313,21 +316,21 @@ struct Tile {
     // A 32-column block of 16 staged rows as a matrix operand: lane l holds
     // column l % 32, rows (l / 32) * 8 + 0 .. 7. Each transposing read gives a
     // lane four rows of one column out of the 4 x 16 blocks that 16 lanes name.
-    static_assert(TO == TI, "one width");
+    template <int kWidth>
     __device__ __forceinline__ bf16x8 operand(const uint16_t* rows, int step, int col) {
         const int t = step * 16 + (lane >> 5) * 8 + ((lane & 15) >> 2);
         const int c = (col >> 3) + ((lane >> 4) & 1) * 2 + ((lane & 3) >> 1);
-        const uint16_t* p = rows + t * TI + chunk_at<TI>(t, c) * 8 + (lane & 1) * 4;
+        const uint16_t* p = rows + t * kWidth + chunk_at<kWidth>(t, c) * 8 + (lane & 1) * 4;
         const s16x4 u = __builtin_amdgcn_ds_read_tr16_b64_v4i16((TIDE_LDS s16x4*)p);
-        const s16x4 v = __builtin_amdgcn_ds_read_tr16_b64_v4i16((TIDE_LDS s16x4*)(p + 4 * TI));
+        const s16x4 v = __builtin_amdgcn_ds_read_tr16_b64_v4i16((TIDE_LDS s16x4*)(p + 4 * kWidth));
         const bf16x4 x = __builtin_bit_cast(bf16x4, u), y = __builtin_bit_cast(bf16x4, v);
         return __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7);
     }
     __device__ __forceinline__ void operands(int b, int step, bf16x8 (&fo)[FO], bf16x8 (&fi)[FI]) {
 #pragma unroll
-        for (int f = 0; f < FO; ++f) fo[f] = operand(stage_o(b), step, (wave / WI) * (TO / WO) + f * 32);
+        for (int f = 0; f < FO; ++f) fo[f] = operand<TO>(stage_o(b), step, (wave / WI) * (TO / WO) + f * 32);
 #pragma unroll
-        for (int f = 0; f < FI; ++f) fi[f] = operand(stage_i(b), step, (wave % WI) * (TI / WI) + f * 32);
+        for (int f = 0; f < FI; ++f) fi[f] = operand<TI>(stage_i(b), step, (wave % WI) * (TI / WI) + f * 32);
     }
 
     // Asks the scheduler to spread a step's LDS and memory instructions over
@@ -398,8 +401,10 @@ struct Tile {
                 if (b > 0 && t >= hi) break;
                 step<0>(t, b, m, fo, fi, acc);
                 step<1>(t, b, m, fo, fi, acc);
-                step<2>(t, b, m, fo, fi, acc);
-                step<3>(t, b, m, fo, fi, acc);
+                if constexpr (kSteps == 4) {
+                    step<2>(t, b, m, fo, fi, acc);
+                    step<3>(t, b, m, fo, fi, acc);
+                }
             }
         }
         sync();
@@ -511,9 +516,10 @@ struct Tile {
     }
 };
 
-template <int kTile, bool kSaved, int kAccess>
-__global__ __launch_bounds__(kTile == 256 ? 512 : 256, kTile == 64 ? 1 : 2) void weight_grads(Args a, GradPtrs g) {
-    using K = Tile<kTile, kSaved, kAccess>;
+template <int TO, int TI, bool kSaved, int kAccess>
+__global__ __launch_bounds__(TI == 256 ? 512 : 256, TO == 64 ? 1 : 2) void weight_grads(Args a, GradPtrs g) {
+    using K = Tile<TO, TI, kSaved, kAccess>;
+    constexpr bool kInTeams = K::kTeams > 1;
     __shared__ __attribute__((aligned(1024))) uint16_t lds[K::kTeams * K::kLds / 2];
     // Workgroups go round robin over the XCDs: each XCD gets one run of tiles,
     // so that tiles that share rows share an L2.
@@ -533,21 +539,21 @@ __global__ __launch_bounds__(kTile == 256 ? 512 : 256, kTile == 64 ? 1 : 2) void
         lo = lo < 0 ? 0 : lo > a.n ? a.n : lo;
         hi = hi < lo ? lo : hi > a.n ? a.n : hi;
     }
-    const int team = kTile == 64 ? __builtin_amdgcn_readfirstlane(threadIdx.x / K::kThreads) : 0;
-    if (kTile == 64) {                 // whole stages to each team of each split
-        const int64_t parts = a.splits * K::kTeams, stages = (hi - lo + kDepth - 1) / kDepth;
-        const int64_t each = (stages + parts - 1) / parts * kDepth;
+    const int team = kInTeams ? __builtin_amdgcn_readfirstlane(threadIdx.x / K::kThreads) : 0;
+    if (kInTeams) {                    // whole stages to each team of each split
+        const int64_t parts = a.splits * K::kTeams, stages = (hi - lo + K::kDepth - 1) / K::kDepth;
+        const int64_t each = (stages + parts - 1) / parts * K::kDepth;
         lo = min(lo + (split * K::kTeams + team) * each, hi);
         hi = min(lo + each, hi);
     }
     const int tid = threadIdx.x % K::kThreads;
-    K k{a, lds + team * (K::kLds / 2), lo, hi, (int64_t)to * kTile, (int64_t)ti * kTile, tid, tid & 63, tid >> 6};
+    K k{a, lds + team * (K::kLds / 2), lo, hi, (int64_t)to * TO, (int64_t)ti * TI, tid, tid & 63, tid >> 6};
     f32x16 acc[K::FO][K::FI] = {};
-    if (kTile != 64 && a.accumulate) k.add_to(acc, g.p[e]);
+    if (!kInTeams && a.accumulate) k.add_to(acc, g.p[e]);
     k.sum(acc);
-    if constexpr (kTile == 64)
+    if constexpr (kInTeams)
         k.finish_teams(acc, lds, team, g.p[e],
-                       a.splits > 1 ? a.partial + ((int64_t)part * tiles + to * a.tiles_i + ti) * (kTile * kTile)
+                       a.splits > 1 ? a.partial + ((int64_t)part * tiles + to * a.tiles_i + ti) * (TO * TI)
                                     : nullptr);
     else
         k.finish(acc, g.p[e]);
@@ -555,7 +561,7 @@ __global__ __launch_bounds__(kTile == 256 ? 512 : 256, kTile == 64 ? 1 : 2) void
 
 // Joins the splits of 64 tiles, in order: four columns a lane.
 __global__ __launch_bounds__(256) void join_splits(Args a, GradPtrs g) {
-    constexpr int kTile = 64, kPer = kTile * kTile / 4 / 256;      // workgroups a tile
+    constexpr int kTile = 64, kPer = kTile * kTile / 4 / 256;      // workgroups for a tile
     const int tiles = a.tiles_o * a.tiles_i;
     const int j = blockIdx.x % kPer * 256 + threadIdx.x, tile = blockIdx.x / kPer % tiles;
     const int e = blockIdx.x / kPer / tiles;
@@ -575,18 +581,18 @@ __global__ __launch_bounds__(256) void join_splits(Args a, GradPtrs g) {
            (int64_t)(tile % a.tiles_i) * kTile + j % (kTile / 4) * 4, v);
 }
 
-template <int kTile>
+template <int TO, int TI>
 hipError_t launch_tiles(const Args& a, const GradPtrs& g, Access how, hipStream_t stream) {
     const int64_t groups = (int64_t)a.count * a.splits * a.tiles_o * a.tiles_i;
-    const dim3 grid((uint32_t)((groups + 7) / 8 * 8)), threads(kTile == 256 ? 512 : 256);
+    const dim3 grid((uint32_t)((groups + 7) / 8 * 8)), threads(TI == 256 ? 512 : 256);
     if (a.codes) {
-        if (how == kBuffers) weight_grads<kTile, true, kBuffers><<<grid, threads, 0, stream>>>(a, g);
-        else if (how == kVectors) weight_grads<kTile, true, kVectors><<<grid, threads, 0, stream>>>(a, g);
-        else if constexpr (kTile == 64) weight_grads<kTile, true, kElements><<<grid, threads, 0, stream>>>(a, g);
+        if (how == kBuffers) weight_grads<TO, TI, true, kBuffers><<<grid, threads, 0, stream>>>(a, g);
+        else if (how == kVectors) weight_grads<TO, TI, true, kVectors><<<grid, threads, 0, stream>>>(a, g);
+        else if constexpr (TO == 64) weight_grads<TO, TI, true, kElements><<<grid, threads, 0, stream>>>(a, g);
     } else {
-        if (how == kBuffers) weight_grads<kTile, false, kBuffers><<<grid, threads, 0, stream>>>(a, g);
-        else if (how == kVectors) weight_grads<kTile, false, kVectors><<<grid, threads, 0, stream>>>(a, g);
-        else if constexpr (kTile == 64) weight_grads<kTile, false, kElements><<<grid, threads, 0, stream>>>(a, g);
+        if (how == kBuffers) weight_grads<TO, TI, false, kBuffers><<<grid, threads, 0, stream>>>(a, g);
+        else if (how == kVectors) weight_grads<TO, TI, false, kVectors><<<grid, threads, 0, stream>>>(a, g);
+        else if constexpr (TO == 64) weight_grads<TO, TI, false, kElements><<<grid, threads, 0, stream>>>(a, g);
     }
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || a.splits == 1) return e;
@@ -600,11 +606,11 @@ hipError_t launch_tiles(const Args& a, const GradPtrs& g, Access how, hipStream_
 Access how_to_read(const Args& a) {
     const int64_t step = a.codes ? 16 : 8, xs = a.codes ? a.codes_stride : a.x_stride * 2;
     const uintptr_t base = a.codes ? (uintptr_t)a.codes : (uintptr_t)a.x;
-    const int64_t rows = a.tokens ? a.x_rows : kDepth;
+    const int64_t rows = a.tokens ? a.x_rows : kMostDepth;
     const int64_t lim = kMostBytes;
     if (a.O < 8 || a.I < step) return kElements;
     if (a.O % 8 == 0 && a.I % step == 0 && ((uintptr_t)a.dy & 15) == 0 && a.dy_stride % 8 == 0 &&
-        (base & 15) == 0 && xs % 16 == 0 && a.dy_stride <= lim / 2 / kDepth && (rows == 0 || xs <= lim / rows) &&
+        (base & 15) == 0 && xs % 16 == 0 && a.dy_stride <= lim / 2 / kMostDepth && (rows == 0 || xs <= lim / rows) &&
         (rows == 0 || a.scales_stride <= lim / rows))
         return kBuffers;
     return kVectors;
@@ -616,48 +622,54 @@ Access how_to_read(const Args& a) {
         if (s_ != TIDE_OK) return s_;         \
     } while (0)
 
-// Tile edge and splits. A large tile reuses each staged element more (1180,
-// 870 and 410 TFLOP/s on long sums, edges 256, 128 and 64), a small one leaves
-// fewer CUs idle and, with its teams, waits less. The costs below, in us, are
-// fits to measured times: a round of workgroups has a part that does not
-// depend on the rows, and each stage of 64 rows adds to it. Both sides where
-// the choice turns: 1024 x 8192 from 8192 rows 193 us with 128 tiles of 256,
-// 180 with 512 of 128; 8 experts of 1984 x 704 33 us (192 of 256) and 40 (768
-// of 128); 512 x 2048 from 1000 rows 18.4 us (64 of 128) and 13.5 (256 of 64);
-// 2048 x 2048 from 64 rows 15 us (256 of 128) and 22 (1024 of 64).
+// Tile and splits. A large tile reuses each staged element more (1200, 1080,
+// 870 and 410 TFLOP/s on long sums, in tiles of 256 x 256, 256 x 128, 128 x 128
+// and 64 x 64), a small one leaves fewer CUs idle and, with its teams, waits
+// less. The costs below, in us, are fits to measured times: a round of
+// workgroups has a part that does not depend on the rows, and each stage of 64
+// rows adds to it. Both sides where the choice turns: 128 experts of 768 x 2048
+// with 512 rows each 255 us in 256 x 256 and 250 in 256 x 128, with 64 rows 112
+// and 92; 1024 x 8192 from 8192 rows 193 us (128 tiles of 256 x 256), 154 (256
+// of 256 x 128) and 158 (512 of 128 x 128); 8 experts of 384 x 700, 512 rows
+// each, 43 us (96 of 256 x 128) and 25 (144 of 128 x 128); 512 x 2048 from 1000
+// rows 18.4 us (64 of 128 x 128) and 13.5 (256 of 64 x 64); 2048 x 2048 from 64
+// rows 15 us (256 of 128 x 128) and 22 (1024 of 64 x 64).
 // Splits: where even tiles of 64 leave CUs idle, the rows of each are divided
 // among several workgroups, whose fp32 sums a second kernel adds in order:
 // 128 x 2048 from 8192 rows 37 us with one, 20 with four.
 struct Plan {
     int64_t tiles_o, tiles_i;
-    int tile, splits;
+    int tile_o, tile_i, splits;
 };
 Plan plan_tiles(int64_t n, int64_t O, int64_t I, int32_t experts) {
-    const int64_t cap = 1 << 20, stages = (n / experts + kDepth - 1) / kDepth;
-    const auto tiles = [&](int64_t edge) {
-        return std::min((O + edge - 1) / edge, cap) * std::min((I + edge - 1) / edge, cap) * experts;
+    const int64_t cap = 1 << 20, stages = (n / experts + kMostDepth - 1) / kMostDepth;
+    const auto tiles = [&](int64_t o, int64_t i) {
+        return std::min((O + o - 1) / o, cap) * std::min((I + i - 1) / i, cap) * experts;
     };
     const auto rounds = [](int64_t groups, int64_t at_once) { return (double)((groups + at_once - 1) / at_once); };
-    const int64_t small = tiles(64);
-    Plan p{0, 0, 64, 1};
+    const double s = (double)stages;
+    const int64_t small = tiles(64, 64);
+    Plan p{0, 0, 64, 64, 1};
     double best = 0;
-    for (int64_t s = 1; s == 1 || (s * small <= 256 && s * 4 <= stages); s *= 2) {
-        const double us = rounds(s * small, 256) * (6 + 0.75 * (double)((stages + 4 * s - 1) / (4 * s))) +
-                          (s > 1 ? 5 + 0.01 * (double)(s * small) : 0);
-        if (s == 1 || us < best) {
+    for (int64_t k = 1; k == 1 || (k * small <= 256 && k * 4 <= stages); k *= 2) {
+        const double us = rounds(k * small, 256) * (6 + 0.75 * (double)((stages + 4 * k - 1) / (4 * k))) +
+                          (k > 1 ? 5 + 0.01 * (double)(k * small) : 0);
+        if (k == 1 || us < best) {
             best = us;
-            p.splits = (int)s;
+            p.splits = (int)k;
         }
     }
     if (O >= 16 && I >= 16) {
-        const int64_t mid = tiles(128), big = tiles(256);
-        const double mid_us = mid <= 256 ? 6 + 0.75 * stages : rounds(mid, 512) * (7 + 1.35 * stages);
-        const double big_us = rounds(big, 256) * (8 + 1.6 * stages);
-        if (mid_us < best) p.tile = 128, p.splits = 1, best = mid_us;
-        if (big_us < best) p.tile = 256, p.splits = 1;
+        const int64_t mid = tiles(128, 128), tall = tiles(256, 128), big = tiles(256, 256);
+        const auto offer = [&](double us, int o, int i) {
+            if (us < best) p = Plan{0, 0, o, i, 1}, best = us;
+        };
+        offer(mid <= 256 ? 6 + 0.75 * s : rounds(mid, 512) * (7 + 1.35 * s), 128, 128);
+        offer(tall <= 256 ? 8 + 1.15 * s : rounds(tall, 512) * (5.5 + 1.95 * s), 256, 128);
+        offer(rounds(big, 256) * (7.5 + 1.65 * s), 256, 256);
     }
-    p.tiles_o = (O + p.tile - 1) / p.tile;
-    p.tiles_i = (I + p.tile - 1) / p.tile;
+    p.tiles_o = (O + p.tile_o - 1) / p.tile_o;
+    p.tiles_i = (I + p.tile_i - 1) / p.tile_i;
     return p;
 }
 
@@ -681,7 +693,7 @@ tide_status tide_weight_grads_workspace(int64_t rows, int64_t out, int64_t in, i
     if (!bytes) return fail(TIDE_ERR_INVALID_ARG, "bytes is NULL");
     TIDE_TRY(check_sizes(rows, out, in, experts));
     const Plan p = plan_tiles(rows, out, in, experts);
-    *bytes = p.splits > 1 ? p.splits * experts * p.tiles_o * p.tiles_i * p.tile * p.tile * 4 : 0;
+    *bytes = p.splits > 1 ? p.splits * experts * p.tiles_o * p.tiles_i * p.tile_o * p.tile_i * 4 : 0;
     return TIDE_OK;
 }
 
@@ -777,10 +789,11 @@ tide_status tide_weight_grads_bf16(const uint16_t* dy, int64_t dy_stride, int64_
             for (int32_t e = 0; e < ne; ++e) g.p[e] = grads[e0 + e];
             a.first = e0;
             a.count = ne;
-            a.partial = (float*)workspace + (int64_t)e0 * p.splits * tiles * p.tile * p.tile;
-            const hipError_t launched = p.tile == 256   ? launch_tiles<256>(a, g, how, stream)
-                                        : p.tile == 128 ? launch_tiles<128>(a, g, how, stream)
-                                                        : launch_tiles<64>(a, g, how, stream);
+            a.partial = (float*)workspace + (int64_t)e0 * p.splits * tiles * p.tile_o * p.tile_i;
+            const hipError_t launched = p.tile_i == 256   ? launch_tiles<256, 256>(a, g, how, stream)
+                                        : p.tile_o == 256 ? launch_tiles<256, 128>(a, g, how, stream)
+                                        : p.tile_o == 128 ? launch_tiles<128, 128>(a, g, how, stream)
+                                                          : launch_tiles<64, 64>(a, g, how, stream);
             if (launched != hipSuccess) return hip_fail(launched, "weight_grads");
         }
         return TIDE_OK;

@@ -102,7 +102,8 @@ def test_many_experts(tide, T, k, E, O, I, masked, pad, saved):
 
 @pytest.mark.parametrize("saved", [False, True])
 @pytest.mark.parametrize("pad", [0, 3])
-@pytest.mark.parametrize("n,O,I", [(1, 4096, 2816), (64, 4104, 2600), (100, 2570, 4611), (333, 4160, 2592)])
+@pytest.mark.parametrize("n,O,I", [(1, 4096, 2816), (64, 4104, 2600), (100, 2570, 4611), (333, 4160, 2592),
+                                   (700, 4100, 2570), (1000, 3856, 2832)])
 def test_one_large_parameter(tide, n, O, I, pad, saved):
     """Enough tiles for the large ones, ragged at both edges."""
     say("weight_grads", n, O, I, pad, saved)
@@ -166,6 +167,13 @@ def test_accumulate(tide, E, saved):
     off = None if E == 1 else torch.tensor([0, 60, 60, 130, 200])
     check(tide, ref.normal((n, O), torch.bfloat16, seed=1), ref.normal((n, I), torch.bfloat16, seed=2), saved,
           off, None, old=ref.normal((E, O, I), torch.bfloat16, seed=3, scale=10.0))
+
+
+@pytest.mark.parametrize("pad", [0, 3])
+@pytest.mark.parametrize("n,O,I", [(100, 2570, 4611), (700, 4100, 2570), (300, 1030, 2050), (600, 520, 515)])
+def test_accumulate_in_large_tiles(tide, n, O, I, pad):
+    check(tide, ref.normal((n, O), torch.bfloat16, seed=1), ref.normal((n, I), torch.bfloat16, seed=2), True,
+          None, None, pad, old=ref.normal((1, O, I), torch.bfloat16, seed=3, scale=10.0))
 
 
 def test_lists_and_tables_of_gradients(tide):
