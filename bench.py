@@ -15,7 +15,7 @@ Prints ONE JSON line on stdout; progress goes to stderr.
 
   python bench.py [--gpus 1] [--steps K] [--warmup W] [--workload NAME]
                   [--placement-engine kernel|sdma|runtime] [--parts] [--victim] [--stock]
-                  [--slot-reuse] [--occupancy] [--graph] [--fence-study] [--offsets]
+                  [--slot-reuse] [--occupancy] [--graph] [--fence-study] [--offsets] [--layer]
                   [--no-cpu-baseline] [--no-per-config]
 """
 import argparse
@@ -725,6 +725,62 @@ def offset_rates(torch, tide, grp, offsets=(0, 1, 2, 3), reps=8):
     return res
 
 
+def layer_rates(torch, tide, tokens=4096, k=8, reps=10):
+    """The operators that run beside the collectives in one step of the
+    Qwen3-MoE layer (128 experts of 768 x 2048, 8 a token), each timed alone by
+    events on buffers of one micro-batch: microseconds, GB/s of the bytes it
+    cannot do without and, for the weight gradients, TFLOP/s."""
+    E, H, F = 128, 2048, 768
+    n, dev, bf = tokens * k, "cuda", torch.bfloat16
+    gen = torch.Generator(device=dev)
+    gen.manual_seed(0)
+    rand = lambda *s: torch.randn(*s, generator=gen, device=dev, dtype=bf)  # noqa: E731
+    empty = lambda *s, dtype=bf: torch.empty(*s, dtype=dtype, device=dev)  # noqa: E731
+    saved = lambda r, c: (empty(r, c, dtype=torch.float8_e4m3fn),  # noqa: E731
+                          empty(r, -(-c // 32), dtype=torch.float8_e8m0fnu))
+    ids = torch.topk(torch.randn(tokens, E, generator=gen, device=dev), k, 1).indices
+    weights = torch.softmax(torch.randn(tokens, k, generator=gen, device=dev), 1)
+    off, tok, slots = empty(E + 1, dtype=torch.int32), empty(n, dtype=torch.int32), empty(tokens, k, dtype=torch.int32)
+    x, dout, rows, y = rand(tokens, H), rand(tokens, H), empty(n, H), rand(n, H)
+    out, dy, dw, dx = empty(tokens, H), empty(n, H), empty(tokens, k, dtype=torch.float32), empty(tokens, H)
+    gate, up, h, dh, dg, du = rand(n, F), rand(n, F), empty(n, F), rand(n, F), empty(n, F), empty(n, F)
+    xs, gs, us = saved(tokens, H), saved(n, F), saved(n, F)
+    wg, wd = empty(E, F, H), empty(E, H, F)
+    code = lambda r, c: r * (c + c // 32)  # noqa: E731
+    calls = [
+        ("route", lambda: tide.route_tokens(ids, E, off, tok, slots), 16 * n, 0),
+        ("dispatch", lambda: tide.dispatch_tokens(x, slots, rows), 4 * n + 2 * H * (tokens + n), 0),
+        ("pack", lambda: tide.checkpoint_pack(x, xs), 2 * tokens * H + code(tokens, H), 0),
+        ("gated", lambda: tide.gated_silu(gate, up, h, gate_saved=gs, up_saved=us), 6 * n * F + 2 * code(n, F), 0),
+        ("combine", lambda: tide.combine_tokens(y, slots, out, weights=weights), 8 * n + 2 * H * (tokens + n), 0),
+        ("combine_grad", lambda: tide.combine_tokens_grad(dout, y, slots, weights, dy, dw),
+         12 * n + 2 * H * (tokens + 2 * n), 0),
+        ("gated_grad", lambda: tide.gated_silu_grad(dh, gs, us, dg, du, out=h), 8 * n * F + 2 * code(n, F), 0),
+        ("weight_grads_down", lambda: tide.weight_grads_bf16(dy, h, wd, offsets=off),
+         2 * n * (H + F) + 2 * E * H * F, 2 * n * H * F),
+        ("weight_grads_gate", lambda: tide.weight_grads_bf16(dg, xs, wg, offsets=off, token_of_row=tok),
+         2 * n * F + code(tokens, H) + 2 * E * H * F, 2 * n * H * F),
+        ("dispatch_grad", lambda: tide.combine_tokens(dy, slots, dx), 4 * n + 2 * H * (tokens + n), 0),
+    ]
+    res = {"tokens": tokens, "experts": E, "experts_a_token": k, "width": H, "expert_width": F}
+    for name, call, nbytes, flops in calls:
+        ts = []
+        for i in range(reps + 2):
+            e = [torch.cuda.Event(enable_timing=True) for _ in range(2)]
+            e[0].record()
+            call()
+            e[1].record()
+            torch.cuda.synchronize()
+            if i >= 2:
+                ts.append(e[0].elapsed_time(e[1]) * 1e-3)
+        s = statistics.median(ts)
+        res[name] = {"us_median": round(s * 1e6, 1), "GBps": round(nbytes / s / 1e9, 1)}
+        if flops:
+            res[name]["TFLOPps"] = round(flops / s / 1e12, 1)
+        log("bench: layer %s %s" % (name, json.dumps(res[name])))
+    return res
+
+
 def one_gpu_share(torch, tide, grp, reps=10):
     """The reduce one GPU of an L-GPU node runs: its N / L ranks (here ranks
     [0, N / L)), full grid, median of `reps` calls between HIP events on the
@@ -833,6 +889,9 @@ def main():
     ap.add_argument("--offsets", action="store_true",
                     help="also time the reduce with all gradients at 0-3 elements past an "
                          "allocation's start")
+    ap.add_argument("--layer", action="store_true",
+                    help="also time the token sort, the 8-bit checkpoints and the weight gradients "
+                         "of one step of the Qwen3-MoE layer")
     ap.add_argument("--no-cpu-baseline", action="store_true",
                     help="skip the oracle (timing and whole-output checks)")
     ap.add_argument("--no-per-config", action="store_true",
@@ -984,6 +1043,8 @@ def main():
         log("bench: gradient offsets")
         offs = offset_rates(torch, tide, grp)
 
+    layer = layer_rates(torch, tide) if args.layer else None
+
     fence = None
     if args.fence_study:
         fence = fence_study(torch, tide, plan, grads, out, shards, params, pair)
@@ -1069,6 +1130,8 @@ def main():
         line["fence_study"] = fence
     if offs is not None:
         line["gradient_offsets"] = offs
+    if layer is not None:
+        line["layer_operators"] = layer
     if graph is not None:
         line["prepared_and_graph"] = graph
     print(json.dumps(line), flush=True)

@@ -16,7 +16,6 @@ using namespace tide;
 namespace {
 
 typedef uint32_t u32_a1 __attribute__((aligned(1)));
-constexpr int kBlock = 32;
 
 // The largest of the kLanes (4 or 8) lanes that share a scale.
 template <int kLanes>
@@ -107,7 +106,7 @@ __device__ __forceinline__ void store_codes(uint8_t* p, int n, const Codes<V>& c
 // second look at each element.
 template <int V>
 __device__ __forceinline__ void pack_row(const Saved& s, int64_t r, int64_t u, int n, float (&v)[V]) {
-    constexpr int kLanes = kBlock / V;
+    constexpr int kLanes = kScaleBlock / V;
     uint32_t m = 0;
 #pragma unroll
     for (int i = 0; i < V; ++i) m = max(m, magnitude(v[i]));
@@ -136,7 +135,7 @@ __device__ __forceinline__ void pack_row(const Saved& s, int64_t r, int64_t u, i
 template <int V>
 __device__ __forceinline__ void unpack_row(const Saved& s, int64_t r, int64_t u, int n, float (&v)[V]) {
     const Codes<V> c = load_codes<V>(s.codes + r * s.codes_stride + u * V, n);
-    const uint32_t byte = *gbl<uint8_t>(s.scales + r * s.scales_stride + u / (kBlock / V));
+    const uint32_t byte = *gbl<uint8_t>(s.scales + r * s.scales_stride + u / (kScaleBlock / V));
 #pragma unroll
     for (int i = 0; i < V / 4; ++i) decode4(c.w[i], byte, v + 4 * i);
 }
@@ -147,7 +146,7 @@ template <int V, bool kWhole, class F>
 __device__ __forceinline__ void each_vector(int64_t n, int64_t width, int lane_log2, F&& f) {
     const int lanes = 1 << lane_log2;
     int64_t units = (width + V - 1) / V;
-    if (kWhole) units = (width + kBlock - 1) / kBlock * (kBlock / V);
+    if (kWhole) units = (width + kScaleBlock - 1) / kScaleBlock * (kScaleBlock / V);
     for (int64_t r = (int64_t)blockIdx.x * (kRowThreads >> lane_log2) + (threadIdx.x >> lane_log2);
          r < n; r += (int64_t)gridDim.x * (kRowThreads >> lane_log2)) {
         for (int64_t u = (int64_t)blockIdx.y * lanes + (threadIdx.x & (lanes - 1)); u < units;
@@ -274,13 +273,13 @@ struct Check {
         if (!s) return fail(TIDE_ERR_INVALID_ARG, "%s is NULL", name);
         const tide_status st = read(name, s->codes, r, c, s->codes_stride, 1);
         if (st != TIDE_OK) return st;
-        return read(name, s->scales, r, (c + kBlock - 1) / kBlock, s->scales_stride, 1);
+        return read(name, s->scales, r, (c + kScaleBlock - 1) / kScaleBlock, s->scales_stride, 1);
     }
     tide_status write(const char* name, const tide_saved* s, int64_t r, int64_t c) {
         if (!s) return fail(TIDE_ERR_INVALID_ARG, "%s is NULL", name);
         const tide_status st = write(name, s->codes, r, c, s->codes_stride, 1);
         if (st != TIDE_OK) return st;
-        return write(name, s->scales, r, (c + kBlock - 1) / kBlock, s->scales_stride, 1);
+        return write(name, s->scales, r, (c + kScaleBlock - 1) / kScaleBlock, s->scales_stride, 1);
     }
     tide_status done() { return no_overlap(wr, nw, rd, nr); }
 };
@@ -296,24 +295,14 @@ Saved device_of(const tide_saved* s) {
     return s ? Saved{s->codes, s->scales, s->codes_stride, s->scales_stride} : Saved{};
 }
 
-#define TIDE_TRY(expr)                        \
-    do {                                      \
-        tide_status s_ = (expr);              \
-        if (s_ != TIDE_OK) return s_;         \
-    } while (0)
-
-// Runs `launch` (grid, stream) with the stream's device current.
+// Runs launch(grid, stream) over the vectors of `rows` x `width` elements.
 template <class F>
-tide_status over_rows(int64_t n, int64_t width, int32_t size, void* stream_v, F&& launch) {
-    if (n == 0 || width == 0) return TIDE_OK;
-    hipStream_t stream = reinterpret_cast<hipStream_t>(stream_v);
-    int dev = 0;
-    TIDE_TRY(stream_device(stream, &dev));
-    DeviceGuard guard(dev);
-    if (guard.status() != hipSuccess) return hip_fail(guard.status(), "hipSetDevice");
-    launch(row_grid(n, (width * size + 15) / 16, size == 2 ? 2 : 3), stream);
-    const hipError_t e = hipGetLastError();
-    return e == hipSuccess ? TIDE_OK : hip_fail(e, "kernel launch");
+tide_status over_rows(int64_t rows, int64_t width, int32_t size, void* stream, F&& launch) {
+    if (rows == 0 || width == 0) return TIDE_OK;
+    return on_stream(stream, [&](hipStream_t s) {
+        launch(row_grid(rows, (width * size + 15) / 16, size == 2 ? 2 : 3), s);
+        return hipGetLastError();
+    });
 }
 
 }  // namespace

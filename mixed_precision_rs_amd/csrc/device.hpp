@@ -128,6 +128,8 @@ __device__ __forceinline__ u32x4 narrow(const float (&v)[4]) {
     return r;
 }
 
+constexpr int kScaleBlock = 32;        // consecutive elements of a row that share a checkpoint scale
+
 // Lanes of a 256-thread workgroup over rows of `units` vectors: 2^lane_log2
 // lanes a row, the rest of the workgroup on further rows. The grid's y
 // dimension covers a row that is wider than its lanes; both dimensions are

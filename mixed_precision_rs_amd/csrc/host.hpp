@@ -20,6 +20,12 @@ tide_status hip_fail(hipError_t e, const char* what);
         if (e_ != hipSuccess) return hip_fail(e_, #expr);       \
     } while (0)
 
+#define TIDE_TRY(expr)                        \
+    do {                                      \
+        tide_status s_ = (expr);              \
+        if (s_ != TIDE_OK) return s_;         \
+    } while (0)
+
 // Makes `dev` the current device for the guard's lifetime. Allocations,
 // events and kernel attributes belong to the current device, and a caller's
 // stream may sit on another one.
@@ -65,5 +71,18 @@ tide_status matrix(const char* name, const void* p, int64_t rows, int64_t cols, 
 // the nr read or with another one written. Rows of one stride that interleave
 // (column windows of a wider matrix) do not share memory.
 tide_status no_overlap(const Mat* written, int nw, const Mat* read, int nr);
+
+// Runs launch(stream), which returns a hipError_t, with the stream's device
+// current.
+template <class F>
+tide_status on_stream(void* stream_v, F&& launch) {
+    hipStream_t stream = reinterpret_cast<hipStream_t>(stream_v);
+    int dev = 0;
+    TIDE_TRY(stream_device(stream, &dev));
+    DeviceGuard guard(dev);
+    if (guard.status() != hipSuccess) return hip_fail(guard.status(), "hipSetDevice");
+    const hipError_t e = launch(stream);
+    return e == hipSuccess ? TIDE_OK : hip_fail(e, "kernel launch");
+}
 
 }  // namespace tide

@@ -331,24 +331,6 @@ tide_status check_sort(int32_t dtype, int64_t T, int32_t k, int64_t nrows) {
     return TIDE_OK;
 }
 
-#define TIDE_TRY(expr)                        \
-    do {                                      \
-        tide_status s_ = (expr);              \
-        if (s_ != TIDE_OK) return s_;         \
-    } while (0)
-
-// Runs `launch` (a hipError_t) with the stream's device current.
-template <class F>
-tide_status on_stream(void* stream_v, F&& launch) {
-    hipStream_t stream = reinterpret_cast<hipStream_t>(stream_v);
-    int dev = 0;
-    TIDE_TRY(stream_device(stream, &dev));
-    DeviceGuard guard(dev);
-    if (guard.status() != hipSuccess) return hip_fail(guard.status(), "hipSetDevice");
-    const hipError_t e = launch(stream);
-    return e == hipSuccess ? TIDE_OK : hip_fail(e, "kernel launch");
-}
-
 }  // namespace
 
 extern "C" {

@@ -15,7 +15,6 @@ using namespace tide;
 namespace {
 
 typedef uint32_t u32x2_a2 __attribute__((ext_vector_type(2), aligned(2)));
-constexpr int kBlock = 32;             // elements that share a scale
 constexpr int kMaxGrads = 256;         // gradient pointers in one launch's arguments
 constexpr int64_t kMaxGroups = 1 << 23;   // workgroups of a launch (2^32 work-items a dimension)
 struct GradPtrs {
@@ -220,7 +219,7 @@ struct Tile {
                 m.i[j] = buffer16(x, out | (row * stride + (uint32_t)col * (kSaved ? 1 : 2)));
                 if constexpr (kSaved)
                     m.s[j] = __builtin_amdgcn_raw_buffer_load_b8(
-                        s, (int)(out | (row * (uint32_t)a.scales_stride + (uint32_t)col / kBlock)), 0, 0);
+                        s, (int)(out | (row * (uint32_t)a.scales_stride + (uint32_t)col / kScaleBlock)), 0, 0);
             }
         } else if constexpr (kAccess == kVectors) {
             const int64_t last = hi - 1;
@@ -241,7 +240,7 @@ struct Tile {
                 row = in ? row : 0;
                 if constexpr (kSaved) {
                     m.i[j] = *gbl<u32x4_a1>(a.codes + row * a.codes_stride + ci);
-                    m.s[j] = *gbl<uint8_t>(a.scales + row * a.scales_stride + min(col, a.I - 1) / kBlock);
+                    m.s[j] = *gbl<uint8_t>(a.scales + row * a.scales_stride + min(col, a.I - 1) / kScaleBlock);
                 } else {
                     m.i[j] = *gbl<u32x4_a2>(a.x + row * a.x_stride + ci);
                 }
@@ -265,7 +264,7 @@ struct Tile {
                 if (n > 0 && row >= 0 && row < a.x_rows) {
                     if constexpr (kSaved) {
                         m.i[j] = codes16(a.codes + row * a.codes_stride + col, (int)(n < 16 ? n : 16));
-                        m.s[j] = *gbl<uint8_t>(a.scales + row * a.scales_stride + col / kBlock);
+                        m.s[j] = *gbl<uint8_t>(a.scales + row * a.scales_stride + col / kScaleBlock);
                     } else {
                         m.i[j] = load_row(a.x + row * a.x_stride + col, (int)(n < 8 ? n : 8));
                     }
@@ -616,12 +615,6 @@ Access how_to_read(const Args& a) {
     return kVectors;
 }
 
-#define TIDE_TRY(expr)                        \
-    do {                                      \
-        tide_status s_ = (expr);              \
-        if (s_ != TIDE_OK) return s_;         \
-    } while (0)
-
 // Tile and splits. A large tile reuses each staged element more (1200, 1080,
 // 870 and 410 TFLOP/s on long sums, in tiles of 256 x 256, 256 x 128, 128 x 128
 // and 64 x 64), a small one leaves fewer CUs idle and, with its teams, waits
@@ -702,7 +695,7 @@ tide_status tide_weight_grads_bf16(const uint16_t* dy, int64_t dy_stride, int64_
                                    const tide_saved* saved, int64_t x_rows, int64_t in,
                                    const int32_t* offsets, const int32_t* token_of_row,
                                    int32_t experts, uint16_t* const* grads, int32_t accumulate,
-                                   void* workspace, int64_t workspace_bytes, void* stream_v) {
+                                   void* workspace, int64_t workspace_bytes, void* stream) {
     try {
         int64_t need = 0;
         TIDE_TRY(tide_weight_grads_workspace(rows, out, in, experts, &need));
@@ -722,7 +715,7 @@ tide_status tide_weight_grads_bf16(const uint16_t* dy, int64_t dy_stride, int64_
         TIDE_TRY(matrix("dy", dy, rows, out, dy_stride, 2, &rd[0]));
         if (saved) {
             TIDE_TRY(matrix("saved", saved->codes, x_rows, in, saved->codes_stride, 1, &rd[1]));
-            TIDE_TRY(matrix("saved", saved->scales, x_rows, (in + kBlock - 1) / kBlock,
+            TIDE_TRY(matrix("saved", saved->scales, x_rows, (in + kScaleBlock - 1) / kScaleBlock,
                             saved->scales_stride, 1, &rd[2]));
         } else {
             TIDE_TRY(matrix("x", x, x_rows, in, x_stride, 2, &rd[1]));
@@ -750,11 +743,6 @@ tide_status tide_weight_grads_bf16(const uint16_t* dy, int64_t dy_stride, int64_
         for (int32_t e = 1; e < experts; ++e)
             if (at[e] - at[e - 1] < bytes)
                 return fail(TIDE_ERR_INVALID_ARG, "two of the grads overlap");
-        hipStream_t stream = reinterpret_cast<hipStream_t>(stream_v);
-        int dev = 0;
-        TIDE_TRY(stream_device(stream, &dev));
-        DeviceGuard guard(dev);
-        if (guard.status() != hipSuccess) return hip_fail(guard.status(), "hipSetDevice");
         Args a{};
         a.dy = dy;
         a.x = x;
@@ -783,20 +771,22 @@ tide_status tide_weight_grads_bf16(const uint16_t* dy, int64_t dy_stride, int64_
         a.tiles_i = (int32_t)p.tiles_i;
         a.splits = p.splits;
         const int32_t most = (int32_t)std::min<int64_t>(kMaxGrads, kMaxGroups / (tiles * p.splits));
-        for (int32_t e0 = 0; e0 < experts; e0 += most) {
-            const int32_t ne = std::min(experts - e0, most);
-            GradPtrs g{};
-            for (int32_t e = 0; e < ne; ++e) g.p[e] = grads[e0 + e];
-            a.first = e0;
-            a.count = ne;
-            a.partial = (float*)workspace + (int64_t)e0 * p.splits * tiles * p.tile_o * p.tile_i;
-            const hipError_t launched = p.tile_i == 256   ? launch_tiles<256, 256>(a, g, how, stream)
-                                        : p.tile_o == 256 ? launch_tiles<256, 128>(a, g, how, stream)
-                                        : p.tile_o == 128 ? launch_tiles<128, 128>(a, g, how, stream)
-                                                          : launch_tiles<64, 64>(a, g, how, stream);
-            if (launched != hipSuccess) return hip_fail(launched, "weight_grads");
-        }
-        return TIDE_OK;
+        return on_stream(stream, [&](hipStream_t s) {
+            for (int32_t e0 = 0; e0 < experts; e0 += most) {
+                const int32_t ne = std::min(experts - e0, most);
+                GradPtrs g{};
+                for (int32_t e = 0; e < ne; ++e) g.p[e] = grads[e0 + e];
+                a.first = e0;
+                a.count = ne;
+                a.partial = (float*)workspace + (int64_t)e0 * p.splits * tiles * p.tile_o * p.tile_i;
+                const hipError_t launched = p.tile_i == 256   ? launch_tiles<256, 256>(a, g, how, s)
+                                            : p.tile_o == 256 ? launch_tiles<256, 128>(a, g, how, s)
+                                            : p.tile_o == 128 ? launch_tiles<128, 128>(a, g, how, s)
+                                                              : launch_tiles<64, 64>(a, g, how, s);
+                if (launched != hipSuccess) return launched;
+            }
+            return hipSuccess;
+        });
     } catch (const std::bad_alloc&) {
         return fail(TIDE_ERR_NO_MEMORY, "host allocation failed");
     } catch (...) {
