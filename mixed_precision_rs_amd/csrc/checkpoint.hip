@@ -16,6 +16,7 @@ using namespace tide;
 namespace {
 
 typedef uint32_t u32_a1 __attribute__((aligned(1)));
+typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
 
 // The largest of the kLanes (4 or 8) lanes that share a scale.
 template <int kLanes>
@@ -99,18 +100,42 @@ __device__ __forceinline__ void store_codes(uint8_t* p, int n, const Codes<V>& c
     }
 }
 
-// Packs this lane's values (n of them in the row; lanes past the row have n <=
-// 0 and zeros, and take part in the maximum all the same). Magnitudes are
-// compared as integers, in which infinities and NaN are the largest: only a
-// block with one of them, or with a value past the largest scale, takes a
-// second look at each element.
-template <int V>
-__device__ __forceinline__ void pack_row(const Saved& s, int64_t r, int64_t u, int n, float (&v)[V]) {
-    constexpr int kLanes = kScaleBlock / V;
+// Largest magnitude of a lane's vector, as fp32 bits.
+__device__ __forceinline__ uint32_t largest(u32x4 raw, const uint16_t*) {
+    u16x2 m = {0, 0};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) m = __builtin_elementwise_max(m, __builtin_bit_cast(u16x2, raw[i] & 0x7FFF7FFFu));
+    return (uint32_t)max(m[0], m[1]) << 16;
+}
+__device__ __forceinline__ uint32_t largest(u32x4 raw, const float*) {
     uint32_t m = 0;
 #pragma unroll
-    for (int i = 0; i < V; ++i) m = max(m, magnitude(v[i]));
-    m = block_max<kLanes>(m);
+    for (int i = 0; i < 4; ++i) m = max(m, raw[i] & 0x7FFFFFFFu);
+    return m;
+}
+
+// A lane's vector as codes: x / 2^e to nearest even; the division is exact.
+template <int V>
+__device__ __forceinline__ Codes<V> encode(const float (&v)[V], uint32_t byte) {
+    const float inv = scale_of(254 - byte);
+    Codes<V> c;
+#pragma unroll
+    for (int i = 0; i < V / 4; ++i)
+        c.w[i] = encode4(v[4 * i] * inv, v[4 * i + 1] * inv, v[4 * i + 2] * inv, v[4 * i + 3] * inv);
+    return c;
+}
+
+// Packs this lane's vector (n elements of it in the row; lanes past the row
+// have n <= 0 and zeros, and take part in the maximum all the same).
+// Magnitudes are compared as integers, in which infinities and NaN are the
+// largest: only a block with one of them, or with a value past the largest
+// scale, takes a second look at each element.
+template <class T>
+__device__ __forceinline__ void pack_row(const Saved& s, int64_t r, int64_t u, int n, u32x4 raw) {
+    constexpr int V = kVecOf<T>, kLanes = kScaleBlock / V;
+    uint32_t m = block_max<kLanes>(largest(raw, (const T*)nullptr));
+    float v[V];
+    widen(raw, v);
     if (m > kLargest) {
         m = 0;
 #pragma unroll
@@ -123,12 +148,7 @@ __device__ __forceinline__ void pack_row(const Saved& s, int64_t r, int64_t u, i
     }
     const uint32_t byte = scale_byte(m);
     if (n <= 0) return;
-    const float inv = scale_of(254 - byte);
-    Codes<V> c;
-#pragma unroll
-    for (int i = 0; i < V / 4; ++i)
-        c.w[i] = encode4(v[4 * i] * inv, v[4 * i + 1] * inv, v[4 * i + 2] * inv, v[4 * i + 3] * inv);
-    store_codes<V>(s.codes + r * s.codes_stride + u * V, n, c);
+    store_codes<V>(s.codes + r * s.codes_stride + u * V, n, encode<V>(v, byte));
     if ((u & (kLanes - 1)) == 0)
         *gbl_mut<uint8_t>(s.scales + r * s.scales_stride + u / kLanes) = (uint8_t)byte;
 }
@@ -162,9 +182,9 @@ __global__ __launch_bounds__(kRowThreads) void pack_rows(const T* x, int64_t x_s
                                                          int64_t width, Saved to, int lane_log2) {
     constexpr int V = kVecOf<T>;
     each_vector<V, true>(n, width, lane_log2, [&](int64_t r, int64_t u, int left) {
-        float v[V] = {};
-        if (left > 0) widen(load_row(x + r * x_stride + u * V, left), v);
-        pack_row<V>(to, r, u, left, v);
+        u32x4 v{};
+        if (left > 0) v = load_row(x + r * x_stride + u * V, left);
+        pack_row<T>(to, r, u, left, v);
     });
 }
 
@@ -181,13 +201,15 @@ __global__ __launch_bounds__(kRowThreads) void unpack_rows(Saved from, int64_t n
 }
 
 // sigmoid(g) and sigmoid(-g), neither by a difference that cancels: with e =
-// exp(-|g|) they are 1 / (1 + e) and e / (1 + e). e = 2^p, p = -|g| log2(e) in
-// two floats (the rounding of one alone would be off by |g| 2^-24 of e), past
-// the range of normal results taken 2^64 too large and brought back; the
-// reciprocal is refined once. 20 instructions instead of 45 of the library's
-// expf and division, which bounded the forward pass (210 -> GATED us at 4096 x
-// 28672).
+// exp(-|g|) they are 1 / (1 + e) and e / (1 + e). e = 2^p, p = -|g| log2(e),
+// past the range of normal results taken 2^64 too large and brought back. For
+// fp32 results p has a second float (one alone is off by |g| 2^-24 of e) and
+// the reciprocal is refined once; a bf16 result hides both. 14 and 20
+// instructions instead of 45 of the library's expf and division, which bounded
+// the forward pass.
+template <class T>
 __device__ __forceinline__ void sigmoids(float g, float& s, float& c) {
+    constexpr bool kFull = sizeof(T) == 4;
     const float a = fmaxf(-fabsf(g), -200.0f);     // exp(-200) is 0; a NaN comes back with the factor g
     const float kLog2e = 0x1.715476p+0f, kRest = 0x1.4ae0cp-26f;
     float p = a * kLog2e;
@@ -195,11 +217,11 @@ __device__ __forceinline__ void sigmoids(float g, float& s, float& c) {
     const bool far = p < -120.0f;
     p = far ? p + 64.0f : p;
     float e = __builtin_amdgcn_exp2f(p);
-    e = __builtin_fmaf(e, rest * 0x1.62e43p-1f, e);
+    if (kFull) e = __builtin_fmaf(e, rest * 0x1.62e43p-1f, e);
     e = far ? e * 0x1p-64f : e;
     const float d = 1.0f + e;
     float big = __builtin_amdgcn_rcpf(d);
-    big = __builtin_fmaf(__builtin_fmaf(-d, big, 1.0f), big, big);
+    if (kFull) big = __builtin_fmaf(__builtin_fmaf(-d, big, 1.0f), big, big);
     const float small = e * big;
     s = g >= 0.0f ? big : small;
     c = g >= 0.0f ? small : big;
@@ -213,22 +235,23 @@ __global__ __launch_bounds__(kRowThreads) void gated_rows(const T* gate, int64_t
                                                           Saved up_to, int lane_log2) {
     constexpr int V = kVecOf<T>;
     each_vector<V, true>(n, width, lane_log2, [&](int64_t r, int64_t u, int left) {
-        float g[V] = {}, v[V] = {}, h[V];
+        u32x4 a{}, b{};
         if (left > 0) {
-            const u32x4 a = load_row(gate + r * gate_stride + u * V, left);
-            const u32x4 b = load_row(up + r * up_stride + u * V, left);
+            a = load_row(gate + r * gate_stride + u * V, left);
+            b = load_row(up + r * up_stride + u * V, left);
+            float g[V], v[V], h[V];
             widen(a, g);
             widen(b, v);
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 float s, c;
-                sigmoids(g[i], s, c);
+                sigmoids<T>(g[i], s, c);
                 h[i] = g[i] * s * v[i];
             }
             store_row(out + r * out_stride + u * V, left, narrow(h));
         }
-        if (gate_to.codes) pack_row<V>(gate_to, r, u, left, g);
-        if (up_to.codes) pack_row<V>(up_to, r, u, left, v);
+        if (gate_to.codes) pack_row<T>(gate_to, r, u, left, a);
+        if (up_to.codes) pack_row<T>(up_to, r, u, left, b);
     });
 }
 
@@ -248,7 +271,7 @@ __global__ __launch_bounds__(kRowThreads) void gated_rows_grad(const T* dout, in
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             float s, c;
-            sigmoids(g[i], s, c);
+            sigmoids<T>(g[i], s, c);
             const float t = g[i] * s;
             dg[i] = d[i] * v[i] * __builtin_fmaf(t, c, s);
             du[i] = d[i] * t;
