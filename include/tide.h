@@ -511,8 +511,9 @@ tide_status tide_plan_event_count(const tide_plan* plan, int64_t* events);
  *     share memory with another argument; column windows of one wider matrix
  *     (equal strides) do not share memory. Nothing between a row's end and the
  *     next row is read or written.
- *   - They launch kernels and nothing else (no allocation, no copy, no wait),
- *     keep nothing between calls, and may be captured into a graph. Two calls
+ *   - They launch kernels on `stream` and nothing else (no device allocation,
+ *     no copy, no wait), keep nothing between calls, and may be captured into a
+ *     graph. Their stores are non-temporal. Two calls
  *     that may run at once need a workspace each.
  *   - Results do not depend on the order in which workgroups run: the same
  *     inputs give the same bits.
@@ -650,8 +651,8 @@ tide_status tide_weight_grads_workspace(int64_t rows, int64_t out, int64_t in, i
  * dy[r]^T x[token_of_row[r]], products of bf16 values added in fp32, rounded
  * once.
  *   dy:      rows x out bf16.
- *   x/saved: exactly one: x_rows x in bf16, or a checkpoint of such a matrix,
- *            whose values are exact in bf16.
+ *   x/saved: one of them: x_rows x in bf16, or a checkpoint of such a matrix
+ *            (tide_checkpoint_pack's), whose values are exact in bf16.
  *   offsets: experts + 1 device entries as tide_route_tokens writes them; NULL
  *            (with experts = 1): one expert has all the rows. Rows outside are
  *            not read into any sum. An expert without rows gets zeros.
@@ -661,6 +662,8 @@ tide_status tide_weight_grads_workspace(int64_t rows, int64_t out, int64_t in, i
  *   grads:   host array of `experts` device pointers, read during the call.
  *   accumulate: not 0: the sum is added to what grads holds, in fp32, before
  *            the rounding.
+ *   workspace: tide_weight_grads_workspace bytes, 16-byte aligned (may be NULL
+ *            when that is 0); what it holds does not matter.
  * Errors: INVALID_ARG, ALIGNMENT, OVERFLOW, UNSUPPORTED (a size past 2^31 - 1,
  * or too many tiles for one launch), NO_MEMORY, HIP.
  */

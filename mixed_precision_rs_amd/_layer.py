@@ -158,7 +158,9 @@ def _workspace(need: int, workspace, stream, dev):
     if stream is None:
         w = torch.empty(need, dtype=torch.uint8, device=dev)
     else:
-        s = torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream
+        s = stream
+        if isinstance(stream, int):
+            s = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
         with torch.cuda.stream(s):
             w = torch.empty(need, dtype=torch.uint8, device=s.device)
     return w.data_ptr(), need, w

@@ -334,37 +334,41 @@ extern "C" {
 
 tide_status tide_checkpoint_pack(int32_t dtype, const void* x, int64_t x_stride, int64_t rows,
                                  int64_t width, const tide_saved* saved, void* stream) {
-    TIDE_TRY(check_type(dtype, rows, width));
-    const int32_t size = dtype == TIDE_DTYPE_FP32 ? 4 : 2;
-    Check c;
-    TIDE_TRY(c.read("x", x, rows, width, x_stride, size));
-    TIDE_TRY(c.write("saved", saved, rows, width));
-    TIDE_TRY(c.done());
-    return over_rows(rows, width, size, stream, [&](RowGrid g, hipStream_t s) {
-        if (size == 2)
-            pack_rows<uint16_t><<<g.grid, dim3(kRowThreads), 0, s>>>(
-                (const uint16_t*)x, x_stride, rows, width, device_of(saved), g.lane_log2);
-        else
-            pack_rows<float><<<g.grid, dim3(kRowThreads), 0, s>>>(
-                (const float*)x, x_stride, rows, width, device_of(saved), g.lane_log2);
+    return guarded([&]() -> tide_status {
+        TIDE_TRY(check_type(dtype, rows, width));
+        const int32_t size = dtype == TIDE_DTYPE_FP32 ? 4 : 2;
+        Check c;
+        TIDE_TRY(c.read("x", x, rows, width, x_stride, size));
+        TIDE_TRY(c.write("saved", saved, rows, width));
+        TIDE_TRY(c.done());
+        return over_rows(rows, width, size, stream, [&](RowGrid g, hipStream_t s) {
+            if (size == 2)
+                pack_rows<uint16_t><<<g.grid, dim3(kRowThreads), 0, s>>>(
+                    (const uint16_t*)x, x_stride, rows, width, device_of(saved), g.lane_log2);
+            else
+                pack_rows<float><<<g.grid, dim3(kRowThreads), 0, s>>>(
+                    (const float*)x, x_stride, rows, width, device_of(saved), g.lane_log2);
+        });
     });
 }
 
 tide_status tide_checkpoint_unpack(int32_t dtype, const tide_saved* saved, int64_t rows,
                                    int64_t width, void* out, int64_t out_stride, void* stream) {
-    TIDE_TRY(check_type(dtype, rows, width));
-    const int32_t size = dtype == TIDE_DTYPE_FP32 ? 4 : 2;
-    Check c;
-    TIDE_TRY(c.read("saved", saved, rows, width));
-    TIDE_TRY(c.write("out", out, rows, width, out_stride, size));
-    TIDE_TRY(c.done());
-    return over_rows(rows, width, size, stream, [&](RowGrid g, hipStream_t s) {
-        if (size == 2)
-            unpack_rows<uint16_t><<<g.grid, dim3(kRowThreads), 0, s>>>(
-                device_of(saved), rows, width, (uint16_t*)out, out_stride, g.lane_log2);
-        else
-            unpack_rows<float><<<g.grid, dim3(kRowThreads), 0, s>>>(
-                device_of(saved), rows, width, (float*)out, out_stride, g.lane_log2);
+    return guarded([&]() -> tide_status {
+        TIDE_TRY(check_type(dtype, rows, width));
+        const int32_t size = dtype == TIDE_DTYPE_FP32 ? 4 : 2;
+        Check c;
+        TIDE_TRY(c.read("saved", saved, rows, width));
+        TIDE_TRY(c.write("out", out, rows, width, out_stride, size));
+        TIDE_TRY(c.done());
+        return over_rows(rows, width, size, stream, [&](RowGrid g, hipStream_t s) {
+            if (size == 2)
+                unpack_rows<uint16_t><<<g.grid, dim3(kRowThreads), 0, s>>>(
+                    device_of(saved), rows, width, (uint16_t*)out, out_stride, g.lane_log2);
+            else
+                unpack_rows<float><<<g.grid, dim3(kRowThreads), 0, s>>>(
+                    device_of(saved), rows, width, (float*)out, out_stride, g.lane_log2);
+        });
     });
 }
 
@@ -372,25 +376,27 @@ tide_status tide_gated_silu(int32_t dtype, const void* gate, int64_t gate_stride
                             int64_t up_stride, int64_t rows, int64_t width, void* out,
                             int64_t out_stride, const tide_saved* gate_saved,
                             const tide_saved* up_saved, void* stream) {
-    TIDE_TRY(check_type(dtype, rows, width));
-    const int32_t size = dtype == TIDE_DTYPE_FP32 ? 4 : 2;
-    Check c;
-    TIDE_TRY(c.read("gate", gate, rows, width, gate_stride, size));
-    TIDE_TRY(c.read("up", up, rows, width, up_stride, size));
-    TIDE_TRY(c.write("out", out, rows, width, out_stride, size));
-    if (gate_saved) TIDE_TRY(c.write("gate_saved", gate_saved, rows, width));
-    if (up_saved) TIDE_TRY(c.write("up_saved", up_saved, rows, width));
-    TIDE_TRY(c.done());
-    return over_rows(rows, width, size, stream, [&](RowGrid g, hipStream_t s) {
-        if (size == 2)
-            gated_rows<uint16_t><<<g.grid, dim3(kRowThreads), 0, s>>>(
-                (const uint16_t*)gate, gate_stride, (const uint16_t*)up, up_stride, rows, width,
-                (uint16_t*)out, out_stride, device_of(gate_saved), device_of(up_saved),
-                g.lane_log2);
-        else
-            gated_rows<float><<<g.grid, dim3(kRowThreads), 0, s>>>(
-                (const float*)gate, gate_stride, (const float*)up, up_stride, rows, width,
-                (float*)out, out_stride, device_of(gate_saved), device_of(up_saved), g.lane_log2);
+    return guarded([&]() -> tide_status {
+        TIDE_TRY(check_type(dtype, rows, width));
+        const int32_t size = dtype == TIDE_DTYPE_FP32 ? 4 : 2;
+        Check c;
+        TIDE_TRY(c.read("gate", gate, rows, width, gate_stride, size));
+        TIDE_TRY(c.read("up", up, rows, width, up_stride, size));
+        TIDE_TRY(c.write("out", out, rows, width, out_stride, size));
+        if (gate_saved) TIDE_TRY(c.write("gate_saved", gate_saved, rows, width));
+        if (up_saved) TIDE_TRY(c.write("up_saved", up_saved, rows, width));
+        TIDE_TRY(c.done());
+        return over_rows(rows, width, size, stream, [&](RowGrid g, hipStream_t s) {
+            if (size == 2)
+                gated_rows<uint16_t><<<g.grid, dim3(kRowThreads), 0, s>>>(
+                    (const uint16_t*)gate, gate_stride, (const uint16_t*)up, up_stride, rows, width,
+                    (uint16_t*)out, out_stride, device_of(gate_saved), device_of(up_saved),
+                    g.lane_log2);
+            else
+                gated_rows<float><<<g.grid, dim3(kRowThreads), 0, s>>>(
+                    (const float*)gate, gate_stride, (const float*)up, up_stride, rows, width,
+                    (float*)out, out_stride, device_of(gate_saved), device_of(up_saved), g.lane_log2);
+        });
     });
 }
 
@@ -399,27 +405,29 @@ tide_status tide_gated_silu_grad(int32_t dtype, const void* dout, int64_t dout_s
                                  int64_t rows, int64_t width, void* dgate, int64_t dgate_stride,
                                  void* dup, int64_t dup_stride, void* out, int64_t out_stride,
                                  void* stream) {
-    TIDE_TRY(check_type(dtype, rows, width));
-    const int32_t size = dtype == TIDE_DTYPE_FP32 ? 4 : 2;
-    Check c;
-    TIDE_TRY(c.read("dout", dout, rows, width, dout_stride, size));
-    TIDE_TRY(c.read("gate_saved", gate_saved, rows, width));
-    TIDE_TRY(c.read("up_saved", up_saved, rows, width));
-    TIDE_TRY(c.write("dgate", dgate, rows, width, dgate_stride, size));
-    TIDE_TRY(c.write("dup", dup, rows, width, dup_stride, size));
-    TIDE_TRY(c.write("out", out, out ? rows : 0, width, out_stride, size));
-    TIDE_TRY(c.done());
-    return over_rows(rows, width, size, stream, [&](RowGrid g, hipStream_t s) {
-        if (size == 2)
-            gated_rows_grad<uint16_t><<<g.grid, dim3(kRowThreads), 0, s>>>(
-                (const uint16_t*)dout, dout_stride, device_of(gate_saved), device_of(up_saved),
-                rows, width, (uint16_t*)dgate, dgate_stride, (uint16_t*)dup, dup_stride,
-                (uint16_t*)out, out_stride, g.lane_log2);
-        else
-            gated_rows_grad<float><<<g.grid, dim3(kRowThreads), 0, s>>>(
-                (const float*)dout, dout_stride, device_of(gate_saved), device_of(up_saved), rows,
-                width, (float*)dgate, dgate_stride, (float*)dup, dup_stride, (float*)out,
-                out_stride, g.lane_log2);
+    return guarded([&]() -> tide_status {
+        TIDE_TRY(check_type(dtype, rows, width));
+        const int32_t size = dtype == TIDE_DTYPE_FP32 ? 4 : 2;
+        Check c;
+        TIDE_TRY(c.read("dout", dout, rows, width, dout_stride, size));
+        TIDE_TRY(c.read("gate_saved", gate_saved, rows, width));
+        TIDE_TRY(c.read("up_saved", up_saved, rows, width));
+        TIDE_TRY(c.write("dgate", dgate, rows, width, dgate_stride, size));
+        TIDE_TRY(c.write("dup", dup, rows, width, dup_stride, size));
+        TIDE_TRY(c.write("out", out, out ? rows : 0, width, out_stride, size));
+        TIDE_TRY(c.done());
+        return over_rows(rows, width, size, stream, [&](RowGrid g, hipStream_t s) {
+            if (size == 2)
+                gated_rows_grad<uint16_t><<<g.grid, dim3(kRowThreads), 0, s>>>(
+                    (const uint16_t*)dout, dout_stride, device_of(gate_saved), device_of(up_saved),
+                    rows, width, (uint16_t*)dgate, dgate_stride, (uint16_t*)dup, dup_stride,
+                    (uint16_t*)out, out_stride, g.lane_log2);
+            else
+                gated_rows_grad<float><<<g.grid, dim3(kRowThreads), 0, s>>>(
+                    (const float*)dout, dout_stride, device_of(gate_saved), device_of(up_saved), rows,
+                    width, (float*)dgate, dgate_stride, (float*)dup, dup_stride, (float*)out,
+                    out_stride, g.lane_log2);
+        });
     });
 }
 

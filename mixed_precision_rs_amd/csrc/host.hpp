@@ -6,6 +6,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <new>
+
 #include "tide.h"
 
 namespace tide {
@@ -71,6 +73,18 @@ tide_status matrix(const char* name, const void* p, int64_t rows, int64_t cols, 
 // the nr read or with another one written. Rows of one stride that interleave
 // (column windows of a wider matrix) do not share memory.
 tide_status no_overlap(const Mat* written, int nw, const Mat* read, int nr);
+
+// Runs the body of a C entry point; no exception leaves it.
+template <class F>
+tide_status guarded(F&& body) {
+    try {
+        return body();
+    } catch (const std::bad_alloc&) {
+        return fail(TIDE_ERR_NO_MEMORY, "host allocation failed");
+    } catch (...) {
+        return fail(TIDE_ERR_INVALID_ARG, "unexpected exception");
+    }
+}
 
 // Runs launch(stream), which returns a hipError_t, with the stream's device
 // current.

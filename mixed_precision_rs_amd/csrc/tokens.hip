@@ -336,61 +336,67 @@ tide_status check_sort(int32_t dtype, int64_t T, int32_t k, int64_t nrows) {
 extern "C" {
 
 tide_status tide_route_workspace(int64_t tokens, int32_t k, int32_t experts, int64_t* bytes) {
-    if (!bytes) return fail(TIDE_ERR_INVALID_ARG, "bytes is NULL");
-    TIDE_TRY(check_sort(TIDE_DTYPE_BF16, tokens, k, 0));
-    if (experts < 1) return fail(TIDE_ERR_INVALID_ARG, "need experts >= 1");
-    if (experts > kMaxExperts)
-        return fail(TIDE_ERR_UNSUPPORTED, "%d experts: at most %d", experts, kMaxExperts);
-    const int64_t nb = route_blocks(tokens * k);
-    *bytes = nb > 1 ? nb * experts * 4 : 0;
-    return TIDE_OK;
+    return guarded([&]() -> tide_status {
+        if (!bytes) return fail(TIDE_ERR_INVALID_ARG, "bytes is NULL");
+        TIDE_TRY(check_sort(TIDE_DTYPE_BF16, tokens, k, 0));
+        if (experts < 1) return fail(TIDE_ERR_INVALID_ARG, "need experts >= 1");
+        if (experts > kMaxExperts)
+            return fail(TIDE_ERR_UNSUPPORTED, "%d experts: at most %d", experts, kMaxExperts);
+        const int64_t nb = route_blocks(tokens * k);
+        *bytes = nb > 1 ? nb * experts * 4 : 0;
+        return TIDE_OK;
+    });
 }
 
 tide_status tide_route_tokens(const void* experts_of, int32_t id_bytes, int64_t tokens, int32_t k,
                               int32_t experts, int32_t* offsets, int32_t* token_of_row,
                               int32_t* slots, void* workspace, int64_t workspace_bytes,
                               void* stream) {
-    int64_t need = 0;
-    TIDE_TRY(tide_route_workspace(tokens, k, experts, &need));
-    if (id_bytes != 4 && id_bytes != 8)
-        return fail(TIDE_ERR_INVALID_ARG, "expert ids have 4 or 8 bytes, not %d", id_bytes);
-    if (need > 0 && (!workspace || workspace_bytes < need))
-        return fail(TIDE_ERR_INVALID_ARG, "workspace holds %lld bytes, %lld needed",
-                    (long long)(workspace ? workspace_bytes : 0), (long long)need);
-    const int64_t n = tokens * k;
-    Mat in, wr[4];
-    TIDE_TRY(matrix("experts_of", experts_of, 1, n, n, id_bytes, &in));
-    TIDE_TRY(matrix("offsets", offsets, 1, experts + 1, experts + 1, 4, &wr[0]));
-    TIDE_TRY(matrix("token_of_row", token_of_row, 1, n, n, 4, &wr[1]));
-    TIDE_TRY(matrix("slots", slots, 1, n, n, 4, &wr[2]));
-    TIDE_TRY(matrix("workspace", workspace, 1, need / 4, need / 4, 4, &wr[3]));
-    TIDE_TRY(no_overlap(wr, 4, &in, 1));
-    return on_stream(stream, [&](hipStream_t s) {
-        return id_bytes == 4 ? launch_route<int32_t>(experts_of, n, k, experts, offsets,
-                                                     token_of_row, slots, (int32_t*)workspace, s)
-                             : launch_route<int64_t>(experts_of, n, k, experts, offsets,
-                                                     token_of_row, slots, (int32_t*)workspace, s);
+    return guarded([&]() -> tide_status {
+        int64_t need = 0;
+        TIDE_TRY(tide_route_workspace(tokens, k, experts, &need));
+        if (id_bytes != 4 && id_bytes != 8)
+            return fail(TIDE_ERR_INVALID_ARG, "expert ids have 4 or 8 bytes, not %d", id_bytes);
+        if (need > 0 && (!workspace || workspace_bytes < need))
+            return fail(TIDE_ERR_INVALID_ARG, "workspace holds %lld bytes, %lld needed",
+                        (long long)(workspace ? workspace_bytes : 0), (long long)need);
+        const int64_t n = tokens * k;
+        Mat in, wr[4];
+        TIDE_TRY(matrix("experts_of", experts_of, 1, n, n, id_bytes, &in));
+        TIDE_TRY(matrix("offsets", offsets, 1, experts + 1, experts + 1, 4, &wr[0]));
+        TIDE_TRY(matrix("token_of_row", token_of_row, 1, n, n, 4, &wr[1]));
+        TIDE_TRY(matrix("slots", slots, 1, n, n, 4, &wr[2]));
+        TIDE_TRY(matrix("workspace", workspace, 1, need / 4, need / 4, 4, &wr[3]));
+        TIDE_TRY(no_overlap(wr, 4, &in, 1));
+        return on_stream(stream, [&](hipStream_t s) {
+            return id_bytes == 4 ? launch_route<int32_t>(experts_of, n, k, experts, offsets,
+                                                         token_of_row, slots, (int32_t*)workspace, s)
+                                 : launch_route<int64_t>(experts_of, n, k, experts, offsets,
+                                                         token_of_row, slots, (int32_t*)workspace, s);
+        });
     });
 }
 
 tide_status tide_dispatch_tokens(int32_t dtype, const void* x, int64_t x_stride, int64_t tokens,
                                  int64_t width, const int32_t* slots, int32_t k, void* rows,
                                  int64_t rows_stride, int64_t nrows, void* stream) {
-    TIDE_TRY(check_sort(dtype, tokens, k, nrows));
-    const int32_t size = dtype == TIDE_DTYPE_FP32 ? 4 : 2;
-    Mat rd[2], wr;
-    TIDE_TRY(matrix("x", x, tokens, width, x_stride, size, &rd[0]));
-    TIDE_TRY(matrix("slots", slots, width ? tokens : 0, k, k, 4, &rd[1]));
-    TIDE_TRY(matrix("rows", rows, nrows, width, rows_stride, size, &wr));
-    TIDE_TRY(no_overlap(&wr, 1, rd, 2));
-    if (tokens == 0 || width == 0 || nrows == 0) return TIDE_OK;
-    return on_stream(stream, [&](hipStream_t s) {
-        const int64_t per = size / 2, units = (width * per + 7) / 8;
-        const RowGrid g = row_grid(tokens, units);
-        dispatch_rows<<<g.grid, dim3(kRowThreads), 0, s>>>(
-            (const uint16_t*)x, x_stride * per, tokens, width * per, k, slots, (uint16_t*)rows,
-            rows_stride * per, (uint32_t)nrows, g.lane_log2);
-        return hipGetLastError();
+    return guarded([&]() -> tide_status {
+        TIDE_TRY(check_sort(dtype, tokens, k, nrows));
+        const int32_t size = dtype == TIDE_DTYPE_FP32 ? 4 : 2;
+        Mat rd[2], wr;
+        TIDE_TRY(matrix("x", x, tokens, width, x_stride, size, &rd[0]));
+        TIDE_TRY(matrix("slots", slots, width ? tokens : 0, k, k, 4, &rd[1]));
+        TIDE_TRY(matrix("rows", rows, nrows, width, rows_stride, size, &wr));
+        TIDE_TRY(no_overlap(&wr, 1, rd, 2));
+        if (tokens == 0 || width == 0 || nrows == 0) return TIDE_OK;
+        return on_stream(stream, [&](hipStream_t s) {
+            const int64_t per = size / 2, units = (width * per + 7) / 8;
+            const RowGrid g = row_grid(tokens, units);
+            dispatch_rows<<<g.grid, dim3(kRowThreads), 0, s>>>(
+                (const uint16_t*)x, x_stride * per, tokens, width * per, k, slots, (uint16_t*)rows,
+                rows_stride * per, (uint32_t)nrows, g.lane_log2);
+            return hipGetLastError();
+        });
     });
 }
 
@@ -398,28 +404,30 @@ tide_status tide_combine_tokens(int32_t dtype, const void* rows, int64_t rows_st
                                 int64_t nrows, int64_t width, const int32_t* slots,
                                 const float* weights, int64_t tokens, int32_t k, void* out,
                                 int64_t out_stride, void* stream) {
-    TIDE_TRY(check_sort(dtype, tokens, k, nrows));
-    const int32_t size = dtype == TIDE_DTYPE_FP32 ? 4 : 2;
-    Mat rd[3], wr;
-    TIDE_TRY(matrix("rows", rows, nrows, width, rows_stride, size, &rd[0]));
-    TIDE_TRY(matrix("slots", slots, width ? tokens : 0, k, k, 4, &rd[1]));
-    TIDE_TRY(matrix("weights", weights, weights && width ? tokens : 0, k, k, 4, &rd[2]));
-    TIDE_TRY(matrix("out", out, tokens, width, out_stride, size, &wr));
-    TIDE_TRY(no_overlap(&wr, 1, rd, 3));
-    if (tokens == 0 || width == 0) return TIDE_OK;
-    return on_stream(stream, [&](hipStream_t s) {
-        const RowGrid g = row_grid(tokens, (width * size + 15) / 16);
-        with_ku(k, [&](auto ku) {
-            if (size == 2)
-                combine_rows<uint16_t, ku.value><<<g.grid, dim3(kRowThreads), 0, s>>>(
-                    (const uint16_t*)rows, rows_stride, (uint32_t)nrows, width, slots, weights,
-                    tokens, k, (uint16_t*)out, out_stride, g.lane_log2);
-            else
-                combine_rows<float, ku.value><<<g.grid, dim3(kRowThreads), 0, s>>>(
-                    (const float*)rows, rows_stride, (uint32_t)nrows, width, slots, weights,
-                    tokens, k, (float*)out, out_stride, g.lane_log2);
+    return guarded([&]() -> tide_status {
+        TIDE_TRY(check_sort(dtype, tokens, k, nrows));
+        const int32_t size = dtype == TIDE_DTYPE_FP32 ? 4 : 2;
+        Mat rd[3], wr;
+        TIDE_TRY(matrix("rows", rows, nrows, width, rows_stride, size, &rd[0]));
+        TIDE_TRY(matrix("slots", slots, width ? tokens : 0, k, k, 4, &rd[1]));
+        TIDE_TRY(matrix("weights", weights, weights && width ? tokens : 0, k, k, 4, &rd[2]));
+        TIDE_TRY(matrix("out", out, tokens, width, out_stride, size, &wr));
+        TIDE_TRY(no_overlap(&wr, 1, rd, 3));
+        if (tokens == 0 || width == 0) return TIDE_OK;
+        return on_stream(stream, [&](hipStream_t s) {
+            const RowGrid g = row_grid(tokens, (width * size + 15) / 16);
+            with_ku(k, [&](auto ku) {
+                if (size == 2)
+                    combine_rows<uint16_t, ku.value><<<g.grid, dim3(kRowThreads), 0, s>>>(
+                        (const uint16_t*)rows, rows_stride, (uint32_t)nrows, width, slots, weights,
+                        tokens, k, (uint16_t*)out, out_stride, g.lane_log2);
+                else
+                    combine_rows<float, ku.value><<<g.grid, dim3(kRowThreads), 0, s>>>(
+                        (const float*)rows, rows_stride, (uint32_t)nrows, width, slots, weights,
+                        tokens, k, (float*)out, out_stride, g.lane_log2);
+            });
+            return hipGetLastError();
         });
-        return hipGetLastError();
     });
 }
 
@@ -428,33 +436,35 @@ tide_status tide_combine_tokens_grad(int32_t dtype, const void* dout, int64_t do
                                      int64_t width, const int32_t* slots, const float* weights,
                                      int64_t tokens, int32_t k, void* drows,
                                      int64_t drows_stride, float* dweights, void* stream) {
-    TIDE_TRY(check_sort(dtype, tokens, k, nrows));
-    const int32_t size = dtype == TIDE_DTYPE_FP32 ? 4 : 2;
-    Mat rd[4], wr[2];
-    TIDE_TRY(matrix("dout", dout, tokens, width, dout_stride, size, &rd[0]));
-    TIDE_TRY(matrix("rows", rows, dweights ? nrows : 0, width, rows_stride, size, &rd[1]));
-    TIDE_TRY(matrix("slots", slots, tokens, k, k, 4, &rd[2]));
-    TIDE_TRY(matrix("weights", weights, weights ? tokens : 0, k, k, 4, &rd[3]));
-    TIDE_TRY(matrix("drows", drows, nrows, width, drows_stride, size, &wr[0]));
-    TIDE_TRY(matrix("dweights", dweights, dweights ? tokens : 0, k, k, 4, &wr[1]));
-    TIDE_TRY(no_overlap(wr, 2, rd, 4));
-    if (tokens == 0 || (width == 0 && !dweights)) return TIDE_OK;
-    return on_stream(stream, [&](hipStream_t s) {
-        const RowGrid g = row_grid(tokens, (width * size + 15) / 16, 6);
-        const dim3 grid(g.grid.x);
-        with_ku(k, [&](auto ku) {
-            if (size == 2)
-                combine_rows_grad<uint16_t, ku.value><<<grid, dim3(kRowThreads), 0, s>>>(
-                    (const uint16_t*)dout, dout_stride, (const uint16_t*)rows, rows_stride,
-                    (uint32_t)nrows, width, slots, weights, tokens, k, (uint16_t*)drows,
-                    drows_stride, dweights, g.lane_log2);
-            else
-                combine_rows_grad<float, ku.value><<<grid, dim3(kRowThreads), 0, s>>>(
-                    (const float*)dout, dout_stride, (const float*)rows, rows_stride,
-                    (uint32_t)nrows, width, slots, weights, tokens, k, (float*)drows,
-                    drows_stride, dweights, g.lane_log2);
+    return guarded([&]() -> tide_status {
+        TIDE_TRY(check_sort(dtype, tokens, k, nrows));
+        const int32_t size = dtype == TIDE_DTYPE_FP32 ? 4 : 2;
+        Mat rd[4], wr[2];
+        TIDE_TRY(matrix("dout", dout, tokens, width, dout_stride, size, &rd[0]));
+        TIDE_TRY(matrix("rows", rows, dweights ? nrows : 0, width, rows_stride, size, &rd[1]));
+        TIDE_TRY(matrix("slots", slots, tokens, k, k, 4, &rd[2]));
+        TIDE_TRY(matrix("weights", weights, weights ? tokens : 0, k, k, 4, &rd[3]));
+        TIDE_TRY(matrix("drows", drows, nrows, width, drows_stride, size, &wr[0]));
+        TIDE_TRY(matrix("dweights", dweights, dweights ? tokens : 0, k, k, 4, &wr[1]));
+        TIDE_TRY(no_overlap(wr, 2, rd, 4));
+        if (tokens == 0 || (width == 0 && !dweights)) return TIDE_OK;
+        return on_stream(stream, [&](hipStream_t s) {
+            const RowGrid g = row_grid(tokens, (width * size + 15) / 16, 6);
+            const dim3 grid(g.grid.x);
+            with_ku(k, [&](auto ku) {
+                if (size == 2)
+                    combine_rows_grad<uint16_t, ku.value><<<grid, dim3(kRowThreads), 0, s>>>(
+                        (const uint16_t*)dout, dout_stride, (const uint16_t*)rows, rows_stride,
+                        (uint32_t)nrows, width, slots, weights, tokens, k, (uint16_t*)drows,
+                        drows_stride, dweights, g.lane_log2);
+                else
+                    combine_rows_grad<float, ku.value><<<grid, dim3(kRowThreads), 0, s>>>(
+                        (const float*)dout, dout_stride, (const float*)rows, rows_stride,
+                        (uint32_t)nrows, width, slots, weights, tokens, k, (float*)drows,
+                        drows_stride, dweights, g.lane_log2);
+            });
+            return hipGetLastError();
         });
-        return hipGetLastError();
     });
 }
 

@@ -4,7 +4,6 @@
 #include <algorithm>
 #include <climits>
 #include <cstdio>
-#include <new>
 #include <vector>
 
 #include "device.hpp"
@@ -683,11 +682,13 @@ extern "C" {
 
 tide_status tide_weight_grads_workspace(int64_t rows, int64_t out, int64_t in, int32_t experts,
                                         int64_t* bytes) {
-    if (!bytes) return fail(TIDE_ERR_INVALID_ARG, "bytes is NULL");
-    TIDE_TRY(check_sizes(rows, out, in, experts));
-    const Plan p = plan_tiles(rows, out, in, experts);
-    *bytes = p.splits > 1 ? p.splits * experts * p.tiles_o * p.tiles_i * p.tile_o * p.tile_i * 4 : 0;
-    return TIDE_OK;
+    return guarded([&]() -> tide_status {
+        if (!bytes) return fail(TIDE_ERR_INVALID_ARG, "bytes is NULL");
+        TIDE_TRY(check_sizes(rows, out, in, experts));
+        const Plan p = plan_tiles(rows, out, in, experts);
+        *bytes = p.splits > 1 ? p.splits * experts * p.tiles_o * p.tiles_i * p.tile_o * p.tile_i * 4 : 0;
+        return TIDE_OK;
+    });
 }
 
 tide_status tide_weight_grads_bf16(const uint16_t* dy, int64_t dy_stride, int64_t rows,
@@ -696,7 +697,7 @@ tide_status tide_weight_grads_bf16(const uint16_t* dy, int64_t dy_stride, int64_
                                    const int32_t* offsets, const int32_t* token_of_row,
                                    int32_t experts, uint16_t* const* grads, int32_t accumulate,
                                    void* workspace, int64_t workspace_bytes, void* stream) {
-    try {
+    return guarded([&]() -> tide_status {
         int64_t need = 0;
         TIDE_TRY(tide_weight_grads_workspace(rows, out, in, experts, &need));
         if (need > 0 && (!workspace || workspace_bytes < need))
@@ -709,8 +710,7 @@ tide_status tide_weight_grads_bf16(const uint16_t* dy, int64_t dy_stride, int64_
         if (!token_of_row && x_rows < rows)
             return fail(TIDE_ERR_INVALID_ARG, "x has %lld rows, dy %lld", (long long)x_rows,
                         (long long)rows);
-        if ((x != nullptr) == (saved != nullptr) && rows > 0 && in > 0)
-            return fail(TIDE_ERR_INVALID_ARG, "need either x or saved");
+        if (x && saved) return fail(TIDE_ERR_INVALID_ARG, "x and saved are both given");
         Mat rd[6];                     // dy, x or codes, scales, offsets, token_of_row, workspace
         TIDE_TRY(matrix("dy", dy, rows, out, dy_stride, 2, &rd[0]));
         if (saved) {
@@ -787,11 +787,7 @@ tide_status tide_weight_grads_bf16(const uint16_t* dy, int64_t dy_stride, int64_
             }
             return hipSuccess;
         });
-    } catch (const std::bad_alloc&) {
-        return fail(TIDE_ERR_NO_MEMORY, "host allocation failed");
-    } catch (...) {
-        return fail(TIDE_ERR_INVALID_ARG, "unexpected exception");
-    }
+    });
 }
 
 }  // extern "C"

@@ -199,6 +199,40 @@ def test_on_side_streams_at_once(tide, how):
             assert same(L.results(), w)
 
 
+@pytest.mark.parametrize("null", [False, True])
+def test_workspace_on_a_stream_handle(tide, null):
+    """A call that allocates its workspace on a raw stream handle, also the null stream's."""
+    n, O, I, T = 6000, 128, 128, 3000
+    dy, x = ref.normal((n, O), BF16, 1).to(dev()), ref.normal((n, I), BF16, 2).to(dev())
+    want, got = (torch.zeros(1, O, I, dtype=BF16, device=dev()) for _ in range(2))
+    ids = ref.experts(T, 4, 16, seed=5).to(dev())
+    outs = [[torch.zeros(s, dtype=torch.int32, device=dev()) for s in (17, T * 4, (T, 4))] for _ in range(2)]
+    tide.weight_grads_bf16(dy, x, want)
+    tide.route_tokens(ids, 16, *outs[0])
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    handle = 0 if null else int(s.cuda_stream)
+    for _ in range(3):
+        got.zero_()
+        torch.cuda.synchronize()
+        tide.weight_grads_bf16(dy, x, got, stream=handle)
+        tide.route_tokens(ids, 16, *outs[1], stream=handle)
+        torch.cuda.synchronize()
+        assert torch.equal(got, want) and all(torch.equal(a, b) for a, b in zip(*outs))
+
+
+def test_x_without_rows(tide):
+    """Every token out of range of an x that has no rows: zeros."""
+    g = torch.full((2, 16, 24), 5.0, dtype=BF16, device=dev())
+    off = torch.tensor([0, 3, 7], dtype=torch.int32, device=dev())
+    tok = torch.full((7,), -1, dtype=torch.int32, device=dev())
+    dy = torch.full((7, 16), float("nan"), dtype=BF16, device=dev())
+    for x in (torch.empty(0, 24, dtype=BF16, device=dev()), saved(0, 24)):
+        g.fill_(5.0)
+        tide.weight_grads_bf16(dy, x, g, offsets=off, token_of_row=tok)
+        assert (g.cpu() == 0).all()
+
+
 def test_refused_on_the_gpu(tide):
     """Refusals that need GPU tensors: other types, sizes, overlaps, strides."""
     z = lambda *s, dt=BF16: torch.zeros(*s, dtype=dt, device=dev())  # noqa: E731
