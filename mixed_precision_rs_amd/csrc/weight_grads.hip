@@ -128,14 +128,15 @@ __device__ __forceinline__ void store4(const Args& a, uint16_t* out, int64_t o, 
 // each: 77 us against 104 in tiles of 256). The 64 tile is for few
 // tiles: its 4 waves are teams of one, each with the whole tile, stages of its
 // own and a quarter of the rows, joined at the end through LDS; nothing but
-// that join waits on another wave.
+// that join waits on another wave. Stages of 32 rows let two workgroups fit a
+// CU (576 x 2080 from 2067 rows 26 -> 20 us).
 // kSaved: x is a checkpoint, decoded on its way into LDS (exact, and free:
 // both forms run at 1150 TFLOP/s).
 template <int TO, int TI, bool kSaved, int kAccess>
 struct Tile {
     static constexpr int kTeams = TO == 64 ? 4 : 1;
     static constexpr int kThreads = (TI == 256 ? 512 : 256) / kTeams;          // of a team
-    static constexpr int kDepth = TO == TI ? kMostDepth : kMostDepth / 2;      // rows of a stage
+    static constexpr int kDepth = TO == TI && TO > 64 ? kMostDepth : kMostDepth / 2;      // rows of a stage
     static constexpr int WO = TO == 64 ? 1 : 2, WI = kThreads / 64 / WO;       // waves over the tile
     static constexpr int FO = TO / WO / 32, FI = TI / WI / 32;  // 32 x 32 blocks of a wave
     static constexpr int kSteps = kDepth / 16;                 // matrix steps of a stage
@@ -515,7 +516,7 @@ struct Tile {
 };
 
 template <int TO, int TI, bool kSaved, int kAccess>
-__global__ __launch_bounds__(TI == 256 ? 512 : 256, TO == 64 ? 1 : 2) void weight_grads(Args a, GradPtrs g) {
+__global__ __launch_bounds__(TI == 256 ? 512 : 256, 2) void weight_grads(Args a, GradPtrs g) {
     using K = Tile<TO, TI, kSaved, kAccess>;
     constexpr bool kInTeams = K::kTeams > 1;
     __shared__ __attribute__((aligned(1024))) uint16_t lds[K::kTeams * K::kLds / 2];
@@ -623,12 +624,13 @@ Access how_to_read(const Args& a) {
 // with 512 rows each 255 us in 256 x 256 and 250 in 256 x 128, with 64 rows 112
 // and 92; 1024 x 8192 from 8192 rows 193 us (128 tiles of 256 x 256), 154 (256
 // of 256 x 128) and 158 (512 of 128 x 128); 8 experts of 384 x 700, 512 rows
-// each, 43 us (96 of 256 x 128) and 25 (144 of 128 x 128); 512 x 2048 from 1000
-// rows 18.4 us (64 of 128 x 128) and 13.5 (256 of 64 x 64); 2048 x 2048 from 64
-// rows 15 us (256 of 128 x 128) and 22 (1024 of 64 x 64).
+// each, 43 us (96 of 256 x 128) and 25 (144 of 128 x 128); 2048 x 2048 from
+// 2000 rows 36 us (1024 of 64 x 64) and 28 (256 of 128 x 128); 576 x 2080 from
+// 2067 rows 29 us (85 of 128 x 128) and 20 (297 of 64 x 64).
 // Splits: where even tiles of 64 leave CUs idle, the rows of each are divided
 // among several workgroups, whose fp32 sums a second kernel adds in order:
-// 128 x 2048 from 8192 rows 37 us with one, 20 with four.
+// 128 x 2048 from 8192 rows 37 us with one, 24 with two, 17 with four, 19 with
+// eight.
 struct Plan {
     int64_t tiles_o, tiles_i;
     int tile_o, tile_i, splits;
@@ -643,8 +645,9 @@ Plan plan_tiles(int64_t n, int64_t O, int64_t I, int32_t experts) {
     const int64_t small = tiles(64, 64);
     Plan p{0, 0, 64, 64, 1};
     double best = 0;
-    for (int64_t k = 1; k == 1 || (k * small <= 256 && k * 4 <= stages); k *= 2) {
-        const double us = rounds(k * small, 256) * (6 + 0.75 * (double)((stages + 4 * k - 1) / (4 * k))) +
+    for (int64_t k = 1; k == 1 || (k * small <= 512 && k * 4 <= stages); k *= 2) {
+        const double each = (double)((stages + 4 * k - 1) / (4 * k));      // stages of a wave
+        const double us = (k * small <= 256 ? 6 + each : rounds(k * small, 512) * (6 + 1.55 * each)) +
                           (k > 1 ? 5 + 0.01 * (double)(k * small) : 0);
         if (k == 1 || us < best) {
             best = us;
