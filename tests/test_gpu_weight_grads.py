@@ -278,3 +278,27 @@ def test_rows_past_32_bit_offsets(tide, saved):
     tide.weight_grads_bf16(d, xin, g)
     want, mag, cnt = ref.weight_grads(dy, xv, torch.tensor([0, n]), None)
     ref.close(g[0], want[0], bound(want[0], mag[0], cnt[0]))
+
+
+@pytest.mark.parametrize("saved", [False, True])
+@pytest.mark.parametrize("n,O,I", [(700, 45, 70), (1500, 520, 515), (300, 4103, 2601)])
+def test_tokens_of_rows_past_32_bit_offsets(tide, n, O, I, saved):
+    T, stride = 1100, 1 << 21
+    if torch.cuda.mem_get_info()[0] < 30 << 30:
+        pytest.skip("needs 30 GiB of GPU memory")
+    dy, x = ref.normal((n, O), torch.bfloat16, seed=3), ref.normal((T, I), torch.bfloat16, seed=4)
+    tokens = torch.randint(0, T, (n,), generator=torch.Generator().manual_seed(5))
+    tokens[[0, 1, 5, n - 1]] = torch.tensor([T - 1, 0, -1, T])        # rows of no token add nothing
+    tokens = tokens.to(torch.int32)
+    if saved:
+        s = ref.saved_of(x)
+        c = torch.empty(T, stride, dtype=torch.uint8, device=dev())[:, 3: 3 + I]
+        c.copy_(s[0].view(torch.uint8).to(dev()))
+        xin, xv = (c.view(torch.float8_e4m3fn), s[1].to(dev())), ref.unpack(*s)
+    else:
+        xin, xv = torch.empty(T, stride, dtype=torch.bfloat16, device=dev())[:, 3: 3 + I], x
+        xin.copy_(x.to(dev()))
+    g = torch.empty(1, O, I, dtype=torch.bfloat16, device=dev())
+    tide.weight_grads_bf16(dy.to(dev()), xin, g, token_of_row=tokens.to(dev()))
+    want, mag, cnt = ref.weight_grads(dy, xv, torch.tensor([0, n]), tokens)
+    ref.close(g[0], want[0], bound(want[0], mag[0], cnt[0]))
