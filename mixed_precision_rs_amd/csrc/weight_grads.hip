@@ -31,6 +31,7 @@ struct Args {
     int64_t n, x_rows, O, I;
     float* partial;                    // with splits > 1: the sums of each split of each tile
     int32_t accumulate, tiles_o, tiles_i, first, count, splits;
+    int32_t past_caches;               // how gradients are stored
 };
 
 typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
@@ -481,7 +482,7 @@ struct Tile {
     // chunk c lies at c ^ o, its halves swapped in every other 16 rows, so that
     // neither the 8-byte writes nor the reads meet a bank twice.
     __device__ __forceinline__ void finish(f32x16 (&acc)[FO][FI], uint16_t* out) {
-        constexpr int C = TI / 8, N = TO * C / kThreads;
+        constexpr int C = TI / 8;
 #pragma unroll
         for (int x = 0; x < FO; ++x) {
             const int o = place_o(row_of(wave, lane, x));
@@ -506,6 +507,12 @@ struct Tile {
             }
         }
         __syncthreads();
+        if (a.past_caches) store_tile<true>(out);
+        else store_tile<false>(out);
+    }
+    template <bool kPastCaches>
+    __device__ __forceinline__ void store_tile(uint16_t* out) {
+        constexpr int C = TI / 8, N = TO * C / kThreads;
         const bool whole = o0 + TO <= a.O && i0 + TI <= a.I;
 #pragma unroll
         for (int j0 = 0; j0 < N; j0 += 4) {
@@ -519,7 +526,8 @@ struct Tile {
                 uint16_t* d = out + (o0 + o) * a.I + i0 + c * 8;
                 const int64_t n = whole ? 8 : o0 + o < a.O ? a.I - i0 - c * 8 : 0;
                 if (n >= 8) {
-                    __builtin_nontemporal_store(v[j], gbl_mut<u32x4_a2>(d));
+                    if constexpr (kPastCaches) __builtin_nontemporal_store(v[j], gbl_mut<u32x4_a2>(d));
+                    else *gbl_mut<u32x4_a2>(d) = v[j];
                 } else {
 #pragma unroll
                     for (int q = 0; q < 7; ++q)
@@ -624,6 +632,16 @@ Access how_to_read(const Args& a) {
     if (a.O < 8 || a.I < step || a.dy_stride > lim / 2 / kMostDepth) return kElements;
     if (rows > 0 && (xs > lim / rows || a.scales_stride > lim / rows)) return a.tokens ? kWide : kElements;
     return kBuffers;
+}
+
+// Whether the gradients are stored past the caches. It leaves those to dy and x
+// (128 experts of 512 x 1001, 128 rows each, 64 us against 82), but the lines
+// that two tiles share, where rows of the gradient do not start on lines, are
+// written twice. With few rows nothing is there to be left in: 128 experts of
+// 512 x 1001, 5 rows each, 57 us past the caches and 42-47 through them; 8192
+// x 8191 from 64 rows 61 and 44-54, 8192 x 12287 from 512 rows 148 and 147-170.
+bool stores_past_caches(int64_t n, int64_t I, int32_t experts) {
+    return I % 64 == 0 || n / experts > kMostDepth;
 }
 
 // Tile and splits. A large tile reuses each staged element more (1200, 1080,
@@ -778,6 +796,7 @@ tide_status tide_weight_grads_bf16(const uint16_t* dy, int64_t dy_stride, int64_
         if (x_rows == 0) a.n = 0;              // no row of x to add
         const Access how = how_to_read(a);
         const Plan p = plan_tiles(rows, out, in, experts);
+        a.past_caches = stores_past_caches(rows, in, experts);
         if (p.tiles_o > kMaxGroups / p.tiles_i)
             return fail(TIDE_ERR_UNSUPPORTED, "gradients of %lld x %lld", (long long)out, (long long)in);
         const int64_t tiles = p.tiles_o * p.tiles_i;
