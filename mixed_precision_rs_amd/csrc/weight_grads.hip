@@ -42,8 +42,9 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kMostDepth = 64;         // rows (tokens) of one stage, at most
 // How rows are read. Buffers: rows of any alignment and of one 16-byte load or
-// more, by buffer loads. Wide: as Buffers, but x through 64-bit addresses, for
-// token indices into more than 2 GiB. Elements: rows shorter than a load.
+// more, by buffer loads. Wide: as Buffers, but through 64-bit addresses, for
+// token indices into more than 2 GiB and for strides of 32 MiB. Elements: rows
+// shorter than a load.
 enum Access { kBuffers, kWide, kElements };
 constexpr uint32_t kBufferWord = 0x00020000;      // raw buffer, bounds checked in bytes
 constexpr uint32_t kOutside = 0x80000000u;        // past every buffer: loads read 0
@@ -155,6 +156,7 @@ struct Tile {
     static constexpr int CI = TI / (kSaved ? 16 : 8);          // 16-byte loads of a row of x
     static constexpr int NI = kDepth * CI / kThreads;
     static_assert(kSteps == 2 || kSteps == 4, "the steps of sum()");
+    static_assert(NO <= 16 && NI <= 16, "the bits of Moving::none");
     static constexpr int kStage = kDepth * (TO + TI);          // elements of one stage
     static constexpr int kLds = 2 * kStage * 2 > TO * TI * 2 ? 2 * kStage * 2 : TO * TI * 2;
 
@@ -166,7 +168,7 @@ struct Tile {
     struct Moving {
         u32x4 o[NO], i[NI];
         uint32_t s[kSaved ? NI : 1];
-        uint32_t none;                 // Wide: bit j: i[j] is of no row
+        uint32_t none;                 // Wide: bit j: o[j], bit 16 + j: i[j] is of no row
         int32_t tok[NI];               // the next one's rows of x
     };
 
@@ -217,7 +219,7 @@ struct Tile {
     __device__ __forceinline__ void load(Moving& m, int64_t t0) {
         const int64_t left = hi - t0 < 0 ? 0 : hi - t0;
         const int rows = left < kDepth ? (int)left : kDepth;
-        if constexpr (kAccess != kElements) {
+        if constexpr (kAccess == kBuffers) {
             // rows past the last lie past the buffer by themselves
             const __amdgpu_buffer_rsrc_t d =
                 buffer(a.dy + t0 * a.dy_stride, rows, (uint32_t)a.dy_stride * 2, (uint32_t)a.O * 2);
@@ -225,8 +227,6 @@ struct Tile {
 #pragma unroll
             for (int j = kPart * NO / kOf; j < (kPart + 1) * NO / kOf; ++j)
                 m.o[j] = buffer16(d, at + (uint32_t)(j * (kThreads / CO)) * (uint32_t)a.dy_stride * 2);
-        }
-        if constexpr (kAccess == kBuffers) {
             // with token indices the whole of x is one buffer, without the stage's rows are
             const uint32_t stride = (uint32_t)(kSaved ? a.codes_stride : a.x_stride * 2);
             const uint32_t length = (uint32_t)a.I * (kSaved ? 1 : 2);
@@ -238,26 +238,32 @@ struct Tile {
             if constexpr (kSaved)
                 s = buffer(a.scales + first * a.scales_stride, span, (uint32_t)a.scales_stride,
                            (uint32_t)(a.I + kScaleBlock - 1) / kScaleBlock);
-            const uint32_t at = (uint32_t)column_i() * (kSaved ? 1 : 2), block = (uint32_t)(i0 + tid % CI * 16) / kScaleBlock;
+            const uint32_t col = (uint32_t)column_i() * (kSaved ? 1 : 2), block = (uint32_t)(i0 + tid % CI * 16) / kScaleBlock;
 #pragma unroll
             for (int j = kPart * NI / kOf; j < (kPart + 1) * NI / kOf; ++j) {
                 const int t = j * (kThreads / CI) + tid / CI;
                 const uint32_t row = a.tokens ? (uint32_t)m.tok[j] : (uint32_t)t;
                 // or'ed in rather than selected, so that no branch guards the products
                 const uint32_t out = row < span && t < rows ? 0 : kOutside;
-                m.i[j] = buffer16(x, min(out | (row * stride + at), kOutside));
+                m.i[j] = buffer16(x, min(out | (row * stride + col), kOutside));
                 if constexpr (kSaved)
                     m.s[j] = __builtin_amdgcn_raw_buffer_load_b8(
                         s, (int)min(out | (row * (uint32_t)a.scales_stride + block), kOutside), 0, 0);
             }
         } else if constexpr (kAccess == kWide) {
+#pragma unroll
+            for (int j = kPart * NO / kOf; j < (kPart + 1) * NO / kOf; ++j) {
+                const int t = j * (kThreads / CO) + tid / CO;
+                m.none = (m.none & ~(1u << j)) | (t < rows ? 0 : 1u << j);
+                m.o[j] = *gbl<u32x4_a2>(a.dy + min(t0 + t, hi - 1) * a.dy_stride + column_o());
+            }
             const int64_t block = min(i0 + tid % CI * 16, a.I - 1) / kScaleBlock;
 #pragma unroll
             for (int j = kPart * NI / kOf; j < (kPart + 1) * NI / kOf; ++j) {
                 const int t = j * (kThreads / CI) + tid / CI;
-                int64_t row = m.tok[j];
+                int64_t row = a.tokens ? m.tok[j] : t0 + t;
                 const bool in = t < rows && (uint64_t)row < (uint64_t)a.x_rows;
-                m.none = (m.none & ~(1u << j)) | (in ? 0 : 1u << j);
+                m.none = (m.none & ~(0x10000u << j)) | (in ? 0 : 0x10000u << j);
                 row = in ? row : 0;
                 if constexpr (kSaved) {
                     m.i[j] = *gbl<u32x4_a1>(a.codes + row * a.codes_stride + column_i());
@@ -300,12 +306,13 @@ struct Tile {
 #pragma unroll
         for (int j = kPart * NO / kOf; j < (kPart + 1) * NO / kOf; ++j) {
             const int t = j * (kThreads / CO) + tid / CO, c = tid % CO;
+            if constexpr (kAccess == kWide) m.o[j] = m.none >> j & 1 ? u32x4{} : m.o[j];
             *(u32x4*)(stage_o(b) + t * TO + chunk_at<TO>(t, c) * 8) = m.o[j];
         }
 #pragma unroll
         for (int j = kPart * NI / kOf; j < (kPart + 1) * NI / kOf; ++j) {
             const int t = j * (kThreads / CI) + tid / CI, c = tid % CI;
-            if constexpr (kAccess == kWide) m.i[j] = m.none >> j & 1 ? u32x4{} : m.i[j];
+            if constexpr (kAccess == kWide) m.i[j] = m.none >> (16 + j) & 1 ? u32x4{} : m.i[j];
             if constexpr (kSaved) {
                 u32x4 p, q;
                 decode16(m.i[j], __uint_as_float(m.s[j] << 23), p, q);
@@ -652,8 +659,9 @@ hipError_t launch_tiles(const Args& a, const GradPtrs& g, Access how, hipStream_
 Access how_to_read(const Args& a) {
     const int64_t step = a.codes ? 16 : 8, xs = a.codes ? a.codes_stride : a.x_stride * 2;
     const int64_t lim = kMostBytes, rows = a.tokens ? a.x_rows : kMostDepth;
-    if (a.O < 8 || a.I < step || a.dy_stride > lim / 2 / kMostDepth) return kElements;
-    if (rows > 0 && (xs > lim / rows || a.scales_stride > lim / rows)) return a.tokens ? kWide : kElements;
+    if (a.O < 8 || a.I < step) return kElements;       // plan_tiles gives these tiles of 64
+    if (a.dy_stride > lim / 2 / kMostDepth || (rows > 0 && (xs > lim / rows || a.scales_stride > lim / rows)))
+        return kWide;
     return kBuffers;
 }
 

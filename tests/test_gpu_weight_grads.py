@@ -302,3 +302,31 @@ def test_tokens_of_rows_past_32_bit_offsets(tide, n, O, I, saved):
     tide.weight_grads_bf16(dy.to(dev()), xin, g, token_of_row=tokens.to(dev()))
     want, mag, cnt = ref.weight_grads(dy, xv, torch.tensor([0, n]), tokens)
     ref.close(g[0], want[0], bound(want[0], mag[0], cnt[0]))
+
+
+@pytest.mark.parametrize("saved", [False, True])
+@pytest.mark.parametrize("far", ["dy", "x"])
+@pytest.mark.parametrize("n,O,I", [(100, 45, 70), (130, 520, 515), (70, 4103, 2601)])
+def test_strides_past_32_mib(tide, n, O, I, far, saved):
+    stride = (1 << 25) + 3 if saved and far == "x" else (1 << 24) + 3
+    if torch.cuda.mem_get_info()[0] < 30 << 30:
+        pytest.skip("needs 30 GiB of GPU memory")
+    dy, x = ref.normal((n, O), torch.bfloat16, seed=6), ref.normal((n, I), torch.bfloat16, seed=7)
+
+    def spread(t):
+        s = torch.empty(n, stride, dtype=t.dtype, device=dev())[:, 5: 5 + t.shape[1]]
+        s.copy_(t.to(dev()))
+        return s
+
+    d = spread(dy) if far == "dy" else dy.to(dev())
+    if saved:
+        s = ref.saved_of(x)
+        c = s[0].view(torch.uint8)
+        c = spread(c) if far == "x" else c.to(dev())
+        xin, xv = (c.view(torch.float8_e4m3fn), s[1].to(dev())), ref.unpack(*s)
+    else:
+        xin, xv = spread(x) if far == "x" else x.to(dev()), x
+    g = torch.empty(1, O, I, dtype=torch.bfloat16, device=dev())
+    tide.weight_grads_bf16(d, xin, g)
+    want, mag, cnt = ref.weight_grads(dy, xv, torch.tensor([0, n]), None)
+    ref.close(g[0], want[0], bound(want[0], mag[0], cnt[0]))
