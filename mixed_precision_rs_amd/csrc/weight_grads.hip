@@ -142,7 +142,8 @@ __device__ __forceinline__ void store_chunk(uint16_t* out, u32x4 v) {
 // CU (576 x 2080 from 2067 rows 26 -> 20 us).
 // kSaved: x is a checkpoint, decoded on its way into LDS (exact, and free:
 // both forms run at 1150 TFLOP/s).
-template <int TO, int TI, bool kSaved, int kAccess>
+// kTokens: there may be token indices (with kBuffers: there are).
+template <int TO, int TI, bool kSaved, int kAccess, bool kTokens>
 struct Tile {
     static constexpr int kTeams = TO == 64 ? 4 : 1;
     static constexpr int kThreads = (TI == 256 ? 512 : 256) / kTeams;          // of a team
@@ -170,6 +171,8 @@ struct Tile {
         uint32_t s[kSaved ? NI : 1];
         uint32_t none;                 // Wide: bit j: o[j], bit 16 + j: i[j] is of no row
         int32_t tok[NI];               // the next one's rows of x
+        uint64_t dropped;              // the next one's rows without a token, a bit each
+        int32_t of_lane;               // the token of row `lane` of the one after it
     };
 
     // A team of one wave needs no barrier: its LDS accesses run in order.
@@ -200,23 +203,38 @@ struct Tile {
     __device__ __forceinline__ int place_o(int r) const { return place<8>(r, a.O - o0); }
     __device__ __forceinline__ int place_i(int r) const { return place<kSaved ? 16 : 8>(r, a.I - i0); }
 
-    // Rows of x of the stage that starts at t0 (0 without token indices and
-    // past the last row: no load uses those).
-    __device__ __forceinline__ void load_tokens(Moving& m, int64_t t0) {
+    __device__ __forceinline__ bool indexed() const { return kTokens && (kAccess == kBuffers || a.tokens); }
+
+    // The tokens of the stage at t0, a row a lane (0 past the last row and
+    // without token indices: no load uses those).
+    __device__ __forceinline__ int32_t lane_token(int64_t t0) const {
         const int64_t left = hi - t0 < 0 ? 0 : hi - t0;
         const int rows = left < kDepth ? (int)left : kDepth;
-        const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(
-            (void*)(a.tokens + t0), (short)0, a.tokens ? rows * 4 : 0, (int)kBufferWord);
+        return __builtin_amdgcn_raw_buffer_load_b32(
+            __builtin_amdgcn_make_buffer_rsrc((void*)(a.tokens + t0), (short)0, indexed() ? rows * 4 : 0,
+                                              (int)kBufferWord), lane * 4, 0, 0);
+    }
+    // What a stage's loads need of its tokens: this thread's rows of x, and which
+    // rows have none in x. Those add nothing, whatever dy holds there (zeros for
+    // their x alone would not do against NaN and infinities).
+    __device__ __forceinline__ void use_tokens(Moving& m, int32_t of_lane) {
 #pragma unroll
-        for (int j = 0; j < NI; ++j) {
-            const int t = j * (kThreads / CI) + tid / CI;
-            m.tok[j] = __builtin_amdgcn_raw_buffer_load_b32(r, t * 4, 0, 0);
-        }
+        for (int j = 0; j < NI; ++j)
+            m.tok[j] = __builtin_amdgcn_ds_bpermute((j * (kThreads / CI) + tid / CI) * 4, of_lane);
+        m.dropped = __ballot((uint32_t)of_lane >= (uint32_t)a.x_rows);
+    }
+    // kOutside where the row of dy in chunk j of this thread is dropped, else 0.
+    __device__ __forceinline__ uint32_t dropped(const Moving& m, int j) const {
+        constexpr int R = kThreads / CO;
+        static_assert(R <= 32 && 32 % R == 0 && kDepth <= 64, "the rows of a chunk are in one word");
+        const uint32_t w = (uint32_t)(m.dropped >> (j * R / 32 * 32));
+        return (w << (32 - R - j * R % 32) << (R - 1 - tid / CO)) & kOutside;
     }
 
-    // Part kPart of kOf of the loads of the stage at t0.
-    template <int kPart, int kOf>
-    __device__ __forceinline__ void load(Moving& m, int64_t t0) {
+    // Part kPart of kOf of the loads of dy for the stage at t0. With kDrop, rows
+    // without a token are not loaded.
+    template <int kPart, int kOf, bool kDrop = kTokens>
+    __device__ __forceinline__ void load_o(Moving& m, int64_t t0) {
         const int64_t left = hi - t0 < 0 ? 0 : hi - t0;
         const int rows = left < kDepth ? (int)left : kDepth;
         if constexpr (kAccess == kBuffers) {
@@ -226,13 +244,39 @@ struct Tile {
             const uint32_t at = (uint32_t)(tid / CO) * (uint32_t)a.dy_stride * 2 + (uint32_t)column_o() * 2;
 #pragma unroll
             for (int j = kPart * NO / kOf; j < (kPart + 1) * NO / kOf; ++j)
-                m.o[j] = buffer16(d, at + (uint32_t)(j * (kThreads / CO)) * (uint32_t)a.dy_stride * 2);
+                m.o[j] = buffer16(d, (at + (uint32_t)(j * (kThreads / CO)) * (uint32_t)a.dy_stride * 2) |
+                                         (kDrop ? dropped(m, j) : 0));
+        } else if constexpr (kAccess == kWide) {
+#pragma unroll
+            for (int j = kPart * NO / kOf; j < (kPart + 1) * NO / kOf; ++j) {
+                const int t = j * (kThreads / CO) + tid / CO;
+                m.none = (m.none & ~(1u << j)) | (t < rows && !(kDrop && dropped(m, j)) ? 0 : 1u << j);
+                m.o[j] = *gbl<u32x4_a2>(a.dy + min(t0 + t, hi - 1) * a.dy_stride + column_o());
+            }
+        } else {
+#pragma unroll
+            for (int j = kPart * NO / kOf; j < (kPart + 1) * NO / kOf; ++j) {
+                const int t = j * (kThreads / CO) + tid / CO, c = tid % CO;
+                const int64_t n = a.O - o0 - c * 8;
+                m.o[j] = u32x4{};
+                if (n > 0 && t < rows && !(kDrop && dropped(m, j)))
+                    m.o[j] = load_row(a.dy + (t0 + t) * a.dy_stride + o0 + c * 8, (int)(n < 8 ? n : 8));
+            }
+        }
+    }
+
+    // The same of x.
+    template <int kPart, int kOf>
+    __device__ __forceinline__ void load_i(Moving& m, int64_t t0) {
+        const int64_t left = hi - t0 < 0 ? 0 : hi - t0;
+        const int rows = left < kDepth ? (int)left : kDepth;
+        if constexpr (kAccess == kBuffers) {
             // with token indices the whole of x is one buffer, without the stage's rows are
             const uint32_t stride = (uint32_t)(kSaved ? a.codes_stride : a.x_stride * 2);
             const uint32_t length = (uint32_t)a.I * (kSaved ? 1 : 2);
             const uint8_t* base = kSaved ? a.codes : (const uint8_t*)a.x;
-            const uint32_t span = a.tokens ? (uint32_t)a.x_rows : (uint32_t)rows;
-            const int64_t first = a.tokens ? 0 : t0;
+            const uint32_t span = kTokens ? (uint32_t)a.x_rows : (uint32_t)rows;
+            const int64_t first = kTokens ? 0 : t0;
             const __amdgpu_buffer_rsrc_t x = buffer(base + first * stride, span, stride, length);
             __amdgpu_buffer_rsrc_t s = x;
             if constexpr (kSaved)
@@ -242,7 +286,7 @@ struct Tile {
 #pragma unroll
             for (int j = kPart * NI / kOf; j < (kPart + 1) * NI / kOf; ++j) {
                 const int t = j * (kThreads / CI) + tid / CI;
-                const uint32_t row = a.tokens ? (uint32_t)m.tok[j] : (uint32_t)t;
+                const uint32_t row = kTokens ? (uint32_t)m.tok[j] : (uint32_t)t;
                 // or'ed in rather than selected, so that no branch guards the products
                 const uint32_t out = row < span && t < rows ? 0 : kOutside;
                 m.i[j] = buffer16(x, min(out | (row * stride + col), kOutside));
@@ -251,17 +295,11 @@ struct Tile {
                         s, (int)min(out | (row * (uint32_t)a.scales_stride + block), kOutside), 0, 0);
             }
         } else if constexpr (kAccess == kWide) {
-#pragma unroll
-            for (int j = kPart * NO / kOf; j < (kPart + 1) * NO / kOf; ++j) {
-                const int t = j * (kThreads / CO) + tid / CO;
-                m.none = (m.none & ~(1u << j)) | (t < rows ? 0 : 1u << j);
-                m.o[j] = *gbl<u32x4_a2>(a.dy + min(t0 + t, hi - 1) * a.dy_stride + column_o());
-            }
             const int64_t block = min(i0 + tid % CI * 16, a.I - 1) / kScaleBlock;
 #pragma unroll
             for (int j = kPart * NI / kOf; j < (kPart + 1) * NI / kOf; ++j) {
                 const int t = j * (kThreads / CI) + tid / CI;
-                int64_t row = a.tokens ? m.tok[j] : t0 + t;
+                int64_t row = indexed() ? m.tok[j] : t0 + t;
                 const bool in = t < rows && (uint64_t)row < (uint64_t)a.x_rows;
                 m.none = (m.none & ~(0x10000u << j)) | (in ? 0 : 0x10000u << j);
                 row = in ? row : 0;
@@ -274,17 +312,9 @@ struct Tile {
             }
         } else {
 #pragma unroll
-            for (int j = kPart * NO / kOf; j < (kPart + 1) * NO / kOf; ++j) {
-                const int t = j * (kThreads / CO) + tid / CO, c = tid % CO;
-                const int64_t n = a.O - o0 - c * 8;
-                m.o[j] = u32x4{};
-                if (n > 0 && t < rows)
-                    m.o[j] = load_row(a.dy + (t0 + t) * a.dy_stride + o0 + c * 8, (int)(n < 8 ? n : 8));
-            }
-#pragma unroll
             for (int j = kPart * NI / kOf; j < (kPart + 1) * NI / kOf; ++j) {
                 const int t = j * (kThreads / CI) + tid / CI, c = tid % CI;
-                const int64_t row = t >= rows ? -1 : a.tokens ? m.tok[j] : t0 + t;
+                const int64_t row = t >= rows ? -1 : indexed() ? m.tok[j] : t0 + t;
                 const int64_t col = i0 + c * (kSaved ? 16 : 8), n = a.I - col;
                 m.i[j] = u32x4{};
                 if constexpr (kSaved) m.s[j] = 0;
@@ -353,7 +383,7 @@ struct Tile {
         constexpr int M = FO * FI, R = 2 * (FO + FI);
         constexpr bool moves = kStep < kParts;
         constexpr int W = moves ? (NO + (kSaved ? 2 : 1) * NI) / kParts : 0;
-        constexpr int L = moves ? (NO + (kSaved ? 2 : 1) * NI) / kParts : kStep == kParts ? NI : 0;
+        constexpr int L = moves ? (NO + (kSaved ? 2 : 1) * NI) / kParts : kStep == kParts && kTokens ? 1 : 0;
         if constexpr (kAt < M) {
             constexpr int r = (kAt + 1) * R / M - kAt * R / M, w = (kAt + 1) * W / M - kAt * W / M;
             constexpr int l = (kAt + 1) * L / M - kAt * L / M;
@@ -377,9 +407,13 @@ struct Tile {
         }
         if constexpr (kStep < kParts) {
             store<kStep, kParts>(m, b ^ 1);
-            load<kStep, kParts>(m, t0 + 2 * kDepth);
+            load_o<kStep, kParts>(m, t0 + 2 * kDepth);
+            load_i<kStep, kParts>(m, t0 + 2 * kDepth);
         }
-        if constexpr (kStep == kParts) load_tokens(m, t0 + 3 * kDepth);
+        if constexpr (kStep == kParts && kTokens) {
+            use_tokens(m, m.of_lane);
+            m.of_lane = lane_token(t0 + 4 * kDepth);
+        }
 #pragma unroll
         for (int x = 0; x < FO; ++x)
 #pragma unroll
@@ -396,11 +430,32 @@ struct Tile {
     __device__ __forceinline__ void sum(f32x16 (&acc)[FO][FI]) {
         if (lo >= hi) return;
         Moving first, m;
-        load_tokens(first, lo);
-        load_tokens(m, lo + kDepth);
-        load<0, 1>(first, lo);
-        load<0, 1>(m, lo + kDepth);
-        load_tokens(m, lo + 2 * kDepth);
+        // The first rows of dy do not wait for their tokens; those without one are
+        // dropped when they are there, by a mask (a select became a branch around
+        // the load and a wait for everything). All other stages' tokens are loaded
+        // a stage before their rows, which then wait for no newer load. 128 experts
+        // of 767 x 2047 with 32 rows each take 114 us, as without the dropping,
+        // and 127 where the first rows do wait.
+        if constexpr (kTokens) {
+            const int32_t first_of = lane_token(lo), next_of = lane_token(lo + kDepth);
+            const int32_t third_of = lane_token(lo + 2 * kDepth);
+            m.of_lane = lane_token(lo + 3 * kDepth);
+            load_o<0, 1, false>(first, lo);
+            __builtin_amdgcn_sched_barrier(0);
+            use_tokens(first, first_of);
+            load_i<0, 1>(first, lo);
+            use_tokens(m, next_of);
+            load_o<0, 1>(m, lo + kDepth);
+            load_i<0, 1>(m, lo + kDepth);
+            use_tokens(m, third_of);
+#pragma unroll
+            for (int j = 0; j < NO; ++j) first.o[j] &= (dropped(first, j) >> 31) - 1;
+        } else {
+            load_o<0, 1>(first, lo);
+            load_i<0, 1>(first, lo);
+            load_o<0, 1>(m, lo + kDepth);
+            load_i<0, 1>(m, lo + kDepth);
+        }
         store<0, 1>(first, 0);
         sync();
         bf16x8 fo[2][FO], fi[2][FI];
@@ -568,9 +623,9 @@ struct Tile {
     }
 };
 
-template <int TO, int TI, bool kSaved, int kAccess>
+template <int TO, int TI, bool kSaved, int kAccess, bool kTokens>
 __global__ __launch_bounds__(TI == 256 ? 512 : 256, 2) void weight_grads(Args a, GradPtrs g) {
-    using K = Tile<TO, TI, kSaved, kAccess>;
+    using K = Tile<TO, TI, kSaved, kAccess, kTokens>;
     constexpr bool kInTeams = K::kTeams > 1;
     __shared__ __attribute__((aligned(1024))) uint16_t lds[K::kTeams * K::kLds / 2];
     // Workgroups go round robin over the XCDs: each XCD gets one run of tiles,
@@ -637,15 +692,15 @@ template <int TO, int TI>
 hipError_t launch_tiles(const Args& a, const GradPtrs& g, Access how, hipStream_t stream) {
     const int64_t groups = (int64_t)a.count * a.splits * a.tiles_o * a.tiles_i;
     const dim3 grid((uint32_t)((groups + 7) / 8 * 8)), threads(TI == 256 ? 512 : 256);
-    if (a.codes) {
-        if (how == kBuffers) weight_grads<TO, TI, true, kBuffers><<<grid, threads, 0, stream>>>(a, g);
-        else if (how == kWide) weight_grads<TO, TI, true, kWide><<<grid, threads, 0, stream>>>(a, g);
-        else if constexpr (TO == 64) weight_grads<TO, TI, true, kElements><<<grid, threads, 0, stream>>>(a, g);
-    } else {
-        if (how == kBuffers) weight_grads<TO, TI, false, kBuffers><<<grid, threads, 0, stream>>>(a, g);
-        else if (how == kWide) weight_grads<TO, TI, false, kWide><<<grid, threads, 0, stream>>>(a, g);
-        else if constexpr (TO == 64) weight_grads<TO, TI, false, kElements><<<grid, threads, 0, stream>>>(a, g);
-    }
+    const auto run = [&](auto saved) {
+        constexpr bool kSaved = saved.value;
+        if (how == kBuffers && a.tokens) weight_grads<TO, TI, kSaved, kBuffers, true><<<grid, threads, 0, stream>>>(a, g);
+        else if (how == kBuffers) weight_grads<TO, TI, kSaved, kBuffers, false><<<grid, threads, 0, stream>>>(a, g);
+        else if (how == kWide) weight_grads<TO, TI, kSaved, kWide, true><<<grid, threads, 0, stream>>>(a, g);
+        else if constexpr (TO == 64) weight_grads<TO, TI, kSaved, kElements, true><<<grid, threads, 0, stream>>>(a, g);
+    };
+    if (a.codes) run(std::true_type{});
+    else run(std::false_type{});
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || a.splits == 1) return e;
     const int64_t blocks = (int64_t)a.count * a.tiles_o * a.tiles_i * (64 * 64 / 4 / 256);

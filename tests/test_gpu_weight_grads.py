@@ -330,3 +330,55 @@ def test_strides_past_32_mib(tide, n, O, I, far, saved):
     tide.weight_grads_bf16(d, xin, g)
     want, mag, cnt = ref.weight_grads(dy, xv, torch.tensor([0, n]), None)
     ref.close(g[0], want[0], bound(want[0], mag[0], cnt[0]))
+
+
+def rows_without_a_token(tokens, dy, x_rows, seed):
+    """A tenth of the rows, the first and the last among them, get tokens out of
+    range, and values that no sum may meet."""
+    n = tokens.numel()
+    bad = torch.rand(n, generator=torch.Generator().manual_seed(seed)) < 0.1
+    bad[[0, n - 1]] = True
+    m = int(bad.sum())
+    tokens[bad] = torch.tensor([-1, x_rows, 2 ** 31 - 1, -2 ** 31]).repeat(m // 4 + 1)[:m]
+    held = torch.tensor([float("nan"), float("inf"), -float("inf")]).repeat(m // 3 + 1)[:m]
+    dy[bad] = held.to(dy.dtype)[:, None]
+
+
+@pytest.mark.parametrize("saved", [False, True])
+@pytest.mark.parametrize("pad", [0, 3])
+@pytest.mark.parametrize("n,O,I", [  # each tile, the split sums, rows shorter than a load
+    (90, 40, 64), (6000, 128, 512), (70, 1990, 2039), (64, 4104, 2600), (700, 4100, 2570), (100, 7, 130)])
+def test_rows_without_a_token_add_nothing_whatever_they_hold(tide, n, O, I, pad, saved):
+    say("weight_grads, rows without a token", n, O, I, pad, saved)
+    T = n // 2 + 1
+    dy, x = ref.normal((n, O), torch.bfloat16, seed=n), ref.normal((T, I), torch.bfloat16, seed=I)
+    tokens = torch.randint(0, T, (n,), generator=torch.Generator().manual_seed(8))
+    rows_without_a_token(tokens, dy, T, seed=9)
+    check(tide, dy, x, saved, None, tokens, pad)
+    check(tide, dy, x, saved, torch.tensor([0, n // 3, n // 3, n]), tokens, pad,
+          old=ref.normal((3, O, I), torch.bfloat16, seed=3))
+
+
+@pytest.mark.parametrize("saved", [False, True])
+@pytest.mark.parametrize("n,O,I", [(700, 45, 70), (500, 1500, 2000), (300, 4103, 2601), (700, 4100, 2570)])
+def test_rows_without_a_token_and_far_rows(tide, n, O, I, saved):
+    """The same where x passes 32-bit offsets, in each tile."""
+    T, stride = 1100, 1 << 21
+    if torch.cuda.mem_get_info()[0] < 30 << 30:
+        pytest.skip("needs 30 GiB of GPU memory")
+    say("weight_grads, rows without a token, far rows", n, O, I, saved)
+    dy, x = ref.normal((n, O), torch.bfloat16, seed=3), ref.normal((T, I), torch.bfloat16, seed=4)
+    tokens = torch.randint(0, T, (n,), generator=torch.Generator().manual_seed(5))
+    rows_without_a_token(tokens, dy, T, seed=6)
+    if saved:
+        s = ref.saved_of(x)
+        c = torch.empty(T, stride, dtype=torch.uint8, device=dev())[:, 3: 3 + I]
+        c.copy_(s[0].view(torch.uint8).to(dev()))
+        xin, xv = (c.view(torch.float8_e4m3fn), s[1].to(dev())), ref.unpack(*s)
+    else:
+        xin, xv = torch.empty(T, stride, dtype=torch.bfloat16, device=dev())[:, 3: 3 + I], x
+        xin.copy_(x.to(dev()))
+    g = torch.empty(1, O, I, dtype=torch.bfloat16, device=dev())
+    tide.weight_grads_bf16(dy.to(dev()), xin, g, token_of_row=tokens.int().to(dev()))
+    want, mag, cnt = ref.weight_grads(dy, xv, torch.tensor([0, n]), tokens)
+    ref.close(g[0], want[0], bound(want[0], mag[0], cnt[0]))
