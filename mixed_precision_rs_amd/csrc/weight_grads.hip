@@ -71,6 +71,15 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(const void* p, uint32_t
     return __builtin_amdgcn_make_buffer_rsrc((void*)p, (short)0, max(bytes, 0), (int)kBufferWord);
 }
 
+// The scale block of column c of a row; of the row's last column for loads past
+// its end, whose values are not stored: no byte behind a row's scales is read.
+__host__ __device__ constexpr int64_t scale_block(int64_t c, int64_t width) {
+    return (c < width ? c : width - 1) / kScaleBlock;
+}
+static_assert(scale_block(0, 1) == 0 && scale_block(31, 33) == 0 && scale_block(32, 33) == 1 &&
+                  scale_block(48, 33) == 1 && scale_block(240, 33) == 1 && scale_block(240, 241) == 7,
+              "within the row's scales");
+
 // Sixteen e4m3 codes with one scale as two chunks of bf16 (exact).
 __device__ __forceinline__ void decode16(u32x4 c, float scale, u32x4& lo, u32x4& hi) {
 #pragma unroll
@@ -282,7 +291,8 @@ struct Tile {
             if constexpr (kSaved)
                 s = buffer(a.scales + first * a.scales_stride, span, (uint32_t)a.scales_stride,
                            (uint32_t)(a.I + kScaleBlock - 1) / kScaleBlock);
-            const uint32_t col = (uint32_t)column_i() * (kSaved ? 1 : 2), block = (uint32_t)(i0 + tid % CI * 16) / kScaleBlock;
+            const uint32_t col = (uint32_t)column_i() * (kSaved ? 1 : 2);
+            const uint32_t block = (uint32_t)scale_block(i0 + tid % CI * 16, a.I);
 #pragma unroll
             for (int j = kPart * NI / kOf; j < (kPart + 1) * NI / kOf; ++j) {
                 const int t = j * (kThreads / CI) + tid / CI;
@@ -295,7 +305,7 @@ struct Tile {
                         s, (int)min(out | (row * (uint32_t)a.scales_stride + block), kOutside), 0, 0);
             }
         } else if constexpr (kAccess == kWide) {
-            const int64_t block = min(i0 + tid % CI * 16, a.I - 1) / kScaleBlock;
+            const int64_t block = scale_block(i0 + tid % CI * 16, a.I);
 #pragma unroll
             for (int j = kPart * NI / kOf; j < (kPart + 1) * NI / kOf; ++j) {
                 const int t = j * (kThreads / CI) + tid / CI;
