@@ -309,6 +309,22 @@ def gated_silu_grad(dout, gate_saved, up_saved, dgate, dup, out=None, stream=Non
          [dout, *gate_saved, *up_saved, dgate, dup, out], sobj)
 
 
+def _grads_list(grads, out: int, in_: int, dev: Optional[int]):
+    """Array of the addresses of a list of (out, in) gradients. A tensor of the
+    transposed shape has as many elements, so the shape itself is compared."""
+    want = (out, in_)
+    for i, t in enumerate(grads):
+        if t is None or isinstance(t, int):
+            continue
+        if t.shape != want:
+            raise ValueError("grads[%d] has shape %s, expected %s" % (i, tuple(t.shape), want))
+    _check_many(grads, "bfloat16", [out * in_] * len(grads), lambda i: "grads[%d]" % i)
+    for i, t in enumerate(grads):
+        if t is not None and not isinstance(t, int) and dev is not None and t.get_device() != dev:
+            _place(t, "grads[%d]" % i, dev)
+    return (ctypes.c_void_p * max(len(grads), 1))(*[_ptr(t) for t in grads])
+
+
 def weight_grads_workspace_bytes(rows: int, out: int, in_: int, num_experts: int = 1) -> int:
     """Bytes of workspace weight_grads_bf16 needs (tide_weight_grads_workspace)."""
     n = _I64()
@@ -348,12 +364,7 @@ def weight_grads_bf16(dy, x, grads: Union[object, Sequence[object], PointerTable
         E, arr = grads.n, grads.arr
         keep += grads.refs
     elif isinstance(grads, (list, tuple)):
-        _check_many(grads, "bfloat16", [O * I] * len(grads), lambda i: "grads[%d]" % i)
-        for i, t in enumerate(grads):
-            if not isinstance(t, int) and dev is not None and t.get_device() != dev:
-                _place(t, "grads[%d]" % i, dev)
-        E = len(grads)
-        arr = (ctypes.c_void_p * max(E, 1))(*[_ptr(t) for t in grads])
+        E, arr = len(grads), _grads_list(grads, O, I, dev)
         keep += list(grads)
     else:
         E = grads.shape[0] if grads.dim() == 3 else -1

@@ -291,3 +291,14 @@ def test_refused_on_the_gpu(tide):
     g = z(16, 24)
     with pytest.raises(tide.TideError, match="overlap"):
         tide.weight_grads_bf16(dy, xx, [g, g], offsets=z(3, dt=torch.int32))
+
+
+def test_list_of_transposed_gradients_is_refused(tide):
+    dy, x = (torch.ones(10, c, dtype=BF16, device=dev()) for c in (16, 24))
+    g = torch.full((24, 16), 3.0, dtype=BF16, device=dev())
+    for grads in (g, g[None], [g], [g.view(-1)]):
+        with pytest.raises(ValueError, match="shape"):
+            tide.weight_grads_bf16(dy, x, grads)
+    assert (g.cpu() == 3.0).all()
+    tide.weight_grads_bf16(dy, x, [g.view(16, 24)])
+    assert (g.cpu() == 10.0).all()

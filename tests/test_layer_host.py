@@ -201,3 +201,18 @@ def test_binding_refuses(tide):
         lay._saved((codes, scales), "saved", 2, 64, None)
     with pytest.raises(TypeError):
         lay._saved((codes.view(torch.uint8), scales), "saved", 2, 64, None)
+
+
+def test_list_of_gradients_refuses_other_shapes(tide):
+    """A list's tensors have to be (out, in) each: the transposed shape and a flat
+    tensor hold as many elements."""
+    from mixed_precision_rs_amd import _layer as lay
+    g = lambda *s: torch.zeros(*s, dtype=torch.bfloat16)  # noqa: E731
+    for bad in (g(24, 16), g(16 * 24), g(1, 16, 24), g(16, 23)):
+        with pytest.raises(ValueError, match=r"grads\[1\] has shape .* expected \(16, 24\)"):
+            lay._grads_list([FAKE, bad], 16, 24, None)
+    with pytest.raises(ValueError, match="not contiguous"):
+        lay._grads_list([g(24, 16).t()], 16, 24, None)
+    with pytest.raises(ValueError, match="not a GPU tensor"):
+        lay._grads_list([g(16, 24)], 16, 24, None)
+    assert list(lay._grads_list([FAKE, None], 16, 24, 0)) == [FAKE, None]
