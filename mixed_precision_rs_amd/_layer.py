@@ -67,7 +67,7 @@ def _place(t, what: str, dev: Optional[int]) -> None:
     if not t.is_cuda:
         raise ValueError("%s is not a GPU tensor" % what)
     if dev is not None and t.get_device() != dev:
-        raise ValueError("%s is on GPU %d, the stream on GPU %d" % (what, t.get_device(), dev))
+        raise ValueError("%s is on GPU %d, the call on GPU %d" % (what, t.get_device(), dev))
 
 
 def _mat(t, what: str, dtype, rows: Optional[int], cols: Optional[int], dev) -> Tuple[int, int]:
@@ -116,17 +116,18 @@ def _on(stream, t):
     """(handle, stream object or None, device or None) of a call whose first
     tensor is t. Without a stream: the current one of t's device, which need
     not be the current device. The object is there when the tensors have to be
-    recorded on the stream, the device is None when the handle is a raw integer,
-    whose device only the library can tell."""
+    recorded on the stream. A raw handle does not tell its device: the call is
+    on t's, where all its tensors and its workspace then have to be, and the
+    null handle is that device's null stream."""
+    dev = t.get_device() if t.get_device() >= 0 else None      # None: refused by the checks that follow
     if stream is None:
         import torch
-        dev = t.get_device()
-        if dev < 0:
-            return 0, None, None           # refused by the checks that follow
+        if dev is None:
+            return 0, None, None
         h = torch._C._cuda_getCurrentRawStream(dev)
         return h, None if h == 0 else torch.cuda.current_stream(dev), dev
     h, obj = _stream_handle(stream)
-    return h, obj, None if obj is None else obj.device.index
+    return h, obj, dev if obj is None else obj.device.index
 
 
 def _run(name: str, args, dev: Optional[int], refs, sobj) -> None:
@@ -160,7 +161,7 @@ def _workspace(need: int, workspace, stream, dev):
     else:
         s = stream
         if isinstance(stream, int):
-            s = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
+            s = torch.cuda.ExternalStream(stream, device=dev) if stream else torch.cuda.default_stream(dev)
         with torch.cuda.stream(s):
             w = torch.empty(need, dtype=torch.uint8, device=s.device)
     return w.data_ptr(), need, w

@@ -216,3 +216,41 @@ def test_list_of_gradients_refuses_other_shapes(tide):
     with pytest.raises(ValueError, match="not a GPU tensor"):
         lay._grads_list([g(16, 24)], 16, 24, None)
     assert list(lay._grads_list([FAKE, None], 16, 24, 0)) == [FAKE, None]
+
+
+class OnGpu:
+    """What the binding asks of a tensor about its place."""
+    is_cuda = True
+
+    def __init__(self, dev):
+        self.dev = dev
+
+    def get_device(self):
+        return self.dev
+
+
+def test_raw_handles_take_the_tensors_device(tide, monkeypatch):
+    """With a raw stream handle, also the null one, the workspace is allocated and
+    the other tensors are expected on the first tensor's GPU, which need not be the
+    current one."""
+    import contextlib
+    from mixed_precision_rs_amd import _layer as lay
+    for handle in (77, 0):
+        assert lay._on(handle, OnGpu(3)) == (handle, None, 3)
+        assert lay._on(handle, OnGpu(-1)) == (handle, None, None)      # a CPU tensor: refused as such later
+    lay._place(OnGpu(3), "x", 3)
+    with pytest.raises(ValueError, match="x is on GPU 1, the call on GPU 3"):
+        lay._place(OnGpu(1), "x", 3)
+
+    class Stream:
+        def __init__(self, handle, device):
+            self.device = device
+
+    made, buf = [], torch.zeros(100, dtype=torch.uint8)
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda handle, device="current": Stream(handle, device))
+    monkeypatch.setattr(torch.cuda, "default_stream", lambda device="current": Stream(0, device))
+    monkeypatch.setattr(torch.cuda, "stream", lambda s: contextlib.nullcontext())
+    monkeypatch.setattr(torch, "empty", lambda n, dtype, device: (made.append((n, device)), buf)[1])
+    for handle in (77, 0):
+        lay._workspace(100, None, handle, 3)
+    assert made == [(100, 3), (100, 3)]
