@@ -708,10 +708,10 @@ hipError_t launch_tiles(const Args& a, const GradPtrs& g, Access how, hipStream_
         else if (how == kBuffers) weight_grads<TO, TI, kSaved, kBuffers, false><<<grid, threads, 0, stream>>>(a, g);
         else if (how == kWide) weight_grads<TO, TI, kSaved, kWide, true><<<grid, threads, 0, stream>>>(a, g);
         else if constexpr (TO == 64) weight_grads<TO, TI, kSaved, kElements, true><<<grid, threads, 0, stream>>>(a, g);
+        else return hipErrorInvalidConfiguration;      // plan_tiles and how_to_read disagree
+        return hipGetLastError();
     };
-    if (a.codes) run(std::true_type{});
-    else run(std::false_type{});
-    const hipError_t e = hipGetLastError();
+    const hipError_t e = a.codes ? run(std::true_type{}) : run(std::false_type{});
     if (e != hipSuccess || a.splits == 1) return e;
     const int64_t blocks = (int64_t)a.count * a.tiles_o * a.tiles_i * (64 * 64 / 4 / 256);
     join_splits<<<dim3((uint32_t)blocks), dim3(256), 0, stream>>>(a, g);

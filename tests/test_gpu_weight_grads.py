@@ -382,3 +382,11 @@ def test_rows_without_a_token_and_far_rows(tide, n, O, I, saved):
     tide.weight_grads_bf16(dy.to(dev()), xin, g, token_of_row=tokens.int().to(dev()))
     want, mag, cnt = ref.weight_grads(dy, xv, torch.tensor([0, n]), tokens)
     ref.close(g[0], want[0], bound(want[0], mag[0], cnt[0]))
+
+
+@pytest.mark.parametrize("saved", [False, True])
+@pytest.mark.parametrize("far", ["dy", "x"])
+@pytest.mark.parametrize("n,O,I", [(70, 1990, 2039), (700, 4100, 2570)])
+def test_strides_past_32_mib_in_the_other_tiles(tide, n, O, I, far, saved):
+    """As test_strides_past_32_mib, at sizes that take the 128 x 128 and the 256 x 256 tile."""
+    test_strides_past_32_mib(tide, n, O, I, far, saved)
