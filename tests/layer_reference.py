@@ -147,3 +147,19 @@ def close(got, want, bound, what=""):
     bad = off > lim
     assert not bad.any(), "%s: %d of %d past the bound, worst %.3g over %.3g" % (
         what, int(bad.sum()), bad.numel(), float(off[bad].max()), float(lim[bad].min()))
+
+
+def whole(shape, most, seed):
+    """Whole numbers from -most to most as bf16 (exact up to 256)."""
+    g = torch.Generator().manual_seed(seed)
+    return torch.randint(-most, most + 1, shape, generator=g).to(torch.bfloat16)
+
+
+def rounded_sum(dy, x, offsets, tokens, old=None):
+    """Gradients of whole numbers below 2^24 in all: fp32 sums are exact in any
+    order, so the result is the exact sum rounded once to bf16."""
+    want, mag, _ = weight_grads(dy, x, offsets, tokens)
+    if old is not None:
+        want = want + old.double()
+    assert float(mag.max()) + 256 < 2 ** 24
+    return want.float().to(torch.bfloat16)

@@ -390,3 +390,32 @@ def test_rows_without_a_token_and_far_rows(tide, n, O, I, saved):
 def test_strides_past_32_mib_in_the_other_tiles(tide, n, O, I, far, saved):
     """As test_strides_past_32_mib, at sizes that take the 128 x 128 and the 256 x 256 tile."""
     test_strides_past_32_mib(tide, n, O, I, far, saved)
+
+
+EXACT = [  # split sums, teams of waves with ragged shares, each tile, rows shorter than a load
+    (9001, 64, 40), (6000, 128, 512), (5000, 96, 97), (4097, 128, 136), (2100, 128, 512), (3001, 264, 520), (700, 8, 16),
+    (33, 70, 70), (129, 64, 64), (2001, 1500, 2000), (1000, 1024, 1500), (300, 4103, 2601), (700, 4100, 2570), (1000, 7, 130)]
+
+
+@pytest.mark.parametrize("saved", [False, True])
+@pytest.mark.parametrize("n,O,I", EXACT)
+def test_sums_of_whole_numbers_bit_for_bit(tide, n, O, I, saved):
+    """Small whole numbers, whose sums fp32 holds exactly in any order: one lost
+    row, or partial sums in fewer bits, would show (test_exact_sums_notice)."""
+    say("weight_grads, whole numbers", n, O, I, saved)
+    T = n // 2 + 1
+    dy, x, xt = ref.whole((n, O), 3, n), ref.whole((n, I), 3, I), ref.whole((T, I), 3, I + 1)
+    old = ref.whole((3, O, I), 256, 7)
+    tokens = torch.randint(-1, T + 1, (n,), generator=torch.Generator().manual_seed(8))
+    put = lambda t: tuple(v.to(dev()) for v in ref.saved_of(t)) if saved else t.to(dev())  # noqa: E731
+    if saved:
+        assert torch.equal(ref.unpack(*ref.saved_of(x)), x.double())
+    for off, xx, tok in ((torch.tensor([0, n]), x, None), (torch.tensor([3, n // 3, n // 3 + 1, n - 1]), x, None),
+                         (torch.tensor([0, n // 3, n // 2, n]), xt, tokens)):
+        E = len(off) - 1
+        for start in (None, old[:E]):
+            g = torch.full((E, O, I), 5.0, dtype=torch.bfloat16, device=dev()) if start is None else start.to(dev())
+            tide.weight_grads_bf16(dy.to(dev()), put(xx), g, offsets=off.int().to(dev()),
+                                   token_of_row=None if tok is None else tok.int().to(dev()),
+                                   accumulate=start is not None)
+            assert torch.equal(g.cpu(), ref.rounded_sum(dy, xx, off, tok, start)), (off, start is not None)

@@ -254,3 +254,21 @@ def test_raw_handles_take_the_tensors_device(tide, monkeypatch):
     for handle in (77, 0):
         lay._workspace(100, None, handle, 3)
     assert made == [(100, 3), (100, 3)]
+
+
+@pytest.mark.parametrize("n,O,I", [(9001, 64, 40), (6000, 128, 512), (5000, 96, 97), (2100, 128, 512), (129, 64, 64)])
+def test_exact_sums_notice(n, O, I):
+    """The whole numbers that the weight gradients are compared on bit for bit: a
+    row left out, and sums joined from four partials in bf16, give other results."""
+    import layer_reference as ref
+    dy, x, all_ = ref.whole((n, O), 3, n), ref.whole((n, I), 3, I), torch.tensor([0, n])
+    want = ref.rounded_sum(dy, x, all_, None)
+    for r in list(range(0, n, n // 20)) + [n - 1]:
+        less = (dy.double().t() @ x.double() - dy[r].double()[:, None] * x[r].double())[None]
+        assert not torch.equal(less.float().to(torch.bfloat16), want), r
+    parts = [ref.rounded_sum(dy[i::4], x[i::4], torch.tensor([0, len(dy[i::4])]), None).float() for i in range(4)]
+    # whole numbers up to 256 are exact in bf16: partials that stay there (33 rows' do) lose nothing
+    if max(float(p.abs().max()) for p in parts) > 256:
+        assert not torch.equal(sum(parts).to(torch.bfloat16), want)
+    else:
+        assert n < 200
