@@ -318,13 +318,12 @@ Saved device_of(const tide_saved* s) {
     return s ? Saved{s->codes, s->scales, s->codes_stride, s->scales_stride} : Saved{};
 }
 
-// Runs launch(grid, stream) over the vectors of `rows` x `width` elements.
+// Runs launch(grid, stream), which returns a hipError_t, over the vectors of `rows` x `width` elements.
 template <class F>
 tide_status over_rows(int64_t rows, int64_t width, int32_t size, void* stream, F&& launch) {
     if (rows == 0 || width == 0) return TIDE_OK;
     return on_stream(stream, [&](hipStream_t s) {
-        launch(row_grid(rows, (width * size + 15) / 16, size == 2 ? 2 : 3), s);
-        return hipGetLastError();
+        return launch(row_grid(rows, (width * size + 15) / 16, size == 2 ? 2 : 3), s);
     });
 }
 
@@ -343,10 +342,10 @@ tide_status tide_checkpoint_pack(int32_t dtype, const void* x, int64_t x_stride,
         TIDE_TRY(c.done());
         return over_rows(rows, width, size, stream, [&](RowGrid g, hipStream_t s) {
             if (size == 2)
-                pack_rows<uint16_t><<<g.grid, dim3(kRowThreads), 0, s>>>(
+                return enqueue(pack_rows<uint16_t>, g.grid, kRowThreads, 0, s,
                     (const uint16_t*)x, x_stride, rows, width, device_of(saved), g.lane_log2);
             else
-                pack_rows<float><<<g.grid, dim3(kRowThreads), 0, s>>>(
+                return enqueue(pack_rows<float>, g.grid, kRowThreads, 0, s,
                     (const float*)x, x_stride, rows, width, device_of(saved), g.lane_log2);
         });
     });
@@ -363,10 +362,10 @@ tide_status tide_checkpoint_unpack(int32_t dtype, const tide_saved* saved, int64
         TIDE_TRY(c.done());
         return over_rows(rows, width, size, stream, [&](RowGrid g, hipStream_t s) {
             if (size == 2)
-                unpack_rows<uint16_t><<<g.grid, dim3(kRowThreads), 0, s>>>(
+                return enqueue(unpack_rows<uint16_t>, g.grid, kRowThreads, 0, s,
                     device_of(saved), rows, width, (uint16_t*)out, out_stride, g.lane_log2);
             else
-                unpack_rows<float><<<g.grid, dim3(kRowThreads), 0, s>>>(
+                return enqueue(unpack_rows<float>, g.grid, kRowThreads, 0, s,
                     device_of(saved), rows, width, (float*)out, out_stride, g.lane_log2);
         });
     });
@@ -388,12 +387,12 @@ tide_status tide_gated_silu(int32_t dtype, const void* gate, int64_t gate_stride
         TIDE_TRY(c.done());
         return over_rows(rows, width, size, stream, [&](RowGrid g, hipStream_t s) {
             if (size == 2)
-                gated_rows<uint16_t><<<g.grid, dim3(kRowThreads), 0, s>>>(
+                return enqueue(gated_rows<uint16_t>, g.grid, kRowThreads, 0, s,
                     (const uint16_t*)gate, gate_stride, (const uint16_t*)up, up_stride, rows, width,
                     (uint16_t*)out, out_stride, device_of(gate_saved), device_of(up_saved),
                     g.lane_log2);
             else
-                gated_rows<float><<<g.grid, dim3(kRowThreads), 0, s>>>(
+                return enqueue(gated_rows<float>, g.grid, kRowThreads, 0, s,
                     (const float*)gate, gate_stride, (const float*)up, up_stride, rows, width,
                     (float*)out, out_stride, device_of(gate_saved), device_of(up_saved), g.lane_log2);
         });
@@ -418,13 +417,14 @@ tide_status tide_gated_silu_grad(int32_t dtype, const void* dout, int64_t dout_s
         TIDE_TRY(c.done());
         return over_rows(rows, width, size, stream, [&](RowGrid g, hipStream_t s) {
             if (size == 2)
-                gated_rows_grad<uint16_t><<<g.grid, dim3(kRowThreads), 0, s>>>(
+                return enqueue(gated_rows_grad<uint16_t>, g.grid, kRowThreads, 0, s,
                     (const uint16_t*)dout, dout_stride, device_of(gate_saved), device_of(up_saved),
                     rows, width, (uint16_t*)dgate, dgate_stride, (uint16_t*)dup, dup_stride,
                     (uint16_t*)out, out_stride, g.lane_log2);
             else
-                gated_rows_grad<float><<<g.grid, dim3(kRowThreads), 0, s>>>(
-                    (const float*)dout, dout_stride, device_of(gate_saved), device_of(up_saved), rows,
+                return enqueue(gated_rows_grad<float>, g.grid, kRowThreads, 0, s,
+                    (const float*)dout, dout_stride, device_of(gate_saved), device_of(up_saved),
+                    rows,
                     width, (float*)dgate, dgate_stride, (float*)dup, dup_stride, (float*)out,
                     out_stride, g.lane_log2);
         });

@@ -86,6 +86,17 @@ tide_status guarded(F&& body) {
     }
 }
 
+// Launches a kernel and returns this launch's own error: hipGetLastError would
+// also report, and take away, one that the caller's earlier calls left behind.
+template <class... P, class... A>
+hipError_t enqueue(void (*kernel)(P...), dim3 grid, uint32_t threads, size_t lds, hipStream_t stream,
+                   A... values) {
+    return [&](P... v) {
+        void* args[] = {(void*)&v...};
+        return hipLaunchKernel(reinterpret_cast<const void*>(kernel), grid, dim3(threads), args, lds, stream);
+    }(values...);
+}
+
 // Runs launch(stream), which returns a hipError_t, with the stream's device
 // current.
 template <class F>

@@ -316,11 +316,11 @@ __global__ __launch_bounds__(kRowThreads) void combine_rows_grad(
 }
 
 template <class F>
-void with_ku(int32_t k, F&& f) {
-    if (k == 1) f(std::integral_constant<int, 1>{});
-    else if (k == 2) f(std::integral_constant<int, 2>{});
-    else if (k <= 4) f(std::integral_constant<int, 4>{});
-    else f(std::integral_constant<int, 8>{});
+hipError_t with_ku(int32_t k, F&& f) {
+    if (k == 1) return f(std::integral_constant<int, 1>{});
+    if (k == 2) return f(std::integral_constant<int, 2>{});
+    if (k <= 4) return f(std::integral_constant<int, 4>{});
+    return f(std::integral_constant<int, 8>{});
 }
 
 template <class Id>
@@ -328,14 +328,12 @@ hipError_t launch_route(const void* ids, int64_t n, int32_t k, int32_t E, int32_
                         int32_t* tokens, int32_t* slots, int32_t* counts, hipStream_t stream) {
     const int64_t chunk = route_chunk(n), nb = route_blocks(n);
     if (nb > 1) {
-        route_count<Id><<<dim3((uint32_t)nb), dim3(kRouteThreads), 0, stream>>>(
+        const hipError_t e = enqueue(route_count<Id>, dim3((uint32_t)nb), kRouteThreads, 0, stream,
             (const Id*)ids, n, E, chunk, counts);
-        const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
-    route_place<Id><<<dim3((uint32_t)nb), dim3(kRouteThreads), (size_t)kRouteWaves * E * 4, stream>>>(
+    return enqueue(route_place<Id>, dim3((uint32_t)nb), kRouteThreads, (size_t)kRouteWaves * E * 4, stream,
         (const Id*)ids, n, k, E, chunk, counts, offsets, tokens, slots);
-    return hipGetLastError();
 }
 
 tide_status check_sort(int32_t dtype, int64_t T, int32_t k, int64_t nrows) {
@@ -409,10 +407,9 @@ tide_status tide_dispatch_tokens(int32_t dtype, const void* x, int64_t x_stride,
         return on_stream(stream, [&](hipStream_t s) {
             const int64_t per = size / 2, units = (width * per + 7) / 8;
             const RowGrid g = row_grid(tokens, units);
-            dispatch_rows<<<g.grid, dim3(kRowThreads), 0, s>>>(
+            return enqueue(dispatch_rows, g.grid, kRowThreads, 0, s,
                 (const uint16_t*)x, x_stride * per, tokens, width * per, k, slots, (uint16_t*)rows,
                 rows_stride * per, (uint32_t)nrows, g.lane_log2);
-            return hipGetLastError();
         });
     });
 }
@@ -433,17 +430,16 @@ tide_status tide_combine_tokens(int32_t dtype, const void* rows, int64_t rows_st
         if (tokens == 0 || width == 0) return TIDE_OK;
         return on_stream(stream, [&](hipStream_t s) {
             const RowGrid g = row_grid(tokens, (width * size + 15) / 16);
-            with_ku(k, [&](auto ku) {
+            return with_ku(k, [&](auto ku) {
                 if (size == 2)
-                    combine_rows<uint16_t, ku.value><<<g.grid, dim3(kRowThreads), 0, s>>>(
+                    return enqueue(combine_rows<uint16_t, ku.value>, g.grid, kRowThreads, 0, s,
                         (const uint16_t*)rows, rows_stride, (uint32_t)nrows, width, slots, weights,
                         tokens, k, (uint16_t*)out, out_stride, g.lane_log2);
                 else
-                    combine_rows<float, ku.value><<<g.grid, dim3(kRowThreads), 0, s>>>(
+                    return enqueue(combine_rows<float, ku.value>, g.grid, kRowThreads, 0, s,
                         (const float*)rows, rows_stride, (uint32_t)nrows, width, slots, weights,
                         tokens, k, (float*)out, out_stride, g.lane_log2);
             });
-            return hipGetLastError();
         });
     });
 }
@@ -468,19 +464,18 @@ tide_status tide_combine_tokens_grad(int32_t dtype, const void* dout, int64_t do
         return on_stream(stream, [&](hipStream_t s) {
             const RowGrid g = row_grid(tokens, (width * size + 15) / 16, 6);
             const dim3 grid(g.grid.x);
-            with_ku(k, [&](auto ku) {
+            return with_ku(k, [&](auto ku) {
                 if (size == 2)
-                    combine_rows_grad<uint16_t, ku.value><<<grid, dim3(kRowThreads), 0, s>>>(
+                    return enqueue(combine_rows_grad<uint16_t, ku.value>, grid, kRowThreads, 0, s,
                         (const uint16_t*)dout, dout_stride, (const uint16_t*)rows, rows_stride,
                         (uint32_t)nrows, width, slots, weights, tokens, k, (uint16_t*)drows,
                         drows_stride, dweights, g.lane_log2);
                 else
-                    combine_rows_grad<float, ku.value><<<grid, dim3(kRowThreads), 0, s>>>(
+                    return enqueue(combine_rows_grad<float, ku.value>, grid, kRowThreads, 0, s,
                         (const float*)dout, dout_stride, (const float*)rows, rows_stride,
                         (uint32_t)nrows, width, slots, weights, tokens, k, (float*)drows,
                         drows_stride, dweights, g.lane_log2);
             });
-            return hipGetLastError();
         });
     });
 }

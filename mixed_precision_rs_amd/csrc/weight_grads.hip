@@ -701,21 +701,22 @@ __global__ __launch_bounds__(256) void join_splits(Args a, GradPtrs g) {
 template <int TO, int TI>
 hipError_t launch_tiles(const Args& a, const GradPtrs& g, Access how, hipStream_t stream) {
     const int64_t groups = (int64_t)a.count * a.splits * a.tiles_o * a.tiles_i;
-    const dim3 grid((uint32_t)((groups + 7) / 8 * 8)), threads(TI == 256 ? 512 : 256);
+    const dim3 grid((uint32_t)((groups + 7) / 8 * 8));
+    constexpr uint32_t threads = TI == 256 ? 512 : 256;
+    const auto start = [&](auto kernel) { return enqueue(kernel, grid, threads, 0, stream, a, g); };
     const auto run = [&](auto saved) {
         constexpr bool kSaved = saved.value;
-        if (how == kBuffers && a.tokens) weight_grads<TO, TI, kSaved, kBuffers, true><<<grid, threads, 0, stream>>>(a, g);
-        else if (how == kBuffers) weight_grads<TO, TI, kSaved, kBuffers, false><<<grid, threads, 0, stream>>>(a, g);
-        else if (how == kWide) weight_grads<TO, TI, kSaved, kWide, true><<<grid, threads, 0, stream>>>(a, g);
-        else if constexpr (TO == 64) weight_grads<TO, TI, kSaved, kElements, true><<<grid, threads, 0, stream>>>(a, g);
-        else return hipErrorInvalidConfiguration;      // plan_tiles and how_to_read disagree
-        return hipGetLastError();
+        if (how == kBuffers && a.tokens) return start(weight_grads<TO, TI, kSaved, kBuffers, true>);
+        if (how == kBuffers) return start(weight_grads<TO, TI, kSaved, kBuffers, false>);
+        if (how == kWide) return start(weight_grads<TO, TI, kSaved, kWide, true>);
+        if constexpr (TO == 64)
+            if (how == kElements) return start(weight_grads<TO, TI, kSaved, kElements, true>);
+        return hipErrorInvalidConfiguration;           // plan_tiles and how_to_read disagree
     };
     const hipError_t e = a.codes ? run(std::true_type{}) : run(std::false_type{});
     if (e != hipSuccess || a.splits == 1) return e;
     const int64_t blocks = (int64_t)a.count * a.tiles_o * a.tiles_i * (64 * 64 / 4 / 256);
-    join_splits<<<dim3((uint32_t)blocks), dim3(256), 0, stream>>>(a, g);
-    return hipGetLastError();
+    return enqueue(join_splits, dim3((uint32_t)blocks), 256, 0, stream, a, g);
 }
 
 // The buffers' 32-bit byte offsets have to reach a stage of dy and, with token

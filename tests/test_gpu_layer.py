@@ -302,3 +302,24 @@ def test_list_of_transposed_gradients_is_refused(tide):
     assert (g.cpu() == 3.0).all()
     tide.weight_grads_bf16(dy, x, [g.view(16, 24)])
     assert (g.cpu() == 10.0).all()
+
+
+def test_an_earlier_error_of_the_caller_is_not_reported(tide):
+    """An error that the program's own HIP call left behind is neither reported as
+    a layer call's nor taken from the program."""
+    import ctypes
+    with open("/proc/self/maps") as f:
+        hip = ctypes.CDLL(next(line.split()[-1] for line in f if "libamdhip64" in line))
+    L = Layer(tide, 40, 2, 4, 64, 32, 7)
+    L.step()
+    torch.cuda.synchronize()
+    want = L.results()
+    bad = hip.hipSetDevice(1 << 20)                      # refused by the runtime on the host
+    assert bad != 0
+    try:
+        L.step()
+        left = hip.hipGetLastError()
+    finally:
+        hip.hipGetLastError()
+    torch.cuda.synchronize()
+    assert left == bad and same(L.results(), want)
