@@ -123,7 +123,7 @@ __device__ __forceinline__ void store4(const Args& a, uint16_t* out, int64_t o, 
 }
 
 // Eight columns of a gradient. The empty statements keep the two stores from
-// being merged into one without the hint (128 experts of 768 x 2048: 216 us).
+// being merged into one without the hint (128 experts of 768 x 2048: 216 us instead of 166).
 template <bool kPastCaches>
 __device__ __forceinline__ void store_chunk(uint16_t* out, u32x4 v) {
     if constexpr (kPastCaches) {
@@ -151,7 +151,7 @@ __device__ __forceinline__ void store_chunk(uint16_t* out, u32x4 v) {
 // CU (576 x 2080 from 2067 rows 26 -> 20 us).
 // kSaved: x is a checkpoint, decoded on its way into LDS (exact, and free:
 // both forms run at 1150 TFLOP/s).
-// kTokens: there may be token indices (with kBuffers: there are).
+// kTokens: there are token indices (with kElements: there may be).
 template <int TO, int TI, bool kSaved, int kAccess, bool kTokens>
 struct Tile {
     static constexpr int kTeams = TO == 64 ? 4 : 1;
@@ -212,7 +212,7 @@ struct Tile {
     __device__ __forceinline__ int place_o(int r) const { return place<8>(r, a.O - o0); }
     __device__ __forceinline__ int place_i(int r) const { return place<kSaved ? 16 : 8>(r, a.I - i0); }
 
-    __device__ __forceinline__ bool indexed() const { return kTokens && (kAccess == kBuffers || a.tokens); }
+    __device__ __forceinline__ bool indexed() const { return kTokens && (kAccess != kElements || a.tokens); }
 
     // The tokens of the stage at t0, a row a lane (0 past the last row and
     // without token indices: no load uses those).
@@ -232,11 +232,11 @@ struct Tile {
             m.tok[j] = __builtin_amdgcn_ds_bpermute((j * (kThreads / CI) + tid / CI) * 4, of_lane);
         m.dropped = __ballot((uint32_t)of_lane >= (uint32_t)a.x_rows);
     }
-    // kOutside where the row of dy in chunk j of this thread is dropped, else 0.
-    __device__ __forceinline__ uint32_t dropped(const Moving& m, int j) const {
+    // kOutside where the row of dy in chunk j of this thread is one of `rows`, else 0.
+    __device__ __forceinline__ uint32_t is_of(uint64_t rows, int j) const {
         constexpr int R = kThreads / CO;
         static_assert(R <= 32 && 32 % R == 0 && kDepth <= 64, "the rows of a chunk are in one word");
-        const uint32_t w = (uint32_t)(m.dropped >> (j * R / 32 * 32));
+        const uint32_t w = (uint32_t)(rows >> (j * R / 32 * 32));
         return (w << (32 - R - j * R % 32) << (R - 1 - tid / CO)) & kOutside;
     }
 
@@ -254,12 +254,13 @@ struct Tile {
 #pragma unroll
             for (int j = kPart * NO / kOf; j < (kPart + 1) * NO / kOf; ++j)
                 m.o[j] = buffer16(d, (at + (uint32_t)(j * (kThreads / CO)) * (uint32_t)a.dy_stride * 2) |
-                                         (kDrop ? dropped(m, j) : 0));
+                                         (kDrop ? is_of(m.dropped, j) : 0));
         } else if constexpr (kAccess == kWide) {
+            const uint64_t gone = (kDrop ? m.dropped : 0) | (rows < 64 ? ~0ull << rows : 0);
 #pragma unroll
             for (int j = kPart * NO / kOf; j < (kPart + 1) * NO / kOf; ++j) {
                 const int t = j * (kThreads / CO) + tid / CO;
-                m.none = (m.none & ~(1u << j)) | (t < rows && !(kDrop && dropped(m, j)) ? 0 : 1u << j);
+                m.none = (m.none & ~(1u << j)) | is_of(gone, j) >> (31 - j);
                 m.o[j] = *gbl<u32x4_a2>(a.dy + min(t0 + t, hi - 1) * a.dy_stride + column_o());
             }
         } else {
@@ -268,7 +269,7 @@ struct Tile {
                 const int t = j * (kThreads / CO) + tid / CO, c = tid % CO;
                 const int64_t n = a.O - o0 - c * 8;
                 m.o[j] = u32x4{};
-                if (n > 0 && t < rows && !(kDrop && dropped(m, j)))
+                if (n > 0 && t < rows && !(kDrop && is_of(m.dropped, j)))
                     m.o[j] = load_row(a.dy + (t0 + t) * a.dy_stride + o0 + c * 8, (int)(n < 8 ? n : 8));
             }
         }
@@ -459,7 +460,7 @@ struct Tile {
             load_i<0, 1>(m, lo + kDepth);
             use_tokens(m, third_of);
 #pragma unroll
-            for (int j = 0; j < NO; ++j) first.o[j] &= (dropped(first, j) >> 31) - 1;
+            for (int j = 0; j < NO; ++j) first.o[j] &= (is_of(first.dropped, j) >> 31) - 1;
         } else {
             load_o<0, 1>(first, lo);
             load_i<0, 1>(first, lo);
@@ -708,7 +709,8 @@ hipError_t launch_tiles(const Args& a, const GradPtrs& g, Access how, hipStream_
         constexpr bool kSaved = saved.value;
         if (how == kBuffers && a.tokens) return start(weight_grads<TO, TI, kSaved, kBuffers, true>);
         if (how == kBuffers) return start(weight_grads<TO, TI, kSaved, kBuffers, false>);
-        if (how == kWide) return start(weight_grads<TO, TI, kSaved, kWide, true>);
+        if (how == kWide && a.tokens) return start(weight_grads<TO, TI, kSaved, kWide, true>);
+        if (how == kWide) return start(weight_grads<TO, TI, kSaved, kWide, false>);
         if constexpr (TO == 64)
             if (how == kElements) return start(weight_grads<TO, TI, kSaved, kElements, true>);
         return hipErrorInvalidConfiguration;           // plan_tiles and how_to_read disagree
