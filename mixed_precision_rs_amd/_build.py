@@ -2,6 +2,7 @@
 import os
 import subprocess
 import sys
+from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -34,10 +35,10 @@ def hipcc() -> str:
 
 
 def build(out: str = LIB, extra=(), verbose: bool = False) -> str:
-    objs = []
     bdir = os.path.join(ROOT, "_build")
     os.makedirs(bdir, exist_ok=True)
-    for src in SOURCES:
+
+    def compile_(src: str) -> str:
         obj = os.path.join(bdir, os.path.basename(src) + ".o")
         cmd = [hipcc(), *HIPCC_FLAGS, *extra, "-c", src, "-o", obj]
         if verbose:
@@ -45,7 +46,10 @@ def build(out: str = LIB, extra=(), verbose: bool = False) -> str:
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError("hipcc failed for %s:\n%s%s" % (src, r.stdout, r.stderr))
-        objs.append(obj)
+        return obj
+
+    with ThreadPoolExecutor(max_workers=4) as pool:
+        objs = list(pool.map(compile_, SOURCES))
     tmp = out + ".tmp%d" % os.getpid()
     # The DMA-engine path calls the HSA runtime directly.
     cmd = [hipcc(), "--offload-arch=gfx950", "-shared", "-fPIC", "-o", tmp, *objs,
