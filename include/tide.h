@@ -513,8 +513,7 @@ tide_status tide_plan_event_count(const tide_plan* plan, int64_t* events);
  *     next row is read or written.
  *   - They launch kernels on `stream` and nothing else (no device allocation,
  *     no copy, no wait), keep nothing between calls, and may be captured into a
- *     graph. Their stores are non-temporal. Two calls
- *     that may run at once need a workspace each.
+ *     graph. Two calls that may run at once need a workspace each.
  *   - Results do not depend on the order in which workgroups run: the same
  *     inputs give the same bits.
  *   - Index contents are checked by the kernels: an expert id outside
@@ -552,7 +551,8 @@ tide_status tide_route_workspace(int64_t tokens, int32_t k, int32_t experts, int
  *   token_of_row: tokens * k; the token of each row, rows from
  *               offsets[experts] on are left as they were.
  *   slots:      tokens x k; the row of each pair, -1 where it has none.
- *   workspace:  tide_route_workspace bytes (may be NULL when that is 0).
+ *   workspace:  tide_route_workspace bytes, 4-byte aligned (may be NULL when
+ *               that is 0).
  * Errors: INVALID_ARG, ALIGNMENT, UNSUPPORTED (as above), HIP.
  */
 tide_status tide_route_tokens(const void* experts_of, int32_t id_bytes, int64_t tokens, int32_t k,
@@ -619,7 +619,8 @@ tide_status tide_checkpoint_unpack(int32_t dtype, const tide_saved* saved, int64
 /*
  * The gated activation out = silu(gate) * up, silu(g) = g / (1 + exp(-g)), in
  * fp32, rounded once; in the same pass, where gate_saved / up_saved are not
- * NULL, the checkpoints of gate and up.
+ * NULL, the checkpoints of gate and up. (For gates below -87 the sigmoid is below
+ * fp32's normal range and has fewer bits, here and in the gradient.)
  * Errors: as tide_checkpoint_pack.
  */
 tide_status tide_gated_silu(int32_t dtype, const void* gate, int64_t gate_stride, const void* up,
@@ -658,7 +659,7 @@ tide_status tide_weight_grads_workspace(int64_t rows, int64_t out, int64_t in, i
  *            not read into any sum. An expert without rows gets zeros.
  *   token_of_row: rows device entries; NULL: row r of dy belongs to row r of x
  *            (x_rows >= rows). A row whose token is outside [0, x_rows) adds
- *            nothing.
+ *            nothing, whatever dy holds there.
  *   grads:   host array of `experts` device pointers, read during the call.
  *   accumulate: not 0: the sum is added to what grads holds, in fp32, before
  *            the rounding.

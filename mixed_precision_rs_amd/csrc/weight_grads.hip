@@ -139,18 +139,20 @@ __device__ __forceinline__ void store_chunk(uint16_t* out, u32x4 v) {
 // LDS as bf16, 64 or 32 at a time, and read back transposed
 // (ds_read_b64_tr_b16), since the matrix instruction wants the summed index
 // (the row) inside a lane; products are 32x32x16 bf16 with fp32 sums. The 256
-// tile has 8 waves of 128 x 64 (128 sums a lane, two waves a SIMD: 4 waves of
-// 128 x 128 leave every wait exposed and reach 1060 instead of 1200 TFLOP/s on
-// 8192 x 8192 x 8192), the 128 tile 4 of 64 x 64. The 256 x 128 tile has 4
+// tile has 8 waves of 128 x 64 (128 sums a lane, two waves a SIMD): 1300
+// TFLOP/s on 8192 x 8192 x 8192, where 4 waves of 128 x 128, which leave every
+// wait exposed, had 1060. The 128 tile has 4 of 64 x 64. The 256 x 128 tile has 4
 // waves of 128 x 64 and stages of 32 rows, so that two workgroups fit a CU: one
 // stores its tile while the other sums (128 experts of 768 x 2048, 32 rows
-// each: 77 us against 104 in tiles of 256). The 64 tile is for few
+// each: 67 us against 91 in tiles of 256). The 64 tile is for few
 // tiles: its 4 waves are teams of one, each with the whole tile, stages of its
 // own and a quarter of the rows, joined at the end through LDS; nothing but
 // that join waits on another wave. Stages of 32 rows let two workgroups fit a
-// CU (576 x 2080 from 2067 rows 26 -> 20 us).
-// kSaved: x is a checkpoint, decoded on its way into LDS (exact, and free:
-// both forms run at 1150 TFLOP/s).
+// CU (576 x 2080 from 2067 rows: 26 us in stages of 64, 19 so).
+// kSaved: x is a checkpoint, decoded on its way into LDS (exact, and free: 826
+// us on 8192 x 8192 x 8192, from bf16 841-849). The two chunks that a lane
+// decodes go to every other chunk of a row, which the counters show as bank
+// conflicts (17% of the LDS cycles of the 256 tile, 1% in its bf16 form).
 // kTokens: there are token indices (with kElements: there may be).
 template <int TO, int TI, bool kSaved, int kAccess, bool kTokens>
 struct Tile {
@@ -565,8 +567,8 @@ struct Tile {
     }
 
     // The tile goes through LDS so that whole rows are stored: row o's 16-byte
-    // chunk c lies at c ^ o, its halves swapped in every other 16 rows, so that
-    // neither the 8-byte writes nor the reads meet a bank twice.
+    // chunk c lies at c ^ o, its halves swapped in every other 16 rows, so that,
+    // by their addresses, neither the 8-byte writes nor the reads meet a bank twice.
     __device__ __forceinline__ void finish(f32x16 (&acc)[FO][FI], uint16_t* out) {
         const bool whole = o0 + TO <= a.O && i0 + TI <= a.I;
         if (whole) {
@@ -723,7 +725,7 @@ hipError_t launch_tiles(const Args& a, const GradPtrs& g, Access how, hipStream_
 
 // The buffers' 32-bit byte offsets have to reach a stage of dy and, with token
 // indices, all of x. Alignment does not matter to them: from 4096 rows, 4096 x
-// 4096 takes 143 us and 4095 x 4095, rows end to end, 134.
+// 4096 takes 112-117 us and 4095 x 4095, rows end to end, 125.
 Access how_to_read(const Args& a) {
     const int64_t step = a.codes ? 16 : 8, xs = a.codes ? a.codes_stride : a.x_stride * 2;
     const int64_t lim = kMostBytes, rows = a.tokens ? a.x_rows : kMostDepth;
@@ -734,31 +736,33 @@ Access how_to_read(const Args& a) {
 }
 
 // Whether the gradients are stored past the caches. It leaves those to dy and x
-// (128 experts of 512 x 1001, 128 rows each, 64 us against 82), but the lines
-// that two tiles share, where rows of the gradient do not start on lines, are
-// written twice. With few rows nothing is there to be left in: 128 experts of
-// 512 x 1001, 5 rows each, 57 us past the caches and 42-47 through them; 8192
-// x 8191 from 64 rows 61 and 44-54, 8192 x 12287 from 512 rows 148 and 147-170.
+// (128 experts of 767 x 2047, 128 rows each, 164 us against 178-180), but the
+// lines that two tiles share, where rows of the gradient do not start on lines,
+// are written twice. With few rows nothing is there to be left in: the same with
+// 64 rows each 166 us past the caches and 140-146 through them; 128 experts of
+// 512 x 1001 with 5 rows each 56 and 36-38, with 128 62 and 47-63, with 192 64
+// and 55-72; 8192 x 8191 from 64 rows 59 and 39.
 bool stores_past_caches(int64_t n, int64_t I, int32_t experts) {
     return I % 64 == 0 || n / experts > kMostDepth;
 }
 
-// Tile and splits. A large tile reuses each staged element more (1200, 1080,
-// 870 and 410 TFLOP/s on long sums, in tiles of 256 x 256, 256 x 128, 128 x 128
+// Tile and splits. A large tile reuses each staged element more (1300, 1150,
+// 990 and 480 TFLOP/s on long sums, in tiles of 256 x 256, 256 x 128, 128 x 128
 // and 64 x 64), a small one leaves fewer CUs idle and, with its teams, waits
-// less. The costs below, in us, are fits to measured times: a round of
+// less. The costs below, in us, were fitted to measured times: a round of
 // workgroups has a part that does not depend on the rows, and each stage of 64
 // rows adds to it. Both sides where the choice turns: 128 experts of 768 x 2048
-// with 512 rows each 255 us in 256 x 256 and 250 in 256 x 128, with 64 rows 112
-// and 92; 1024 x 8192 from 8192 rows 193 us (128 tiles of 256 x 256), 154 (256
-// of 256 x 128) and 158 (512 of 128 x 128); 8 experts of 384 x 700, 512 rows
-// each, 43 us (96 of 256 x 128) and 25 (144 of 128 x 128); 2048 x 2048 from
-// 2000 rows 36 us (1024 of 64 x 64) and 28 (256 of 128 x 128); 576 x 2080 from
-// 2067 rows 29 us (85 of 128 x 128) and 20 (297 of 64 x 64).
+// with 512 rows each 276-280 us in 256 x 256 and 276-297 in 256 x 128, with 64
+// rows 93 and 77; 1024 x 8192 from 8192 rows 152-154 us (128 tiles of 256 x 256),
+// 138-145 (256 of 256 x 128) and 147-151 (512 of 128 x 128); 8 experts of 384 x
+// 700, 512 rows each, 17 us (96 of 256 x 128) and 13 (144 of 128 x 128); 2048 x
+// 2048 from 2000 rows 35-37 us (1024 of 64 x 64) and 25-28 (256 of 128 x 128);
+// 576 x 2080 from 2067 rows 24 us (85 of 128 x 128) and 19 (297 of 64 x 64).
 // Splits: where even tiles of 64 leave CUs idle, the rows of each are divided
 // among several workgroups, whose fp32 sums a second kernel adds in order:
-// 128 x 2048 from 8192 rows 37 us with one, 24 with two, 17 with four, 19 with
-// eight.
+// 128 x 2048 from 8192 rows 29 us with one, 21 with two, 17 with four, 19 with
+// eight. The rows are taken as evenly spread over the experts: how many each
+// has is known on the device only.
 struct Plan {
     int64_t tiles_o, tiles_i;
     int tile_o, tile_i, splits;
