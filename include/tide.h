@@ -675,6 +675,221 @@ tide_status tide_weight_grads_bf16(const uint16_t* dy, int64_t dy_stride, int64_
                                    int32_t experts, uint16_t* const* grads, int32_t accumulate,
                                    void* workspace, int64_t workspace_bytes, void* stream);
 
+/*
+ * ---- The ends of the step, and what stands before its attention ---------------
+ *
+ * Token ids to rows of the embedding table and the table's gradient, norms and
+ * position rotation of queries and keys, the loss's log probabilities and their
+ * gradient, and the gradient norm with clipping. The gradients of the table and
+ * of the norms' weights are tensors that the reduce-scatter reads, the clipped
+ * tensors are what it leaves. The conventions of the section above hold here too.
+ */
+
+/* Bytes of device workspace tide_sort_ids needs. Host-only. Errors:
+ * INVALID_ARG; UNSUPPORTED (tokens or vocab past 2^31 - 1). */
+tide_status tide_sort_ids_workspace(int64_t tokens, int64_t vocab, int64_t* bytes);
+
+/*
+ * Sorts tokens by id, stably, for any vocabulary (tide_route_tokens sorts for up
+ * to 512 experts).
+ *   ids:     tokens ids of id_bytes (4 or 8: int32 or int64). An id outside
+ *            [0, vocab) (a padding token) has no place.
+ *   offsets: vocab + 1; id v's tokens are order[offsets[v] .. offsets[v+1] - 1].
+ *   order:   tokens; entries from offsets[vocab] on are left as they were.
+ *   workspace: tide_sort_ids_workspace bytes, 4-byte aligned; what it holds
+ *            does not matter.
+ * Errors: INVALID_ARG, ALIGNMENT, UNSUPPORTED (as above), HIP.
+ */
+tide_status tide_sort_ids(const void* ids, int32_t id_bytes, int64_t tokens, int64_t vocab,
+                          int32_t* offsets, int32_t* order, void* workspace,
+                          int64_t workspace_bytes, void* stream);
+
+/*
+ * Embedding lookup: out[t] = scale * table[ids[t]], the product in fp32, rounded
+ * once (scale 1 copies). table is vocab x width, out tokens x width. A token
+ * whose id is outside [0, vocab) gets zeros.
+ * Errors: INVALID_ARG, ALIGNMENT, OVERFLOW, HIP.
+ */
+tide_status tide_embed_tokens(int32_t dtype, const void* ids, int32_t id_bytes, int64_t tokens,
+                              const void* table, int64_t table_stride, int64_t vocab,
+                              int64_t width, float scale, void* out, int64_t out_stride,
+                              void* stream);
+
+/* Bytes of device workspace tide_embed_tokens_grad needs. Host-only. Errors:
+ * INVALID_ARG, OVERFLOW, UNSUPPORTED. */
+tide_status tide_embed_tokens_grad_workspace(int64_t tokens, int64_t width, int64_t* bytes);
+
+/*
+ * Gradient of tide_embed_tokens to the whole table: grad[v] = scale * sum of
+ * dout[order[i]], offsets[v] <= i < offsets[v+1], in that order's fixed
+ * grouping, in fp32, rounded once; zeros where id v has no token. With
+ * accumulate not 0 the sum is added to what grad holds, in fp32, before the
+ * rounding, and rows without a token are not touched.
+ *   dout: tokens x width; grad: vocab x width; offsets, order: from
+ *   tide_sort_ids (offsets are clamped to the tokens there are, an entry of
+ *   order outside [0, tokens) adds nothing).
+ *   workspace: tide_embed_tokens_grad_workspace bytes, 16-byte aligned; what it
+ *   holds does not matter.
+ * Errors: INVALID_ARG, ALIGNMENT, OVERFLOW, UNSUPPORTED (tokens or vocab past
+ * 2^31 - 1), HIP.
+ */
+tide_status tide_embed_tokens_grad(int32_t dtype, const void* dout, int64_t dout_stride,
+                                   int64_t tokens, int64_t width, const int32_t* offsets,
+                                   const int32_t* order, int64_t vocab, float scale, void* grad,
+                                   int64_t grad_stride, int32_t accumulate, void* workspace,
+                                   int64_t workspace_bytes, void* stream);
+
+/*
+ * Log probabilities of given tokens from logits (tokens x vocab), in one pass,
+ * in fp32. With m the largest logit of a row and s = sum exp(x - m):
+ *   logprob[t]  = x[target] - m - log(s); 0 where the target is outside
+ *                 [0, vocab) (a position that does not count).
+ *   stats[t]    = (m, log(s)), tokens x 2, for tide_token_logprobs_grad; may be
+ *                 NULL.
+ *   entropy[t]  = log(s) - sum exp(x - m) (x - m) / s; may be NULL.
+ *   top_ids, top_logprobs: tokens x top, the `top` (0 to 32) most probable
+ *                 tokens and their log probabilities, larger logits first, the
+ *                 lower id first where logits are equal; NULL when top is 0. A
+ *                 logit of -infinity or NaN is no alternative: where too few
+ *                 others are left, the id is -1 and the log probability
+ *                 -infinity.
+ * Logits of -infinity have probability 0 and add nothing to the entropy. A row
+ * in which every logit is -infinity (or without columns) has m = log(s) =
+ * -infinity, log probability -infinity and entropy 0. In a row that holds a NaN
+ * or +infinity, log(s), entropy and log probabilities are NaN.
+ *   targets: tokens ids of id_bytes (4 or 8: int32 or int64).
+ * Errors: INVALID_ARG, ALIGNMENT, OVERFLOW, UNSUPPORTED (vocab past 2^31 - 1,
+ * top past 32), HIP.
+ */
+tide_status tide_token_logprobs(int32_t dtype, const void* logits, int64_t logits_stride,
+                                int64_t tokens, int64_t vocab, const void* targets,
+                                int32_t id_bytes, float* logprob, float* stats, float* entropy,
+                                int32_t top, int32_t* top_ids, float* top_logprobs, void* stream);
+
+/*
+ * Gradient of tide_token_logprobs to the logits, in fp32, rounded once: with
+ * lp = x - stats[t][0] - stats[t][1] and p = exp(lp),
+ *   dlogits[t, i] = dlogprob[t] * ([i = target] - p) - dentropy[t] * p * (lp + entropy[t]).
+ * A row whose target is outside [0, vocab) has no first term, whatever
+ * dlogprob holds there; without dentropy (NULL; then entropy may be NULL) its
+ * logits are not read and its gradient is zeros, as is that of a row in which
+ * every logit is -infinity. dlogits may be logits itself (the same address and
+ * stride): the gradient then takes the logits' place.
+ * Errors: as tide_token_logprobs.
+ */
+tide_status tide_token_logprobs_grad(int32_t dtype, const void* logits, int64_t logits_stride,
+                                     int64_t tokens, int64_t vocab, const void* targets,
+                                     int32_t id_bytes, const float* stats, const float* dlogprob,
+                                     const float* entropy, const float* dentropy, void* dlogits,
+                                     int64_t dlogits_stride, void* stream);
+
+/* Heads of a projection: head h of token t starts at element
+ * t * token_stride + h * head_stride of data; its elements are adjacent. */
+typedef struct tide_heads {
+    void* data;
+    int64_t token_stride;
+    int64_t head_stride;
+    int32_t heads;
+    int32_t reserved;        /* must be 0 */
+} tide_heads;
+
+/* The rotation of tide_norm_rotate. */
+typedef struct tide_rotation {
+    const void* positions;   /* tokens ids of id_bytes: the row of cos and sin of each token; NULL:
+                                token t takes row t. A token whose position is outside
+                                [0, table_rows) is not rotated. */
+    const float* cos;        /* table_rows x pairs fp32, rows table_stride elements apart; */
+    const float* sin;        /* NULL (both) when pairs is 0 */
+    int64_t table_rows;
+    int64_t table_stride;
+    int32_t id_bytes;        /* 4 or 8 (int32 or int64) */
+    int32_t pairs;           /* the first 2 * pairs elements of a head are rotated */
+    int32_t adjacent;        /* 0: elements (i, i + pairs) are a pair, else (2i, 2i + 1) */
+    int32_t reserved;        /* must be 0 */
+} tide_rotation;
+
+/*
+ * Queries and keys normalised head by head and rotated by position, in one
+ * pass: y = x * weight / sqrt(mean(x^2) + eps), then each pair (a, b) of the
+ * first 2 * pairs elements becomes (a cos - b sin, a sin + b cos); in fp32,
+ * rounded once.
+ *   q, k, q_out, k_out: heads of `tokens` tokens and head_dim elements (even,
+ *     at most 512); k and k_out both NULL for queries alone. Strides are
+ *     at least head_dim; heads of one tensor do not share memory.
+ *   q_weight, k_weight: head_dim elements of the same type, NULL for ones.
+ *   rotation: NULL for none.
+ * Errors: INVALID_ARG, ALIGNMENT, OVERFLOW, UNSUPPORTED (head_dim), HIP.
+ */
+tide_status tide_norm_rotate(int32_t dtype, int64_t tokens, int32_t head_dim,
+                             const tide_heads* q, const tide_heads* k, const void* q_weight,
+                             const void* k_weight, float eps, const tide_rotation* rotation,
+                             const tide_heads* q_out, const tide_heads* k_out, void* stream);
+
+/* Bytes of device workspace tide_norm_rotate_grad needs (with weights'
+ * gradients). Host-only. Errors: INVALID_ARG, UNSUPPORTED. */
+tide_status tide_norm_rotate_grad_workspace(int64_t tokens, int32_t heads, int32_t head_dim,
+                                            int64_t* bytes);
+
+/*
+ * Gradient of tide_norm_rotate at the same q, k, weights and rotation. With g
+ * the rotation's transpose applied to dq_out, n = x / sqrt(mean(x^2) + eps) and
+ * r = 1 / sqrt(mean(x^2) + eps): dq = r * (g * weight - n * mean(g * weight * n)),
+ * dq_weight = sum over tokens and heads of g * n; likewise for k. In fp32, each
+ * rounded once; weights' gradients are of the same type as the weights.
+ *   dq_weight, dk_weight: may be NULL (not computed).
+ *   accumulate: not 0: the weights' gradients are added to what is there, in
+ *     fp32, before the rounding.
+ *   workspace: tide_norm_rotate_grad_workspace(tokens, q heads + k heads,
+ *     head_dim) bytes, 16-byte aligned, when a weight's gradient is asked for.
+ * Errors: as tide_norm_rotate.
+ */
+tide_status tide_norm_rotate_grad(int32_t dtype, int64_t tokens, int32_t head_dim,
+                                  const tide_heads* dq_out, const tide_heads* dk_out,
+                                  const tide_heads* q, const tide_heads* k, const void* q_weight,
+                                  const void* k_weight, float eps, const tide_rotation* rotation,
+                                  const tide_heads* dq, const tide_heads* dk, void* dq_weight,
+                                  void* dk_weight, int32_t accumulate, void* workspace,
+                                  int64_t workspace_bytes, void* stream);
+
+/* Bytes of device workspace tide_grad_squares needs for these sizes. Host-only.
+ * Errors: INVALID_ARG, OVERFLOW. */
+tide_status tide_grad_squares_workspace(int32_t dtype, const int64_t* elems, int32_t tensors,
+                                        int64_t* bytes);
+
+/*
+ * The square of the global gradient norm: *total = sum of x^2 over every element
+ * of every tensor, in fp64 (no square overflows or vanishes), in a fixed order;
+ * with accumulate not 0 it is added to *total. Where tensors are shards of
+ * several ranks, add the ranks' totals (an all-reduce of one fp64) before
+ * tide_clip_grads.
+ *   grads, elems: host arrays of `tensors` device pointers and element counts,
+ *     read during the call; an entry with 0 elements may be NULL. A tensor may
+ *     be named twice (and then counts twice).
+ *   total: one fp64 on the device, 8-byte aligned.
+ *   workspace: tide_grad_squares_workspace bytes, 8-byte aligned; what it holds
+ *     does not matter.
+ * Errors: INVALID_ARG, ALIGNMENT, OVERFLOW, HIP.
+ */
+tide_status tide_grad_squares(int32_t dtype, const void* const* grads, const int64_t* elems,
+                              int32_t tensors, double* total, int32_t accumulate, void* workspace,
+                              int64_t workspace_bytes, void* stream);
+
+/*
+ * Clips gradients by their global norm: with norm = sqrt(*total), out[i] =
+ * grads[i] * min(1, max_norm / norm), the factor in fp64, the product rounded
+ * once to fp32 and, for bf16, once more to bf16. Where norm is at most max_norm, 0 or
+ * not finite, the factor is 1 (a caller that skips such a step looks at *norm).
+ *   out: host array of device pointers, the sizes of grads; NULL or an entry
+ *     equal to grads[i]: in place (then nothing is read or written where the
+ *     factor is 1). No tensor written may share memory with another one.
+ *   norm: one fp32 on the device that receives the norm; may be NULL.
+ *   max_norm: at least 0.
+ * Errors: INVALID_ARG, ALIGNMENT, OVERFLOW, NO_MEMORY, HIP.
+ */
+tide_status tide_clip_grads(int32_t dtype, const void* const* grads, const int64_t* elems,
+                            int32_t tensors, const double* total, double max_norm,
+                            void* const* out, float* norm, void* stream);
+
 /* Static text for a status code. */
 const char* tide_status_string(tide_status status);
 

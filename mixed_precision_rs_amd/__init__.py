@@ -2,7 +2,9 @@
 bf16 -> fp32 reduce-scatter into padded rank-major shards and the all-gather
 placement into parameter storage (C ABI in include/tide.h, HIP kernels for
 gfx950 in csrc/), and the training layer beside them: tokens sorted by expert
-and back, 8-bit activation checkpoints, and weight gradients from them.
+and back, 8-bit activation checkpoints, and weight gradients from them; at the
+step's ends embedding, log probabilities, gradient norm and clipping, and norm
+and rotation of queries and keys.
 Importing this package loads libtide.so and fails loudly if it has not been
 built."""
 from ._lib import (  # noqa: F401
@@ -60,6 +62,23 @@ from ._layer import (  # noqa: F401
     route_workspace_bytes,
     weight_grads_bf16,
     weight_grads_workspace_bytes,
+)
+
+from ._step import (  # noqa: F401
+    TensorTable,
+    clip_grads,
+    embed_tokens,
+    embed_tokens_grad,
+    embed_tokens_grad_workspace_bytes,
+    grad_squares,
+    grad_squares_workspace_bytes,
+    norm_rotate,
+    norm_rotate_grad,
+    norm_rotate_grad_workspace_bytes,
+    sort_ids,
+    sort_ids_workspace_bytes,
+    token_logprobs,
+    token_logprobs_grad,
 )
 
 lib()  # load now: no silent fallback exists

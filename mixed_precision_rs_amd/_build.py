@@ -11,7 +11,9 @@ LIB = os.path.join(HERE, "libtide.so")
 SOURCES = [os.path.join(CSRC, "kernels.hip"), os.path.join(CSRC, "plan.cpp"),
            os.path.join(CSRC, "sdma.cpp"), os.path.join(CSRC, "noalloc.hip"),
            os.path.join(CSRC, "host.cpp"), os.path.join(CSRC, "tokens.hip"), os.path.join(CSRC, "checkpoint.hip"),
-           os.path.join(CSRC, "weight_grads.hip")]
+           os.path.join(CSRC, "weight_grads.hip"), os.path.join(CSRC, "embedding.hip"),
+           os.path.join(CSRC, "logprobs.hip"), os.path.join(CSRC, "heads.hip"),
+           os.path.join(CSRC, "grad_norm.hip")]
 HEADERS = [os.path.join(CSRC, "tide_internal.hpp"), os.path.join(CSRC, "sdma.hpp"),
            os.path.join(CSRC, "host.hpp"), os.path.join(CSRC, "device.hpp"),
            os.path.join(ROOT, "include", "tide.h")]

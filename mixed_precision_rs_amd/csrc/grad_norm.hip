@@ -1,0 +1,272 @@
+// The square of the gradient norm over many tensors (tide_grad_squares) and
+// clipping by it (tide_clip_grads) for gfx950.
+//
+// Tensors are cut into tiles of kTile elements, and the workgroups walk the
+// tiles; which workgroup has which tile follows from the sizes alone, so the
+// sum does not depend on when they run. Squares and sums are fp64: a square of
+// an fp32 number is exact in it, and neither overflows nor vanishes.
+#include <algorithm>
+#include <climits>
+#include <vector>
+
+#include "device.hpp"
+#include "host.hpp"
+
+using namespace tide;
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kTile = 16384;           // elements
+constexpr int kMostTensors = 128;      // in one launch's arguments
+constexpr int64_t kMostGroups = 2048;
+
+struct Tensors {
+    const void* in[kMostTensors];
+    void* out[kMostTensors];
+    int64_t elems[kMostTensors];
+    int32_t first[kMostTensors];       // first tile
+    int32_t count, tiles;
+};
+
+__device__ __forceinline__ int tensor_of(const Tensors& a, int tile) {
+    int lo = 0, hi = a.count - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) / 2;
+        if (a.first[mid] <= tile) lo = mid;
+        else hi = mid - 1;
+    }
+    return lo;
+}
+
+__device__ __forceinline__ double block_sum(double v) {
+    __shared__ double part[kThreads / 64];
+#pragma unroll
+    for (int d = 32; d > 0; d >>= 1) v += __shfl_xor(v, d);
+    if ((threadIdx.x & 63) == 0) part[threadIdx.x / 64] = v;
+    __syncthreads();
+    v = 0.0;
+#pragma unroll
+    for (int w = 0; w < kThreads / 64; ++w) v += part[w];
+    return v;
+}
+
+// Calls f(pointer index base, elements left, tensor) for this thread's vectors of a tile.
+template <class T, class F>
+__device__ __forceinline__ void each_vector(const Tensors& a, int tile, F&& f) {
+    constexpr int N = kVecOf<T>;
+    const int i = tensor_of(a, tile);
+    const int64_t lo = (int64_t)(tile - a.first[i]) * kTile;
+    const int64_t hi = a.elems[i] - lo < kTile ? a.elems[i] : lo + kTile;
+#pragma unroll 4
+    for (int64_t e = lo + threadIdx.x * N; e < hi; e += kThreads * N)
+        f(i, e, hi - e < N ? (int)(hi - e) : N);
+}
+
+template <class T>
+__global__ __launch_bounds__(kThreads) void sum_squares(Tensors a, double* partial) {
+    constexpr int N = kVecOf<T>;
+    double sum = 0.0;
+    for (int tile = blockIdx.x; tile < a.tiles; tile += gridDim.x)
+        each_vector<T>(a, tile, [&](int i, int64_t e, int n) {
+            float v[N];
+            widen(load_row((const T*)a.in[i] + e, n), v);
+#pragma unroll
+            for (int c = 0; c < N; ++c) sum = __builtin_fma((double)v[c], (double)v[c], sum);
+        });
+    sum = block_sum(sum);
+    if (threadIdx.x == 0) *gbl_mut<double>(partial + blockIdx.x) = sum;
+}
+
+__global__ __launch_bounds__(kThreads) void sum_partials(const double* partial, int64_t n,
+                                                         double* total, int accumulate) {
+    double sum = 0.0;
+    for (int64_t i = threadIdx.x; i < n; i += kThreads) sum += *gbl<double>(partial + i);
+    sum = block_sum(sum);
+    if (threadIdx.x == 0) *gbl_mut<double>(total) = accumulate ? *gbl<double>(total) + sum : sum;
+}
+
+template <class T>
+__global__ __launch_bounds__(kThreads) void clip(Tensors a, const double* total, double most, float* norm_to) {
+    constexpr int N = kVecOf<T>;
+    const double norm = sqrt(*gbl<double>(total));
+    if (norm_to && blockIdx.x == 0 && threadIdx.x == 0) *gbl_mut<float>(norm_to) = (float)norm;
+    const bool scaled = norm > most && norm < __builtin_inf();
+    const double factor = most / norm;
+    for (int tile = blockIdx.x; tile < a.tiles; tile += gridDim.x)
+        each_vector<T>(a, tile, [&](int i, int64_t e, int n) {
+            if (!scaled && a.in[i] == a.out[i]) return;
+            u32x4 raw = load_row((const T*)a.in[i] + e, n);
+            if (scaled) {
+                float v[N];
+                widen(raw, v);
+#pragma unroll
+                for (int c = 0; c < N; ++c) v[c] = (float)((double)v[c] * factor);
+                raw = narrow(v);
+            }
+            store_row((T*)a.out[i] + e, n, raw);
+        });
+}
+
+tide_status check_sizes(int32_t dtype, const int64_t* elems, int32_t tensors) {
+    if (dtype != TIDE_DTYPE_BF16 && dtype != TIDE_DTYPE_FP32)
+        return fail(TIDE_ERR_INVALID_ARG, "dtype %d is not BF16 (0) or FP32 (1)", dtype);
+    if (tensors < 0) return fail(TIDE_ERR_INVALID_ARG, "negative tensor count");
+    if (tensors && !elems) return fail(TIDE_ERR_INVALID_ARG, "elems is NULL");
+    int64_t all = 0;
+    for (int32_t i = 0; i < tensors; ++i) {
+        if (elems[i] < 0) return fail(TIDE_ERR_INVALID_ARG, "elems[%d] is negative", i);
+        if (__builtin_add_overflow(all, elems[i], &all) || all > INT64_MAX / 8)
+            return fail(TIDE_ERR_OVERFLOW, "the tensors' sizes overflow int64");
+    }
+    return TIDE_OK;
+}
+
+// Calls go(Tensors, workgroups, workgroups before) for each launch: up to
+// kMostTensors tensors and 2^30 tiles (a larger tensor is cut).
+template <class F>
+hipError_t each_launch(const void* const* in, void* const* out, const int64_t* elems, int32_t tensors,
+                       int32_t size, F&& go) {
+    constexpr int64_t kMostTiles = (int64_t)1 << 30;
+    Tensors a{};
+    int64_t tiles = 0, groups = 0;
+    const auto flush = [&]() -> hipError_t {
+        if (a.count == 0) return hipSuccess;
+        a.tiles = (int32_t)tiles;
+        const int64_t g = tiles < kMostGroups ? tiles : kMostGroups;
+        const hipError_t e = go(a, g, groups);
+        groups += g;
+        a.count = 0;
+        tiles = 0;
+        return e;
+    };
+    for (int32_t i = 0; i < tensors; ++i) {
+        for (int64_t at = 0; at < elems[i];) {
+            const int64_t left = elems[i] - at;
+            const int64_t n = left < kMostTiles * kTile ? left : kMostTiles * kTile;
+            const int64_t t = (n + kTile - 1) / kTile;
+            if (a.count == kMostTensors || tiles + t > kMostTiles) {
+                const hipError_t e = flush();
+                if (e != hipSuccess) return e;
+            }
+            a.in[a.count] = in ? (const char*)in[i] + at * size : nullptr;
+            a.out[a.count] = out ? (char*)out[i] + at * size : (void*)a.in[a.count];
+            a.elems[a.count] = n;
+            a.first[a.count] = (int32_t)tiles;
+            ++a.count;
+            tiles += t;
+            at += n;
+        }
+    }
+    return flush();
+}
+
+}  // namespace
+
+extern "C" {
+
+tide_status tide_grad_squares_workspace(int32_t dtype, const int64_t* elems, int32_t tensors,
+                                        int64_t* bytes) {
+    return guarded([&]() -> tide_status {
+        if (!bytes) return fail(TIDE_ERR_INVALID_ARG, "bytes is NULL");
+        TIDE_TRY(check_sizes(dtype, elems, tensors));
+        int64_t groups = 0;
+        (void)each_launch(nullptr, nullptr, elems, tensors, 0, [&](const Tensors&, int64_t g, int64_t) {
+            groups += g;
+            return hipSuccess;
+        });
+        *bytes = groups * 8;
+        return TIDE_OK;
+    });
+}
+
+tide_status tide_grad_squares(int32_t dtype, const void* const* grads, const int64_t* elems,
+                              int32_t tensors, double* total, int32_t accumulate, void* workspace,
+                              int64_t workspace_bytes, void* stream) {
+    return guarded([&]() -> tide_status {
+        int64_t need = 0;
+        TIDE_TRY(tide_grad_squares_workspace(dtype, elems, tensors, &need));
+        if (need > 0 && (!workspace || workspace_bytes < need))
+            return fail(TIDE_ERR_INVALID_ARG, "workspace holds %lld bytes, %lld needed",
+                        (long long)(workspace ? workspace_bytes : 0), (long long)need);
+        if (tensors && !grads) return fail(TIDE_ERR_INVALID_ARG, "grads is NULL");
+        const int32_t size = dtype == TIDE_DTYPE_FP32 ? 4 : 2;
+        Mat wr[2];
+        TIDE_TRY(matrix("total", total, 1, 1, 1, 8, &wr[0]));
+        TIDE_TRY(matrix("workspace", workspace, 1, need / 8, need / 8, 8, &wr[1]));
+        TIDE_TRY(no_overlap(wr, 2, nullptr, 0));
+        for (int32_t i = 0; i < tensors; ++i) {
+            Mat rd;
+            TIDE_TRY(matrix("one of the grads", grads[i], 1, elems[i], elems[i], size, &rd));
+            TIDE_TRY(no_overlap(wr, 2, &rd, 1));
+        }
+        return on_stream(stream, [&](hipStream_t s) {
+            const hipError_t e = each_launch(grads, nullptr, elems, tensors, size,
+                                             [&](const Tensors& a, int64_t groups, int64_t before) {
+                double* to = (double*)workspace + before;
+                const dim3 grid((uint32_t)groups);
+                return size == 2 ? enqueue(sum_squares<uint16_t>, grid, kThreads, 0, s, a, to)
+                                 : enqueue(sum_squares<float>, grid, kThreads, 0, s, a, to);
+            });
+            if (e != hipSuccess) return e;
+            return enqueue(sum_partials, dim3(1), kThreads, 0, s, (const double*)workspace, need / 8, total,
+                           accumulate ? 1 : 0);
+        });
+    });
+}
+
+tide_status tide_clip_grads(int32_t dtype, const void* const* grads, const int64_t* elems,
+                            int32_t tensors, const double* total, double max_norm,
+                            void* const* out, float* norm, void* stream) {
+    return guarded([&]() -> tide_status {
+        TIDE_TRY(check_sizes(dtype, elems, tensors));
+        if (!(max_norm >= 0.0)) return fail(TIDE_ERR_INVALID_ARG, "max_norm has to be 0 or more");
+        if (tensors && !grads) return fail(TIDE_ERR_INVALID_ARG, "grads is NULL");
+        const int32_t size = dtype == TIDE_DTYPE_FP32 ? 4 : 2;
+        Mat rd[1], small[1];
+        TIDE_TRY(matrix("total", total, 1, 1, 1, 8, &rd[0]));
+        TIDE_TRY(matrix("norm", norm, norm ? 1 : 0, 1, 1, 4, &small[0]));
+        TIDE_TRY(no_overlap(small, 1, rd, 1));
+        // Every range that is read or written, in order of address: one that is
+        // written shares no byte with another, but for a tensor in place.
+        struct Range {
+            uintptr_t lo, hi;
+            bool written;
+        };
+        std::vector<Range> at;
+        at.reserve(2 * (size_t)tensors + 2);
+        at.push_back(Range{rd[0].base, rd[0].base + 8, false});
+        if (norm) at.push_back(Range{small[0].base, small[0].base + 4, true});
+        for (int32_t i = 0; i < tensors; ++i) {
+            Mat a, b;
+            TIDE_TRY(matrix("one of the grads", grads[i], 1, elems[i], elems[i], size, &a));
+            TIDE_TRY(matrix("one of the outputs", out ? out[i] : grads[i], 1, elems[i], elems[i], size, &b));
+            if (a.rows == 0) continue;
+            if (a.base != b.base) at.push_back(Range{a.base, a.base + (uintptr_t)a.width, false});
+            at.push_back(Range{b.base, b.base + (uintptr_t)b.width, true});
+        }
+        std::sort(at.begin(), at.end(), [](const Range& a, const Range& b) { return a.lo < b.lo; });
+        uintptr_t end = 0, written_end = 0;
+        for (const Range& r : at) {
+            if (r.lo < (r.written ? end : written_end))
+                return fail(TIDE_ERR_INVALID_ARG, "a tensor that is written overlaps another one");
+            end = std::max(end, r.hi);
+            if (r.written) written_end = std::max(written_end, r.hi);
+        }
+        return on_stream(stream, [&](hipStream_t s) {
+            bool first = true;
+            const hipError_t e = each_launch(grads, out, elems, tensors, size,
+                                             [&](const Tensors& a, int64_t groups, int64_t) {
+                float* to = first ? norm : nullptr;
+                first = false;
+                const dim3 grid((uint32_t)groups);
+                return size == 2 ? enqueue(clip<uint16_t>, grid, kThreads, 0, s, a, total, max_norm, to)
+                                 : enqueue(clip<float>, grid, kThreads, 0, s, a, total, max_norm, to);
+            });
+            if (e != hipSuccess || !first || !norm) return e;
+            return enqueue(clip<float>, dim3(1), kThreads, 0, s, Tensors{}, total, max_norm, norm);
+        });
+    });
+}
+
+}  // extern "C"

@@ -1,0 +1,232 @@
+"""Log probabilities, entropy and alternatives, and the gradient to the logits,
+against the definition in 64 bits on the CPU."""
+import math
+
+import pytest
+import torch
+
+import layer_reference as ref
+import step_reference as step
+from gpu_util import dev, say
+
+pytestmark = pytest.mark.gpu
+BF16, F32 = torch.bfloat16, torch.float32
+INF, NAN = math.inf, math.nan
+
+
+@pytest.fixture(scope="module")
+def tide():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    import mixed_precision_rs_amd as t
+    return t
+
+
+def window(t, pad, fill=NAN):
+    b = torch.full((t.shape[0], t.shape[1] + pad), fill, dtype=torch.float32).to(t.dtype).to(dev())
+    w = b[:, pad // 2: pad // 2 + t.shape[1]]
+    w.copy_(t.to(dev()))
+    return w
+
+
+def run(tide, x, targets, top=0, pad=0, **kw):
+    T = x.shape[0]
+    f = lambda *s: torch.full(s, 55.0, device=dev())  # noqa: E731
+    got = {"logprob": f(T), "stats": f(T, 2), "entropy": f(T)}
+    if top:
+        got.update(top_ids=torch.full((T, top), 55, dtype=torch.int32, device=dev()), top_logprobs=f(T, top))
+    tide.token_logprobs(window(x, pad), targets.to(dev()), **got, **kw)
+    return got
+
+
+def check(got, want, top, what):
+    ref.close(got["logprob"], want["logprob"], want["d_logprob"], what + " logprob")
+    bad = torch.isnan(want["log_s"])
+    ref.close(got["stats"][:, 1], want["log_s"], want["d_log_s"], what + " log s")
+    assert torch.equal(got["stats"][:, 0].cpu()[~bad].double(), want["m"][~bad]), what
+    ref.close(got["entropy"], want["entropy"], want["d_entropy"], what + " entropy")
+    if top:
+        assert torch.equal(got["top_ids"].cpu(), want["top_ids"]), what
+        ref.close(got["top_logprobs"], want["top_logprobs"], want["d_top"], what + " alternatives")
+
+
+def some_targets(T, V, seed, dtype=torch.int64):
+    g = torch.Generator().manual_seed(seed)
+    t = torch.randint(0, max(V, 1), (T,), generator=g)
+    t[::5] = -100
+    if T > 3:
+        t[3] = V
+    if T > 8 and dtype == torch.int64:
+        t[8] = 2 ** 33
+    return t.to(dtype)
+
+
+SHAPES = [(1, 1, 1), (2, 3, 5), (3, 7, 2), (4, 8, 0), (9, 64, 8), (5, 65, 32), (11, 1000, 20), (3, 2047, 7), (2, 2048, 1),
+          (6, 8193, 3), (3, 50001, 20), (2, 131072, 8), (0, 10, 2), (3, 0, 2)]
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("pad", [0, 3])
+@pytest.mark.parametrize("T,V,top", SHAPES)
+def test_forward(tide, T, V, top, pad, dtype):
+    say("logprobs", T, V, top, pad, dtype)
+    x = ref.normal((T, V), dtype, T + V, 3.0)
+    targets = some_targets(T, V, V, torch.int32 if pad else torch.int64)
+    if V == 0:
+        targets = targets.clamp(max=-1)
+    check(run(tide, x, targets, top, pad), step.logprobs(x, targets, top), top, "normal")
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("V", [5, 300, 9000])
+def test_rows_of_masks_infinities_and_nan(tide, V, dtype):
+    g = torch.Generator().manual_seed(V)
+    low = torch.finfo(dtype).min
+    x = torch.randn(14, V, generator=g)
+    x[0] = -INF                                         # nothing is left
+    x[1, : V - 2] = -INF
+    x[2] = low
+    x[3, 1:] = low
+    x[4, V // 2] = NAN
+    x[5, V - 1] = INF
+    x[6] = INF
+    x[7, 0] = torch.finfo(dtype).max
+    x[8] = -INF
+    x[8, V - 1] = -3.0
+    x[9] = NAN
+    x[10] = x[10] * 1e30
+    x[11, ::2] = -INF
+    x[12] = 4.0                                         # all equal
+    x[13] = torch.randint(-2, 3, (V,), generator=g).float()   # many equal
+    x = x.to(dtype)
+    targets = torch.randint(0, V, (14,), generator=g)
+    for t in (targets, torch.full((14,), V - 1), torch.full((14,), -1)):
+        check(run(tide, x, t, 6), step.logprobs(x, t, 6), 6, "odd rows")
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_alternatives_that_one_lane_or_one_stretch_holds(tide, dtype):
+    """The largest logits side by side, at every multiple of a power of two, rising
+    and falling through the row, or all equal: whatever share of a row a lane has,
+    one of these puts more alternatives into it than others hold."""
+    V, top = 40000, 32
+    rows = []
+    for stride in (1, 2, 4, 8, 16, 32, 64, 128, 256, 512, 1024, 2048, 4096, 8192):
+        x = torch.zeros(V)
+        at = torch.arange(0, V, stride)[:40]
+        x[at] = 5.0 + torch.arange(len(at)).float() % 7
+        rows.append(x)
+    rows += [torch.linspace(-4, 4, V), torch.linspace(4, -4, V), torch.zeros(V), torch.full((V,), -INF)]
+    rows[-1][V - 20:] = 1.0
+    for lanes in (64, 256, 512, 1024):                   # one lane's vectors rise, all others are low
+        x = torch.full((V,), -9.0)
+        n = 16 // dtype.itemsize
+        for i, u in enumerate(range(3, V // n, lanes)):
+            x[u * n: u * n + n] = torch.arange(n).float() / 8 + i % 3
+        rows.append(x)
+    x = torch.stack(rows).to(dtype)
+    t = torch.arange(len(rows))
+    check(run(tide, x, t, top), step.logprobs(x, t, top), top, "stretches")
+
+
+def test_outputs_left_out(tide):
+    x, t = ref.normal((5, 777), BF16, 1), some_targets(5, 777, 1)
+    full = run(tide, x, t, 4)
+    lp = torch.empty(5, device=dev())
+    tide.token_logprobs(x.to(dev()), t.to(dev()), lp)
+    assert torch.equal(lp, full["logprob"])
+    again = run(tide, x, t, 4)
+    assert all(torch.equal(full[k], again[k]) for k in full)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("pad", [0, 3])
+@pytest.mark.parametrize("T,V", [(1, 1), (2, 3), (9, 64), (5, 65), (11, 1000), (3, 2047), (2, 50001), (0, 8), (3, 0)])
+def test_gradient(tide, T, V, pad, dtype):
+    say("logprobs gradient", T, V, pad, dtype)
+    x = ref.normal((T, V), dtype, T + V, 3.0)
+    targets = some_targets(T, V, V, torch.int32 if pad else torch.int64)
+    if V == 0:
+        targets = targets.clamp(max=-1)
+    got = run(tide, x, targets)
+    d, h = ref.normal((T,), F32, 3), ref.normal((T,), F32, 4)
+    d[::5] = NAN                                        # those rows' targets do not count
+    for with_h in (False, True):
+        kw = {"entropy": got["entropy"], "dentropy": h.to(dev())} if with_h else {}
+        want, lim = step.logprobs_grad(x, targets, got["stats"].cpu(), d, got["entropy"].cpu(), h if with_h else None)
+        lim = lim + (step.HALF[dtype] + 2 * step.U) * want.abs()
+        whole = torch.full((T, V + pad), 3.0, dtype=dtype, device=dev())
+        dx = whole[:, pad // 2: pad // 2 + V]
+        tide.token_logprobs_grad(window(x, pad), targets.to(dev()), got["stats"], d.to(dev()), dx, **kw)
+        ref.close(dx, want, lim, "gradient")
+        if pad:
+            w = whole.cpu()
+            assert (w[:, : pad // 2] == 3.0).all() and (w[:, pad // 2 + V:] == 3.0).all()
+        place = window(x, pad)
+        tide.token_logprobs_grad(place, targets.to(dev()), got["stats"], d.to(dev()), place, **kw)
+        assert torch.equal(place, dx), "in place"
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_gradient_of_masked_rows(tide, dtype):
+    V = 300
+    x = ref.normal((6, V), F32, 1)
+    x[0] = -INF
+    x[1, 7:] = -INF
+    x[2] = torch.finfo(dtype).min
+    x[3, ::2] = -INF
+    x = x.to(dtype)
+    t = torch.tensor([3, 2, 9, 1, 5, -1])
+    got = run(tide, x, t)
+    d, h = ref.normal((6,), F32, 3), ref.normal((6,), F32, 4)
+    want, lim = step.logprobs_grad(x, t, got["stats"].cpu(), d, got["entropy"].cpu(), h)
+    dx = torch.empty(6, V, dtype=dtype, device=dev())
+    tide.token_logprobs_grad(x.to(dev()), t.to(dev()), got["stats"], d.to(dev()), dx, entropy=got["entropy"], dentropy=h.to(dev()))
+    ref.close(dx, want, lim + (step.HALF[dtype] + 2 * step.U) * want.abs(), "masked")
+    assert not dx[0].any()
+    x = ref.normal((3, V), F32, 1)
+    x[0, 5], x[1, 6] = NAN, INF
+    got = run(tide, x, t[1:4])
+    dx = torch.empty(3, V, device=dev())
+    tide.token_logprobs_grad(x.to(dev()), t[1:4].to(dev()), got["stats"], d[:3].to(dev()), dx)
+    assert torch.isnan(dx[:2]).all() and torch.isfinite(dx[2]).all()
+
+
+def test_gradient_against_differences(tide):
+    """sum_t d_t logprob_t + h_t entropy_t at logits a step apart, in 64 bits."""
+    T, V, eps = 4, 60, 1e-5
+    x, t = ref.normal((T, V), F32, 5, 2.0), torch.tensor([3, 59, -1, 0])
+    d, h = ref.normal((T,), F32, 6), ref.normal((T,), F32, 7)
+
+    def value(y):
+        lp = torch.log_softmax(y, 1)
+        at = torch.where(t >= 0, t, 0)
+        return (torch.where(t >= 0, lp.gather(1, at[:, None])[:, 0], 0.0) * d.double()).sum() - (lp.exp() * lp).sum(1) @ h.double()
+
+    got = run(tide, x, t)
+    dx = torch.empty(T, V, device=dev())
+    tide.token_logprobs_grad(x.to(dev()), t.to(dev()), got["stats"], d.to(dev()), dx, entropy=got["entropy"], dentropy=h.to(dev()))
+    for r, c in ((0, 3), (0, 10), (1, 59), (2, 7), (3, 0), (3, 30)):
+        up, down = x.double().clone(), x.double().clone()
+        up[r, c] += eps
+        down[r, c] -= eps
+        diff = float(value(up) - value(down)) / (2 * eps)
+        # the third derivative times eps^2 is below 1e-9, fp32 inputs of the gradient are off by 1e-6
+        assert abs(float(dx[r, c]) - diff) < 2e-5 * (1 + float(d[r].abs() + h[r].abs())), (r, c)
+
+
+def test_rows_past_two_gib(tide):
+    T, V = 9, 1 << 28
+    x = torch.zeros(T, V, dtype=BF16, device=dev())
+    x[8, V - 1], x[8, 3] = 21.0, 20.5
+    t = torch.full((T,), V - 1, device=dev())
+    lp, st, H = (torch.empty(s, device=dev()) for s in ((T,), (T, 2), (T,)))
+    ids, tops = torch.empty(T, 2, dtype=torch.int32, device=dev()), torch.empty(T, 2, device=dev())
+    tide.token_logprobs(x, t, lp, stats=st, entropy=H, top_ids=ids, top_logprobs=tops)
+    s8 = 1 + math.exp(-0.5) + (V - 2) * math.exp(-21.0)
+    room = (V / 16 + 30) * step.U                        # the reference's bound; here most of it is the sum of equal terms
+    assert ids[8].tolist() == [V - 1, 3] and ids[7].tolist() == [0, 1]
+    assert abs(float(lp[8]) + math.log(s8)) < 1e-3 and abs(float(lp[0]) + math.log(V)) < min(room, 1e-3)
+    d = torch.ones(T, device=dev())
+    tide.token_logprobs_grad(x, t, st, d, x)
+    assert abs(float(x[8, V - 1]) - (1 - 1 / s8)) < 2 ** -8 and abs(float(x[8, 3]) + math.exp(-0.5) / s8) < 2 ** -8
