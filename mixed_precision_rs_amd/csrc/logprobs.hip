@@ -4,9 +4,11 @@
 //
 // A row's maximum m, s = sum exp(x - m) and t = sum exp(x - m) (x - m) come from
 // one pass: each lane keeps the three over its own logits, t and s brought to the
-// new maximum when it rises, and a fixed tree joins the lanes.
+// new maximum when it rises, and a fixed tree joins the lanes. Logits are read
+// once; what bounds the pass besides is the exponential (a quarter of the rate of
+// other instructions) and the five to six instructions around it.
 #include <climits>
-#include <cmath>
+#include <type_traits>
 
 #include "device.hpp"
 #include "host.hpp"
@@ -15,28 +17,31 @@ using namespace tide;
 
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kWaves = kThreads / 64;
 constexpr int kMostTop = 32;
-constexpr float kLog2e = 0x1.715476p+0f;
+constexpr float kLog2e = 0x1.715476p+0f, kLn2 = 0x1.62e43p-1f;
 constexpr float kNegInf = -__builtin_inff();
 // A lane's maximum starts here, not at -infinity: x - m is then never
 // -infinity - -infinity, and logits of -infinity have exp 0.
 constexpr float kLowest = -__FLT_MAX__;
-// exp(-200) is 0 in fp32: differences are held above it where they are
-// factors, so that 0 * -infinity does not arise.
-constexpr float kFar = -200.0f;
+// Up to this magnitude what the rounding of m log2(e) takes is below 2^-8.
+constexpr float kTame = 65536.0f;
+// exp(-200) is 0 in fp32: differences (and exponents of 2) are held above these
+// where they are factors, so that 0 * -infinity does not arise.
+constexpr float kFar = -200.0f, kFar2 = -300.0f;
 
 // exp(z) for z <= 0; a NaN or +infinity - +infinity stays NaN.
 __device__ __forceinline__ float exp_of(float z) { return __builtin_amdgcn_exp2f(z * kLog2e); }
 
+// s and t in 64 bits: a confident row has s = 1 + little, and log(s) is that little.
 struct Sums {
-    float m, s, t;
+    float m;
+    double s, t;
 };
 // t of a sum whose maximum rises by -d: sum e (z + d) = t + s d.
 __device__ __forceinline__ void rise(Sums& a, float m) {
-    const float d = fmaxf(a.m - m, kFar), f = exp_of(d);
-    a.t = __builtin_fmaf(a.s, d, a.t) * f;
+    const float d = fmaxf(a.m - m, kFar);
+    const double f = exp_of(d);
+    a.t = __builtin_fma(a.s, (double)d, a.t) * f;
     a.s *= f;
     a.m = m;
 }
@@ -46,94 +51,247 @@ __device__ __forceinline__ Sums join(Sums a, Sums b) {
     rise(b, m);
     return Sums{m, a.s + b.s, a.t + b.t};
 }
-
-// Alternatives are ordered by (larger logit, lower id).
-struct Best {
-    float v;
-    int32_t id;      // -1: none
-};
-__device__ __forceinline__ bool ahead(Best a, Best b) {
-    return b.id < 0 ? a.id >= 0 : a.id >= 0 && (a.v > b.v || (a.v == b.v && a.id < b.id));
+template <int kLanes>
+__device__ __forceinline__ Sums join_lanes(Sums a) {
+#pragma unroll 1
+    for (int d = kLanes / 2; d > 0; d >>= 1)
+        a = join(a, Sums{__shfl_xor(a.m, d), __shfl_xor(a.s, d), __shfl_xor(a.t, d)});
+    return a;
 }
-__device__ __forceinline__ Best wave_best(Best b) {
+__device__ __forceinline__ float log_of(double s) {
+    return s < 2.0 ? log1pf((float)(s - 1.0)) : logf((float)s);
+}
+
+// Adds n * M logits to a lane's sums, m being the largest of them and of what the
+// lane has. exp(x - m) = 2^(x log2(e) - c) 2^d with c = m log2(e) rounded and d what
+// the rounding took: one fused step and the exponential a logit, and the factor
+// 2^d for all of them together.
+template <bool kEntropy, int M, int N>
+__device__ __forceinline__ void add(Sums& a, const float (&v)[M][N], float m) {
+    rise(a, m);
+    float s[4] = {}, t[4] = {};
+    if (__ballot(!(fabsf(m) < kTame)) == 0) {
+        const float c = m * kLog2e, d = __builtin_fmaf(-m, kLog2e, c);
 #pragma unroll
-    for (int d = 32; d > 0; d >>= 1) {
-        const Best o{__shfl_xor(b.v, d), __shfl_xor(b.id, d)};
-        if (ahead(o, b)) b = o;
+        for (int j = 0; j < M; ++j) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const float p = __builtin_fmaf(v[j][i], kLog2e, -c), e = __builtin_amdgcn_exp2f(p);
+                s[i & 3] += e;
+                if (kEntropy) t[i & 3] = __builtin_fmaf(e, fmaxf(p, kFar2), t[i & 3]);
+            }
+        }
+        const float sum = (s[0] + s[1]) + (s[2] + s[3]), f = __builtin_amdgcn_exp2f(d);
+        a.s += (double)(sum * f);
+        if (kEntropy) a.t += (double)(__builtin_fmaf(sum, d, (t[0] + t[1]) + (t[2] + t[3])) * (f * kLn2));
+    } else {
+#pragma unroll
+        for (int j = 0; j < M; ++j) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const float z = v[j][i] - m, e = exp_of(z);
+                s[i & 3] += e;
+                if (kEntropy) t[i & 3] = __builtin_fmaf(e, fmaxf(z, kFar), t[i & 3]);
+            }
+        }
+        a.s += (double)((s[0] + s[1]) + (s[2] + s[3]));
+        if (kEntropy) a.t += (double)((t[0] + t[1]) + (t[2] + t[3]));
     }
-    return b;
 }
 
-// The best of a lane's logits that comes after `last` (id -1: of all), looked
-// for by its whole wave: lane l of 64 takes the vectors l, l + 64, ... of it.
-template <class T>
-__device__ __forceinline__ Best best_after(const T* row, int64_t V, int owner, Best last) {
-    constexpr int N = kVecOf<T>;
-    const int64_t units = (V + N - 1) / N;
-    Best b{kNegInf, -1};
-    for (int64_t u = owner + (int64_t)(threadIdx.x & 63) * kThreads; u < units; u += 64 * kThreads) {
-        const int n = V - u * N < N ? (int)(V - u * N) : N;
-        float v[N];
-        widen(load_row(row + u * N, n), v);
+// Alternatives are ordered by (larger logit, lower id): as one number, 0 for none.
+__device__ __forceinline__ uint64_t order_of(float v, uint32_t id) {
+    const uint32_t b = __float_as_uint(v + 0.0f);                  // -0 is 0
+    return (uint64_t)(b & 0x80000000u ? ~b : b | 0x80000000u) << 32 | (uint32_t)~id;
+}
+__device__ __forceinline__ float logit_of(uint64_t o) {
+    const uint32_t b = (uint32_t)(o >> 32);
+    return __uint_as_float(b & 0x80000000u ? b & 0x7FFFFFFFu : ~b);
+}
+__device__ __forceinline__ int32_t id_of(uint64_t o) { return (int32_t)~(uint32_t)o; }
+
+template <int kLanes>
+__device__ __forceinline__ uint64_t most_of(uint64_t v) {
 #pragma unroll
-        for (int c = 0; c < N; ++c) {
-            const Best x{v[c], (int32_t)(u * N + c)};
-            if (c < n && v[c] > kNegInf && (last.id < 0 || ahead(last, x)) && ahead(x, b)) b = x;
+    for (int d = kLanes / 2; d > 0; d >>= 1) {
+        const uint64_t o = (uint64_t)__shfl_xor((unsigned long long)v, d);
+        v = o > v ? o : v;
+    }
+    return v;
+}
+
+template <class T>
+__device__ __forceinline__ int vector_of(const T* row, int64_t V, int64_t u, float (&v)[kVecOf<T>]) {
+    constexpr int N = kVecOf<T>;
+    const int n = V - u * N < N ? (int)(V - u * N) : N;
+    widen(load_row(row + u * N, n), v);
+    return n;
+}
+
+// The alternatives of a row, by a workgroup whose lane i has the vectors i, i +
+// kThreads, ... of it and has found the largest logit `most` of them, in vector
+// `unit` (-1: none above -infinity).
+//
+// 64 groups of lanes put forward their best; the top-th of these is no better than
+// the top-th of all logits, and only lanes whose own best reaches it can hold an
+// alternative. Their vectors are looked through again, all at once, and what
+// reaches it is ranked: usually little more than `top` logits. Where it is more
+// than kFound (rows that fall or rise throughout), the lanes' bests are taken one
+// by one instead.
+constexpr int kFound = 512;
+struct TopSpace {
+    uint64_t best[64];
+    uint64_t found[kFound];
+    uint16_t lanes[1024];
+    int lanes_count, count;
+};
+template <class T, int kThreads>
+__device__ __forceinline__ void alternatives(const T* row, int64_t V, float most, int64_t unit, float m, float log_s,
+                                             int32_t top, int32_t* ids, float* logprobs, TopSpace& w) {
+    constexpr int N = kVecOf<T>, kGroup = kThreads / 64;
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int64_t units = (V + N - 1) / N;
+    uint64_t mine = 0;
+    if (unit >= 0) {
+        float v[N];
+        const int n = vector_of(row, V, unit, v);
+#pragma unroll
+        for (int c = N - 1; c >= 0; --c)
+            if (c < n && v[c] == most) mine = order_of(most, (uint32_t)(unit * N + c));
+    }
+    const uint64_t group = most_of<kGroup>(mine);
+    if (tid % kGroup == 0) w.best[tid / kGroup] = group;
+    if (tid == 0) w.lanes_count = w.count = 0;
+    __syncthreads();
+    const uint64_t c = w.best[lane];
+    int rank = 0;
+#pragma unroll 16
+    for (int i = 0; i < 64; ++i) rank += w.best[i] > c ? 1 : 0;
+    const uint64_t last = __ballot(rank == top - 1 && c != 0);
+    const uint64_t least = last ? (uint64_t)__shfl((unsigned long long)c, __ffsll((long long)last) - 1) : 1;
+    if (mine >= least) w.lanes[atomicAdd(&w.lanes_count, 1)] = (uint16_t)tid;
+    __syncthreads();
+    const uint32_t per = (uint32_t)((units + kThreads - 1) / kThreads);
+    const int64_t items = (int64_t)w.lanes_count * per;
+    for (int64_t i = tid; i < items; i += kThreads) {
+        const int64_t l = items >> 32 ? i / per : (int64_t)((uint32_t)i / per), u = w.lanes[l] + (i - l * per) * kThreads;
+        if (u >= units) continue;
+        float v[N];
+        const int n = vector_of(row, V, u, v);
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            const uint64_t o = order_of(v[k], (uint32_t)(u * N + k));
+            if (k < n && v[k] > kNegInf && o >= least) {
+                const int at = atomicAdd(&w.count, 1);
+                if (at < kFound) w.found[at] = o;
+            }
         }
     }
-    return wave_best(b);
+    __syncthreads();
+    const int count = w.count;
+    if (count <= kFound) {
+        for (int i = tid; i < count; i += kThreads) {
+            const uint64_t o = w.found[i];
+            int at = 0;
+            for (int j = 0; j < count; ++j) at += w.found[j] > o ? 1 : 0;
+            if (at >= top) continue;
+            *gbl_mut<int32_t>(ids + at) = id_of(o);
+            *gbl_mut<float>(logprobs + at) = (logit_of(o) - m) - log_s;
+        }
+        if (tid >= count && tid < top) {
+            *gbl_mut<int32_t>(ids + tid) = -1;
+            *gbl_mut<float>(logprobs + tid) = kNegInf;
+        }
+        return;
+    }
+    for (int32_t j = 0; j < top; ++j) {
+        const uint64_t wave = most_of<64>(mine);
+        __syncthreads();
+        if (lane == 0) w.best[tid >> 6] = wave;
+        __syncthreads();
+        uint64_t b = w.best[0];
+#pragma unroll
+        for (int i = 1; i < kGroup; ++i) b = w.best[i] > b ? w.best[i] : b;
+        if (tid == 0) {
+            *gbl_mut<int32_t>(ids + j) = b ? id_of(b) : -1;
+            *gbl_mut<float>(logprobs + j) = b ? (logit_of(b) - m) - log_s : kNegInf;
+        }
+        // The owner's next, looked for by its whole wave.
+        const int owner = (int)(id_of(b) / N % kThreads);
+        if (b == 0 || owner >> 6 != tid >> 6) continue;
+        uint64_t next = 0;
+        for (int64_t u = owner + (int64_t)lane * kThreads; u < units; u += 64 * kThreads) {
+            float v[N];
+            const int n = vector_of(row, V, u, v);
+#pragma unroll
+            for (int k = 0; k < N; ++k) {
+                const uint64_t o = order_of(v[k], (uint32_t)(u * N + k));
+                if (k < n && v[k] > kNegInf && o < b && o > next) next = o;
+            }
+        }
+        next = most_of<64>(next);
+        if (tid == owner) mine = next;
+    }
 }
 
-template <class T, class Id>
+// One workgroup a row. A lane has 32 logits in hand at a time.
+template <class T, class Id, int kThreads, bool kEntropy, bool kTop>
 __global__ __launch_bounds__(kThreads) void row_logprobs(
     const T* logits, int64_t stride, int64_t tokens, int64_t V, const Id* targets, float* logprob,
     float* stats, float* entropy, int32_t top, int32_t* top_ids, float* top_logprobs) {
-    constexpr int N = kVecOf<T>, KU = 4;
+    constexpr int N = kVecOf<T>, KU = 32 / N, kWaves = kThreads / 64;
     __shared__ Sums part[kWaves];
-    __shared__ Best found[kWaves];
+    __shared__ std::conditional_t<kTop, TopSpace, int> space;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int64_t units = (V + N - 1) / N;
+    const int64_t units = (V + N - 1) / N, whole = V / N;
     for (int64_t r = blockIdx.x; r < tokens; r += gridDim.x) {
         const T* row = logits + r * stride;
-        Sums a{kLowest, 0.0f, 0.0f};
-        for (int64_t u0 = tid; u0 < units; u0 += KU * kThreads) {
+        Sums a{kLowest, 0.0, 0.0};
+        float most = kNegInf;
+        int64_t unit = -1;
+        for (int64_t u0 = 0; u0 < units; u0 += KU * kThreads) {
             float v[KU][N];
             float m = a.m;
+            if (u0 + KU * kThreads <= whole) {
+                u32x4 raw[KU];
 #pragma unroll
-            for (int j = 0; j < KU; ++j) {
-                const int64_t u = u0 + j * kThreads, left = V - u * N;
+                for (int j = 0; j < KU; ++j) raw[j] = load16_once(row + (u0 + j * kThreads + tid) * N);
 #pragma unroll
-                for (int c = 0; c < N; ++c) v[j][c] = kNegInf;
-                if (left > 0) {
+                for (int j = 0; j < KU; ++j) widen(raw[j], v[j]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < KU; ++j) {
+                    const int64_t u = u0 + j * kThreads + tid, left = V - u * N;
+#pragma unroll
+                    for (int c = 0; c < N; ++c) v[j][c] = kNegInf;
+                    if (left <= 0) continue;
                     widen(load_row(row + u * N, left < N ? (int)left : N), v[j]);
 #pragma unroll
                     for (int c = 0; c < N; ++c)
                         if (c >= left) v[j][c] = kNegInf;
                 }
-#pragma unroll
-                for (int c = 0; c < N; ++c) m = fmaxf(m, v[j][c]);
             }
-            rise(a, m);
 #pragma unroll
             for (int j = 0; j < KU; ++j) {
+                float b = v[j][0];
 #pragma unroll
-                for (int c = 0; c < N; ++c) {
-                    const float z = v[j][c] - m, e = exp_of(z);
-                    a.s += e;
-                    a.t = __builtin_fmaf(e, fmaxf(z, kFar), a.t);
+                for (int c = 1; c < N; ++c) b = fmaxf(b, v[j][c]);
+                if (kTop && b > most) {
+                    most = b;
+                    unit = u0 + j * kThreads + tid;
                 }
+                m = fmaxf(m, b);
             }
+            add<kEntropy>(a, v, m);
         }
-#pragma unroll
-        for (int d = 32; d > 0; d >>= 1)
-            a = join(a, Sums{__shfl_xor(a.m, d), __shfl_xor(a.s, d), __shfl_xor(a.t, d)});
-        if (lane == 0) part[wave] = a;
-        __syncthreads();
-        a = part[0];
-#pragma unroll
-        for (int w = 1; w < kWaves; ++w) a = join(a, part[w]);
-        const bool none = a.s == 0.0f;             // no logit above -infinity
-        const float log_s = none ? kNegInf : logf(a.s);
+        a = join_lanes<64>(a);
+        if (kWaves > 1) {
+            if (lane == 0) part[wave] = a;
+            __syncthreads();
+            a = join_lanes<kWaves>(part[lane % kWaves]);
+        }
+        const bool none = a.s == 0.0;              // no logit above -infinity
+        const float log_s = none ? kNegInf : log_of(a.s);
         if (tid == 0) {
             const Id at = *gbl<Id>(targets + r);
             float lp = 0.0f;
@@ -148,70 +306,76 @@ __global__ __launch_bounds__(kThreads) void row_logprobs(
                 *gbl_mut<float>(stats + 2 * r) = none ? kNegInf : a.m;
                 *gbl_mut<float>(stats + 2 * r + 1) = log_s;
             }
-            if (entropy) *gbl_mut<float>(entropy + r) = none ? 0.0f : log_s - a.t / a.s;
+            if (kEntropy) *gbl_mut<float>(entropy + r) = none ? 0.0f : log_s - (float)(a.t / a.s);
         }
-        if (top > 0) {
-            Best mine{kNegInf, -1};
-            for (int64_t u = tid; u < units; u += kThreads) {
-                const int n = V - u * N < N ? (int)(V - u * N) : N;
-                float v[N];
-                widen(load_row(row + u * N, n), v);
-#pragma unroll
-                for (int c = 0; c < N; ++c)
-                    if (c < n && v[c] > mine.v) mine = Best{v[c], (int32_t)(u * N + c)};
-            }
-            for (int32_t j = 0; j < top; ++j) {
-                const Best w = wave_best(mine);
-                __syncthreads();
-                if (lane == 0) found[wave] = w;
-                __syncthreads();
-                Best b = found[0];
-#pragma unroll
-                for (int i = 1; i < kWaves; ++i)
-                    if (ahead(found[i], b)) b = found[i];
-                if (tid == 0) {
-                    *gbl_mut<int32_t>(top_ids + r * top + j) = b.id;
-                    *gbl_mut<float>(top_logprobs + r * top + j) = b.id < 0 ? kNegInf : (b.v - a.m) - log_s;
-                }
-                const int owner = (int)(b.id / N % kThreads);
-                if (b.id >= 0 && owner >> 6 == wave) {
-                    const Best next = best_after(row, V, owner, b);
-                    if (tid == owner) mine = next;
-                }
-            }
-        }
+        if constexpr (kTop)
+            alternatives<T, kThreads>(row, V, most, unit, a.m, log_s, top, top_ids + r * top, top_logprobs + r * top, space);
         __syncthreads();
     }
 }
 
-template <class T, class Id>
+// p = exp(x - m - log s) = 2^(x log2(e) - c) 2^d, as in the forward pass; the
+// factor 2^d goes to the row's factors. A lane has KU vectors in hand at a time.
+constexpr int kThreads = 256, kGradVectors = 4;
+template <class T, class Id, bool kEntropy>
 __global__ __launch_bounds__(kThreads) void row_logprobs_grad(
     const T* logits, int64_t stride, int64_t tokens, int64_t V, const Id* targets, const float* stats,
     const float* dlogprob, const float* entropy, const float* dentropy, T* dlogits, int64_t dstride) {
-    constexpr int N = kVecOf<T>;
+    constexpr int N = kVecOf<T>, KU = kGradVectors;
     const int64_t units = (V + N - 1) / N;
     for (int64_t r = blockIdx.x; r < tokens; r += gridDim.x) {
         const Id id = *gbl<Id>(targets + r);
         const int64_t at = id >= 0 && (int64_t)id < V ? (int64_t)id : -1;
         const float m = *gbl<float>(stats + 2 * r), log_s = *gbl<float>(stats + 2 * r + 1);
         const float d = at >= 0 ? *gbl<float>(dlogprob + r) : 0.0f;
-        const float h = dentropy ? *gbl<float>(dentropy + r) : 0.0f, H = dentropy ? *gbl<float>(entropy + r) : 0.0f;
-        const bool zero = (at < 0 && !dentropy) || m == kNegInf;
-        for (int64_t u = (int64_t)blockIdx.y * kThreads + threadIdx.x; u < units; u += (int64_t)gridDim.y * kThreads) {
-            const int n = V - u * N < N ? (int)(V - u * N) : N;
-            float v[N] = {};
+        const float h = kEntropy ? *gbl<float>(dentropy + r) : 0.0f, H = kEntropy ? *gbl<float>(entropy + r) : 0.0f;
+        const bool zero = (at < 0 && !kEntropy) || m == kNegInf, tame = fabsf(m) < kTame;
+        const double exact = ((double)m + (double)log_s) * 0x1.71547652b82fep+0;
+        const float c0 = (float)exact, rest = (float)((double)c0 - exact), f = __builtin_amdgcn_exp2f(rest);
+        for (int64_t u0 = (int64_t)blockIdx.y * KU * kThreads; u0 < units; u0 += (int64_t)gridDim.y * KU * kThreads) {
+            float v[KU][N];
             if (!zero) {
-                widen(load_row(logits + r * stride + u * N, n), v);
+                u32x4 raw[KU];
 #pragma unroll
-                for (int c = 0; c < N; ++c) {
-                    const float lp = (v[c] - m) - log_s, p = exp_of(lp);
-                    float g = u * N + c == at ? d : 0.0f;
-                    g = __builtin_fmaf(-d, p, g);
-                    if (dentropy) g = __builtin_fmaf(-h, p * (fmaxf(lp, kFar) + H), g);
-                    v[c] = g;
+                for (int j = 0; j < KU; ++j) {
+                    const int64_t u = u0 + j * kThreads + threadIdx.x, left = V - u * N;
+                    raw[j] = u32x4{};
+                    if (left > 0) raw[j] = load_row<true>(logits + r * stride + u * N, left < N ? (int)left : N);
                 }
+#pragma unroll
+                for (int j = 0; j < KU; ++j) widen(raw[j], v[j]);
+#pragma unroll
+                for (int j = 0; j < KU; ++j) {
+                    const int64_t first = (u0 + j * kThreads + threadIdx.x) * N;
+#pragma unroll
+                    for (int c = 0; c < N; ++c) {
+                        float p, lp;
+                        if (tame) {
+                            const float q = __builtin_fmaf(v[j][c], kLog2e, -c0);
+                            p = __builtin_amdgcn_exp2f(q) * f;
+                            lp = (fmaxf(q, kFar2) + rest) * kLn2;
+                        } else {
+                            lp = (v[j][c] - m) - log_s;
+                            p = exp_of(lp);
+                            lp = fmaxf(lp, kFar);
+                        }
+                        float g = first + c == at ? d : 0.0f;
+                        g = __builtin_fmaf(-d, p, g);
+                        if (kEntropy) g = __builtin_fmaf(-h, p * (lp + H), g);
+                        v[j][c] = g;
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < KU; ++j)
+#pragma unroll
+                    for (int c = 0; c < N; ++c) v[j][c] = 0.0f;
             }
-            store_row(dlogits + r * dstride + u * N, n, narrow(v));
+#pragma unroll
+            for (int j = 0; j < KU; ++j) {
+                const int64_t u = u0 + j * kThreads + threadIdx.x, left = V - u * N;
+                if (left > 0) store_row(dlogits + r * dstride + u * N, left < N ? (int)left : N, narrow(v[j]));
+            }
         }
     }
 }
@@ -224,6 +388,12 @@ tide_status check(int32_t dtype, int64_t tokens, int64_t vocab, int32_t id_bytes
     if (tokens < 0 || vocab < 0) return fail(TIDE_ERR_INVALID_ARG, "need tokens and vocab >= 0");
     if (vocab > INT32_MAX) return fail(TIDE_ERR_UNSUPPORTED, "vocab must be below 2^31");
     return TIDE_OK;
+}
+
+// Threads of a row's workgroup.
+int threads_of(int64_t tokens, int64_t units) {
+    if (units <= 256) return 64;
+    return tokens < 1024 && units > 2048 ? 1024 : 256;
 }
 
 template <class F>
@@ -257,11 +427,24 @@ tide_status tide_token_logprobs(int32_t dtype, const void* logits, int64_t logit
         if (tokens == 0) return TIDE_OK;
         return on_stream(stream, [&](hipStream_t s) {
             const dim3 grid((uint32_t)(tokens < (1 << 20) ? tokens : (1 << 20)));
+            const int threads = threads_of(tokens, vocab * size / 16);
             return with_types(dtype, id_bytes, [&](auto type, auto id) {
                 using T = decltype(type);
                 using Id = decltype(id);
-                return enqueue(row_logprobs<T, Id>, grid, kThreads, 0, s, (const T*)logits, logits_stride, tokens,
-                               vocab, (const Id*)targets, logprob, stats, entropy, top, top_ids, top_logprobs);
+                const auto go = [&](auto n, auto with_entropy, auto with_top) {
+                    return enqueue(row_logprobs<T, Id, n.value, with_entropy.value, with_top.value>, grid, n.value, 0, s,
+                                   (const T*)logits, logits_stride, tokens, vocab, (const Id*)targets, logprob, stats,
+                                   entropy, top, top_ids, top_logprobs);
+                };
+                const auto with = [&](auto n) {
+                    using Yes = std::true_type;
+                    using No = std::false_type;
+                    if (entropy) return top ? go(n, Yes{}, Yes{}) : go(n, Yes{}, No{});
+                    return top ? go(n, No{}, Yes{}) : go(n, No{}, No{});
+                };
+                return threads == 64    ? with(std::integral_constant<int, 64>{})
+                       : threads == 256 ? with(std::integral_constant<int, 256>{})
+                                        : with(std::integral_constant<int, 1024>{});
             });
         });
     });
@@ -288,15 +471,18 @@ tide_status tide_token_logprobs_grad(int32_t dtype, const void* logits, int64_t 
         TIDE_TRY(no_overlap(&wr, 1, rd, in_place ? 5 : 6));
         if (tokens == 0 || vocab == 0) return TIDE_OK;
         return on_stream(stream, [&](hipStream_t s) {
-            const int64_t groups = (vocab * size / 16 + kThreads) / kThreads;
+            const int64_t per = kGradVectors * kThreads, groups = (vocab * size / 16 + per) / per;
             const dim3 grid((uint32_t)(tokens < (1 << 20) ? tokens : (1 << 20)),
                             (uint32_t)(groups < 32768 ? groups : 32768));
             return with_types(dtype, id_bytes, [&](auto type, auto id) {
                 using T = decltype(type);
                 using Id = decltype(id);
-                return enqueue(row_logprobs_grad<T, Id>, grid, kThreads, 0, s, (const T*)logits, logits_stride,
-                               tokens, vocab, (const Id*)targets, stats, dlogprob, entropy, dentropy, (T*)dlogits,
-                               dlogits_stride);
+                const auto go = [&](auto with_entropy) {
+                    return enqueue(row_logprobs_grad<T, Id, with_entropy.value>, grid, kThreads, 0, s, (const T*)logits,
+                                   logits_stride, tokens, vocab, (const Id*)targets, stats, dlogprob, entropy, dentropy,
+                                   (T*)dlogits, dlogits_stride);
+                };
+                return dentropy ? go(std::true_type{}) : go(std::false_type{});
             });
         });
     });
