@@ -47,28 +47,39 @@ struct Slot {
             b = p < pairs ? p + pairs : p + half;
         }
     }
-    static __device__ __forceinline__ void load(const T* x, int a, int b, float (&u)[W], float (&v)[W]) {
+    // What a slot's loads give, before it is widened.
+    struct Raw {
+        u32x4 p, q;
+    };
+    template <bool kOnce = false>
+    static __device__ __forceinline__ Raw load(const T* x, int a, int b) {
+        Raw r{};
         if constexpr (W == 1) {
             if constexpr (sizeof(T) == 2) {
-                u[0] = lo_bf16(*gbl<uint16_t>(x + a));
-                v[0] = lo_bf16(*gbl<uint16_t>(x + b));
+                r.p[0] = (uint32_t)*gbl<uint16_t>(x + a) << 16;
+                r.q[0] = (uint32_t)*gbl<uint16_t>(x + b) << 16;
             } else {
-                u[0] = *gbl<float>(x + a);
-                v[0] = *gbl<float>(x + b);
+                r.p[0] = *gbl<uint32_t>(x + a);
+                r.q[0] = *gbl<uint32_t>(x + b);
             }
         } else {
+            r.p = kOnce ? load16_once(x + a) : load16(x + a);
+            r.q = kOnce ? load16_once(x + b) : load16(x + b);
+        }
+        return r;
+    }
+    static __device__ __forceinline__ void open(const Raw& r, float (&u)[W], float (&v)[W]) {
+        if constexpr (W == 1) {
+            u[0] = __uint_as_float(r.p[0]);
+            v[0] = __uint_as_float(r.q[0]);
+        } else {
             float p[W], q[W];
-            widen(load16(x + a), p);
-            widen(load16(x + b), q);
+            widen(r.p, p);
+            widen(r.q, q);
 #pragma unroll
             for (int c = 0; c < W; ++c) {
-                if (kAdjacent) {
-                    u[c] = 2 * c < W ? p[(2 * c) % W] : q[(2 * c) % W];
-                    v[c] = 2 * c < W ? p[(2 * c + 1) % W] : q[(2 * c + 1) % W];
-                } else {
-                    u[c] = p[c];
-                    v[c] = q[c];
-                }
+                u[c] = !kAdjacent ? p[c] : 2 * c < W ? p[2 * c % W] : q[2 * c % W];
+                v[c] = !kAdjacent ? q[c] : 2 * c < W ? p[(2 * c + 1) % W] : q[(2 * c + 1) % W];
             }
         }
     }
@@ -86,15 +97,8 @@ struct Slot {
             float p[W], q[W];
 #pragma unroll
             for (int c = 0; c < W; ++c) {
-                if (kAdjacent) {
-                    float& lo = 2 * c < W ? p[(2 * c) % W] : q[(2 * c) % W];
-                    float& hi = 2 * c < W ? p[(2 * c + 1) % W] : q[(2 * c + 1) % W];
-                    lo = u[c];
-                    hi = v[c];
-                } else {
-                    p[c] = u[c];
-                    q[c] = v[c];
-                }
+                p[c] = !kAdjacent ? u[c] : c & 1 ? v[c / 2] : u[c / 2];
+                q[c] = !kAdjacent ? v[c] : c & 1 ? v[W / 2 + c / 2] : u[W / 2 + c / 2];
             }
             store16(x + a, narrow(p));
             store16(x + b, narrow(q));
@@ -150,80 +154,100 @@ __device__ __forceinline__ float inverse_root(float v) {
     return low ? r * 0x1p+48f : r;
 }
 
-// Loads a slot's weights.
+// A slot's weights, 1 where there are none.
 template <class T, int W, bool kAdjacent>
 __device__ __forceinline__ void weights(const void* w, int a, int b, float (&u)[W], float (&v)[W]) {
-    if (w) {
-        Slot<T, W, kAdjacent>::load((const T*)w, a, b, u, v);
-    } else {
-#pragma unroll
-        for (int c = 0; c < W; ++c) u[c] = v[c] = 1.0f;
-    }
+    using S = Slot<T, W, kAdjacent>;
+    constexpr uint32_t kOne = sizeof(T) == 2 && W > 1 ? 0x3F803F80u : 0x3F800000u;
+    typename S::Raw r{{kOne, kOne, kOne, kOne}, {kOne, kOne, kOne, kOne}};
+    if (w) r = S::load((const T*)w, a, b);
+    S::open(r, u, v);
 }
 
-// W pairs a slot, NS slots a lane, 2^lane_log2 lanes a head.
-template <class T, int W, int NS, bool kAdjacent>
+// W pairs a slot, NS slots a lane, 2^lane_log2 lanes a head, 64 >> lane_log2 heads a
+// wave at once and KH times that in all, of one token: its angles are loaded once
+// for them, and all their loads are under way before the first is used. 8192 tokens
+// of 72 heads of 128: 62 us with KH 1, 55 with 2, 56 with 3, 59 with 4 (302 MB moved:
+// 5.5 TB/s). A few tokens take KH 1, for more waves.
+template <class T, int W, int NS, int KH, bool kAdjacent>
 __global__ __launch_bounds__(kThreads) void rotate_heads(Heads q, Heads k, Heads qo, Heads ko,
                                                          const void* qw, const void* kw, Turn turn,
-                                                         int64_t tokens, int dim, float eps,
-                                                         int lane_log2) {
+                                                         int64_t waves, int32_t parts, int dim,
+                                                         float eps, int lane_log2) {
     using S = Slot<T, W, kAdjacent>;
-    const int lanes = 1 << lane_log2, lane = threadIdx.x & (lanes - 1);
+    const int lanes = 1 << lane_log2, lane = threadIdx.x & (lanes - 1), at_once = 64 >> lane_log2;
     const int half = dim / 2, slots = half / W, all = q.heads + k.heads;
-    const int64_t rows = tokens * all, per = kThreads >> lane_log2;
-    for (int64_t r = (int64_t)blockIdx.x * per + (threadIdx.x >> lane_log2); r < rows; r += (int64_t)gridDim.x * per) {
-        const int64_t t = r / all;
-        const int h = (int)(r - t * all);
-        const bool is_q = h < q.heads;
-        const Heads& from = is_q ? q : k;
-        const Heads& to = is_q ? qo : ko;
-        const int hh = is_q ? h : h - q.heads;
-        const T* x = (const T*)from.data + t * from.token_stride + hh * from.head_stride;
-        T* y = (T*)to.data + t * to.token_stride + hh * to.head_stride;
-        const int64_t row = table_row(turn, t);
-        float u[NS][W], v[NS][W], sum = 0.0f;
+    const float per_element = 1.0f / (float)dim;
+    int a[NS], b[NS];
 #pragma unroll
-        for (int i = 0; i < NS; ++i) {
-            const int s = lane + i * lanes;
-            int a, b;
-            S::where(s, half, turn.pairs, a, b);
-            if (s < slots) {
-                S::load(x, a, b, u[i], v[i]);
+    for (int i = 0; i < NS; ++i) S::where(lane + i * lanes, half, turn.pairs, a[i], b[i]);
+    for (int64_t w = (int64_t)blockIdx.x * (kThreads / 64) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); w < waves;
+         w += (int64_t)gridDim.x * (kThreads / 64)) {
+        const int64_t t = w / parts;
+        const int first = (int)(w - t * parts) * KH * at_once + ((threadIdx.x & 63) >> lane_log2);
+        typename S::Raw raw[KH][NS];
 #pragma unroll
-                for (int c = 0; c < W; ++c) sum = __builtin_fmaf(u[i][c], u[i][c], __builtin_fmaf(v[i][c], v[i][c], sum));
+        for (int j = 0; j < KH; ++j) {
+            const int h = first + j * at_once;
+            const T* x = h < q.heads ? (const T*)q.data + t * q.token_stride + h * q.head_stride
+                                     : (const T*)k.data + t * k.token_stride + (h - q.heads) * k.head_stride;
+#pragma unroll
+            for (int i = 0; i < NS; ++i) {
+                raw[j][i] = typename S::Raw{};
+                if (h < all && lane + i * lanes < slots) raw[j][i] = S::template load<true>(x, a[i], b[i]);
             }
         }
-        const float scale = inverse_root(head_sum(sum, lanes) / (float)dim + eps);
+        const int64_t row = table_row(turn, t);
+        float c[NS][W], n[NS][W];
 #pragma unroll
-        for (int i = 0; i < NS; ++i) {
-            const int s = lane + i * lanes;
-            if (s >= slots) continue;
-            int a, b;
-            S::where(s, half, turn.pairs, a, b);
-            float wu[W], wv[W], c[W], n[W];
-            weights<T, W, kAdjacent>(is_q ? qw : kw, a, b, wu, wv);
-            angles<W>(turn, row, s, c, n);
+        for (int i = 0; i < NS; ++i) angles<W>(turn, lane + i * lanes < slots ? row : -1, lane + i * lanes, c[i], n[i]);
 #pragma unroll
-            for (int j = 0; j < W; ++j) {
-                const float p = u[i][j] * scale * wu[j], o = v[i][j] * scale * wv[j];
-                u[i][j] = __builtin_fmaf(p, c[j], -(o * n[j]));
-                v[i][j] = __builtin_fmaf(p, n[j], o * c[j]);
+        for (int j = 0; j < KH; ++j) {
+            const int h = first + j * at_once;
+            float u[NS][W], v[NS][W], sum = 0.0f;
+#pragma unroll
+            for (int i = 0; i < NS; ++i) {
+                S::open(raw[j][i], u[i], v[i]);
+#pragma unroll
+                for (int e = 0; e < W; ++e) sum = __builtin_fmaf(u[i][e], u[i][e], __builtin_fmaf(v[i][e], v[i][e], sum));
             }
-            S::store(y, a, b, u[i], v[i]);
+            const float scale = inverse_root(__builtin_fmaf(head_sum(sum, lanes), per_element, eps));
+            T* y = h < q.heads ? (T*)qo.data + t * qo.token_stride + h * qo.head_stride
+                               : (T*)ko.data + t * ko.token_stride + (h - q.heads) * ko.head_stride;
+#pragma unroll
+            for (int i = 0; i < NS; ++i) {
+                if (h >= all || lane + i * lanes >= slots) continue;
+                float wu[W], wv[W];
+                weights<T, W, kAdjacent>(h < q.heads ? qw : kw, a[i], b[i], wu, wv);
+#pragma unroll
+                for (int e = 0; e < W; ++e) {
+                    const float p = u[i][e] * scale * wu[e], o = v[i][e] * scale * wv[e];
+                    u[i][e] = __builtin_fmaf(p, c[i][e], -(o * n[i][e]));
+                    v[i][e] = __builtin_fmaf(p, n[i][e], o * c[i][e]);
+                }
+                S::store(y, a[i], b[i], u[i], v[i]);
+            }
         }
     }
 }
 
 // The gradient of one set of heads; partial (when not NULL) gets this
-// workgroup's sum of g * n, dim fp32 in element order.
+// workgroup's sum of g * n, dim fp32 in element order. A wave takes 64 >> lane_log2
+// heads of a token at a time, then those some waves further on. (The next ones'
+// loads under way meanwhile: 51 us instead of 49 for 8191 tokens of 36 heads; 512 or
+// 2048 workgroups instead of 1024: 62 and 57.)
+struct Steps {
+    int64_t t;             // the step between a wave's turns: tokens, and sets of heads
+    int32_t part, parts;   // sets of heads of a token
+};
 template <class T, int W, int NS, bool kAdjacent>
 __device__ __forceinline__ void grad_of(const Heads& x, const Heads& dy, const Heads& dx, const void* w,
                                         const Turn& turn, int64_t tokens, int dim, float eps, int lane_log2,
-                                        float* partial, float* joint) {
+                                        Steps step, float* partial, float* joint) {
     using S = Slot<T, W, kAdjacent>;
     const int lanes = 1 << lane_log2, lane = threadIdx.x & (lanes - 1), group = threadIdx.x >> lane_log2;
-    const int half = dim / 2, slots = half / W;
-    const int64_t rows = tokens * x.heads, per = kThreads >> lane_log2;
+    const int half = dim / 2, slots = half / W, at_once = 64 >> lane_log2;
+    const float per_element = 1.0f / (float)dim;
     float wu[NS][W], wv[NS][W], au[NS][W] = {}, av[NS][W] = {};
     int a[NS], b[NS];
 #pragma unroll
@@ -232,22 +256,30 @@ __device__ __forceinline__ void grad_of(const Heads& x, const Heads& dy, const H
         S::where(s, half, turn.pairs, a[i], b[i]);
         if (s < slots) weights<T, W, kAdjacent>(w, a[i], b[i], wu[i], wv[i]);
     }
-    for (int64_t r = (int64_t)blockIdx.x * per + group; r < rows; r += (int64_t)gridDim.x * per) {
-        const int64_t t = r / x.heads;
-        const int h = (int)(r - t * x.heads);
+    const int64_t w0 = (int64_t)blockIdx.x * (kThreads / 64) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    int64_t t = step.parts ? w0 / step.parts : tokens;
+    int32_t part = (int32_t)(w0 - t * step.parts);
+    while (t < tokens) {
+        const int h = part * at_once + ((threadIdx.x & 63) >> lane_log2);
+        const bool mine = h < x.heads;
         const T* px = (const T*)x.data + t * x.token_stride + h * x.head_stride;
         const T* py = (const T*)dy.data + t * dy.token_stride + h * dy.head_stride;
-        T* pd = (T*)dx.data + t * dx.token_stride + h * dx.head_stride;
+        typename S::Raw rx[NS] = {}, ry[NS] = {};
+#pragma unroll
+        for (int i = 0; i < NS; ++i)
+            if (mine && lane + i * lanes < slots) {
+                rx[i] = S::load(px, a[i], b[i]);
+                ry[i] = S::load(py, a[i], b[i]);
+            }
         const int64_t row = table_row(turn, t);
         float u[NS][W], v[NS][W], gu[NS][W], gv[NS][W], sum = 0.0f;
 #pragma unroll
         for (int i = 0; i < NS; ++i) {
             const int s = lane + i * lanes;
-            if (s >= slots) continue;
             float c[W], n[W];
-            S::load(px, a[i], b[i], u[i], v[i]);
-            S::load(py, a[i], b[i], gu[i], gv[i]);
-            angles<W>(turn, row, s, c, n);
+            S::open(rx[i], u[i], v[i]);
+            S::open(ry[i], gu[i], gv[i]);
+            angles<W>(turn, s < slots ? row : -1, s, c, n);
 #pragma unroll
             for (int j = 0; j < W; ++j) {
                 sum = __builtin_fmaf(u[i][j], u[i][j], __builtin_fmaf(v[i][j], v[i][j], sum));
@@ -256,11 +288,11 @@ __device__ __forceinline__ void grad_of(const Heads& x, const Heads& dy, const H
                 gv[i][j] = __builtin_fmaf(o, c[j], -(p * n[j]));
             }
         }
-        const float scale = inverse_root(head_sum(sum, lanes) / (float)dim + eps);
+        const float scale = inverse_root(__builtin_fmaf(head_sum(sum, lanes), per_element, eps));
         float dot = 0.0f;
 #pragma unroll
         for (int i = 0; i < NS; ++i) {
-            if (lane + i * lanes >= slots) continue;
+            if (!mine || lane + i * lanes >= slots) continue;
 #pragma unroll
             for (int j = 0; j < W; ++j) {
                 u[i][j] *= scale;
@@ -272,16 +304,23 @@ __device__ __forceinline__ void grad_of(const Heads& x, const Heads& dy, const H
                 dot = __builtin_fmaf(gu[i][j], u[i][j], __builtin_fmaf(gv[i][j], v[i][j], dot));
             }
         }
-        dot = head_sum(dot, lanes) / (float)dim;
+        dot = head_sum(dot, lanes) * per_element;
+        T* pd = (T*)dx.data + t * dx.token_stride + h * dx.head_stride;
 #pragma unroll
         for (int i = 0; i < NS; ++i) {
-            if (lane + i * lanes >= slots) continue;
+            if (!mine || lane + i * lanes >= slots) continue;
 #pragma unroll
             for (int j = 0; j < W; ++j) {
                 u[i][j] = scale * __builtin_fmaf(-u[i][j], dot, gu[i][j]);
                 v[i][j] = scale * __builtin_fmaf(-v[i][j], dot, gv[i][j]);
             }
             S::store(pd, a[i], b[i], u[i], v[i]);
+        }
+        t += step.t;
+        part += step.part;
+        if (part >= step.parts) {
+            part -= step.parts;
+            ++t;
         }
     }
     if (!partial) return;
@@ -300,7 +339,7 @@ __device__ __forceinline__ void grad_of(const Heads& x, const Heads& dy, const H
     __syncthreads();
     for (int e = threadIdx.x; e < dim; e += kThreads) {
         float sum = 0.0f;
-        for (int g = 0; g < per; ++g) sum += joint[g * dim + e];
+        for (int g = 0; g < kThreads >> lane_log2; ++g) sum += joint[g * dim + e];
         const int p = e / 2;
         int at = e;
         if (!kAdjacent) at = p < turn.pairs ? p + (e & 1) * turn.pairs : p + (e & 1 ? half : turn.pairs);
@@ -312,12 +351,13 @@ template <class T, int W, int NS, bool kAdjacent>
 __global__ __launch_bounds__(kThreads) void rotate_heads_grad(Heads q, Heads k, Heads dqo, Heads dko,
                                                               Heads dq, Heads dk, const void* qw,
                                                               const void* kw, Turn turn, int64_t tokens,
-                                                              int dim, float eps, int lane_log2,
-                                                              float* partial, int want_q, int want_k) {
+                                                              int dim, float eps, int lane_log2, Steps of_q,
+                                                              Steps of_k, float* partial, int want_q, int want_k) {
     __shared__ float joint[kThreads * 2 * W * NS];
     float* mine = partial + (int64_t)blockIdx.x * 2 * dim;
-    grad_of<T, W, NS, kAdjacent>(q, dqo, dq, qw, turn, tokens, dim, eps, lane_log2, want_q ? mine : nullptr, joint);
-    grad_of<T, W, NS, kAdjacent>(k, dko, dk, kw, turn, tokens, dim, eps, lane_log2, want_k ? mine + dim : nullptr, joint);
+    grad_of<T, W, NS, kAdjacent>(q, dqo, dq, qw, turn, tokens, dim, eps, lane_log2, of_q, want_q ? mine : nullptr, joint);
+    grad_of<T, W, NS, kAdjacent>(k, dko, dk, kw, turn, tokens, dim, eps, lane_log2, of_k, want_k ? mine + dim : nullptr,
+                                 joint);
 }
 
 // Weights' gradients: the workgroups' sums in order, 16 runs of them at once.
@@ -332,8 +372,9 @@ __global__ __launch_bounds__(64 * kRuns) void join_weights(const float* partial,
     const int64_t per = (groups + kRuns - 1) / kRuns;
     float sum = 0.0f;
     if (e < dim)
-        for (int64_t g = run * per; g < (run + 1) * per && g < groups; ++g)
-            sum += *gbl<float>(partial + (2 * g + blockIdx.y) * dim + e);
+#pragma unroll 16
+        for (int64_t g = run * per; g < (run + 1) * per; ++g)
+            sum += g < groups ? *gbl<float>(partial + (2 * g + blockIdx.y) * dim + e) : 0.0f;
     part[run][threadIdx.x & 63] = sum;
     __syncthreads();
     if (run || e >= dim) return;
@@ -483,10 +524,16 @@ tide_status tide_norm_rotate(int32_t dtype, int64_t tokens, int32_t head_dim,
         return on_stream(stream, [&](hipStream_t s) {
             return with_slots(size, head_dim, turn.pairs, rotation && rotation->adjacent,
                               [&](auto type, auto w, auto ns, auto adjacent, int lg) {
-                const int64_t per = kThreads >> lg, groups = (tokens * all + per - 1) / per;
-                return enqueue(rotate_heads<decltype(type), w.value, ns.value, adjacent.value>,
-                               dim3((uint32_t)(groups < (1 << 22) ? groups : (1 << 22))), kThreads, 0, s, hq, hk, oq,
-                               ok, q_weight, k_weight, turn, tokens, (int)head_dim, eps, lg);
+                const auto go = [&](auto kh) {
+                    const int64_t at_once = 64 >> lg, sets = (all + at_once - 1) / at_once;
+                    const int64_t parts = (sets + kh.value - 1) / kh.value, waves = tokens * parts;
+                    const int64_t groups = (waves + 3) / 4;
+                    return enqueue(rotate_heads<decltype(type), w.value, ns.value, kh.value, adjacent.value>,
+                                   dim3((uint32_t)(groups < (1 << 22) ? groups : (1 << 22))), kThreads, 0, s, hq, hk, oq,
+                                   ok, q_weight, k_weight, turn, waves, (int32_t)parts, (int)head_dim, eps, lg);
+                };
+                if constexpr (ns.value > 1) return go(std::integral_constant<int, 1>{});
+                else return tokens * all < 16384 ? go(std::integral_constant<int, 1>{}) : go(std::integral_constant<int, 2>{});
             });
         });
     });
@@ -547,10 +594,15 @@ tide_status tide_norm_rotate_grad(int32_t dtype, int64_t tokens, int32_t head_di
         return on_stream(stream, [&](hipStream_t s) {
             const hipError_t e = with_slots(size, head_dim, turn.pairs, rotation && rotation->adjacent,
                                             [&](auto type, auto w, auto ns, auto adjacent, int lg) {
+                const int64_t waves = groups * (kThreads / 64);
+                const auto steps = [&](int32_t heads) {
+                    const int64_t at_once = 64 >> lg, parts = (heads + at_once - 1) / at_once;
+                    return parts ? Steps{waves / parts, (int32_t)(waves % parts), (int32_t)parts} : Steps{};
+                };
                 return enqueue(rotate_heads_grad<decltype(type), w.value, ns.value, adjacent.value>,
                                dim3((uint32_t)groups), kThreads, 0, s, hq, hk, gq, gk, xq, xk, q_weight, k_weight,
-                               turn, tokens, (int)head_dim, eps, lg, (float*)workspace, dq_weight ? 1 : 0,
-                               dk_weight ? 1 : 0);
+                               turn, tokens, (int)head_dim, eps, lg, steps(hq.heads), steps(hk.heads),
+                               (float*)workspace, dq_weight ? 1 : 0, dk_weight ? 1 : 0);
             });
             if (e != hipSuccess || need == 0) return e;
             const dim3 grid((uint32_t)((head_dim + 63) / 64), 2);
