@@ -32,6 +32,8 @@ struct Turn {
     int32_t id_bytes, pairs;
 };
 
+typedef uint32_t u32x2_a2 __attribute__((ext_vector_type(2), aligned(2)));
+
 // A lane's slot of W pairs: elements first(s) + c and second(s) + c for halves,
 // first(s) + 2 c and + 2 c + 1 for adjacent pairs. Elements that are not rotated
 // are paired alike, (i, i + half of them).
@@ -62,6 +64,12 @@ struct Slot {
                 r.p[0] = *gbl<uint32_t>(x + a);
                 r.q[0] = *gbl<uint32_t>(x + b);
             }
+        } else if constexpr (W * sizeof(T) == 8) {
+            const u32x2 p = *gbl<u32x2_a2>(x + a), q = *gbl<u32x2_a2>(x + b);
+            r.p[0] = p[0];
+            r.p[1] = p[1];
+            r.q[0] = q[0];
+            r.q[1] = q[1];
         } else {
             r.p = kOnce ? load16_once(x + a) : load16(x + a);
             r.q = kOnce ? load16_once(x + b) : load16(x + b);
@@ -73,7 +81,7 @@ struct Slot {
             u[0] = __uint_as_float(r.p[0]);
             v[0] = __uint_as_float(r.q[0]);
         } else {
-            float p[W], q[W];
+            float p[kVecOf<T>], q[kVecOf<T>];
             widen(r.p, p);
             widen(r.q, q);
 #pragma unroll
@@ -94,14 +102,20 @@ struct Slot {
                 *gbl_mut<float>(x + b) = v[0];
             }
         } else {
-            float p[W], q[W];
+            float p[kVecOf<T>] = {}, q[kVecOf<T>] = {};
 #pragma unroll
             for (int c = 0; c < W; ++c) {
                 p[c] = !kAdjacent ? u[c] : c & 1 ? v[c / 2] : u[c / 2];
                 q[c] = !kAdjacent ? v[c] : c & 1 ? v[W / 2 + c / 2] : u[W / 2 + c / 2];
             }
-            store16(x + a, narrow(p));
-            store16(x + b, narrow(q));
+            const u32x4 lo = narrow(p), hi = narrow(q);
+            if constexpr (W * sizeof(T) == 8) {
+                *gbl_mut<u32x2_a2>(x + a) = u32x2{lo[0], lo[1]};
+                *gbl_mut<u32x2_a2>(x + b) = u32x2{hi[0], hi[1]};
+            } else {
+                store16(x + a, lo);
+                store16(x + b, hi);
+            }
         }
     }
 };
@@ -460,26 +474,26 @@ tide_status check_turn(const tide_rotation* r, int64_t tokens, int32_t dim, Turn
     return TIDE_OK;
 }
 
-// Calls go(T, W, NS, adjacent, lane_log2): whole vectors where every slot of W
-// pairs lies on one side of the rotated elements' end, single pairs otherwise.
+// Calls go(T, W, NS, adjacent, lane_log2), with the widest slots of W pairs that
+// lie on one side of the rotated elements' end each: whole vectors, half ones of
+// bf16, or single pairs.
 template <class F>
 hipError_t with_slots(int32_t size, int dim, int pairs, bool adjacent, F&& go) {
-    const int W = size == 2 ? 8 : 4, half = dim / 2;
-    const bool whole = half % W == 0 && pairs % W == 0;
-    const int slots = whole ? half / W : half;
-    int lg = 0;
-    while (lg < 6 && (1 << lg) < slots) ++lg;
-    const auto with = [&](auto type) {
-        using T = decltype(type);
-        constexpr int V = kVecOf<T>;
-        using One = std::integral_constant<int, 1>;
-        using Vec = std::integral_constant<int, V>;
-        using Four = std::integral_constant<int, kMostDim / 128>;
-        if (whole)
-            return adjacent ? go(type, Vec{}, One{}, std::true_type{}, lg) : go(type, Vec{}, One{}, std::false_type{}, lg);
-        return adjacent ? go(type, One{}, Four{}, std::true_type{}, lg) : go(type, One{}, Four{}, std::false_type{}, lg);
+    const int half = dim / 2;
+    const auto fits = [&](int w) { return half % w == 0 && pairs % w == 0; };
+    const auto with = [&](auto type, auto w, auto ns) {
+        const int slots = half / w.value;
+        int lg = 0;
+        while (lg < 6 && (1 << lg) < slots) ++lg;
+        return adjacent ? go(type, w, ns, std::true_type{}, lg) : go(type, w, ns, std::false_type{}, lg);
     };
-    return size == 2 ? with(uint16_t{}) : with(float{});
+    using One = std::integral_constant<int, 1>;
+    using Four = std::integral_constant<int, 4>;
+    using Eight = std::integral_constant<int, 8>;
+    using Most = std::integral_constant<int, kMostDim / 128>;
+    if (size == 2)
+        return fits(8) ? with(uint16_t{}, Eight{}, One{}) : fits(4) ? with(uint16_t{}, Four{}, One{}) : with(uint16_t{}, One{}, Most{});
+    return fits(4) ? with(float{}, Four{}, One{}) : with(float{}, One{}, Most{});
 }
 
 tide_status check_type(int32_t dtype) {

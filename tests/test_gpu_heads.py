@@ -87,6 +87,7 @@ CASES = [  # T, Hq, Hk, D, pairs, adjacent
     (1, 32, 4, 128, 64, False), (5, 3, 1, 64, 32, False), (37, 4, 2, 128, 64, True), (9, 2, 2, 128, 32, False),
     (9, 2, 2, 128, 32, True), (4, 5, 1, 80, 40, False), (4, 3, 3, 96, 20, False), (6, 2, 1, 2, 1, False), (6, 2, 1, 2, 1, True),
     (3, 2, 1, 20, 7, False), (3, 2, 1, 20, 7, True), (3, 1, 1, 512, 256, False), (3, 1, 1, 510, 255, True), (3, 2, 1, 500, 100, False),
+    (5, 2, 1, 80, 20, False), (5, 2, 1, 80, 20, True), (3, 1, 1, 512, 100, False),
     (7, 3, 2, 256, 128, True), (8, 2, 1, 64, 0, False), (130, 9, 1, 128, 64, False), (0, 2, 1, 64, 32, False), (3, 0, 2, 64, 32, False),
     (3, 2, 0, 64, 32, False), (2, 2, 1, 0, 0, False)]
 
