@@ -8,31 +8,21 @@ Argument marshalling only, as in _layer.py: tensors with unit column stride are
 taken with their row strides, outputs are passed in.
 """
 import ctypes
+import struct
 from typing import Optional, Sequence, Union
 
 from ._lib import PointerTable, _check
 from ._layer import (_SIGNATURES, _dtype_code, _flat, _fn, _mat, _on, _place, _run, _workspace)
 
 
-class Heads(ctypes.Structure):
-    """tide_heads."""
-    _fields_ = [("data", ctypes.c_void_p), ("token_stride", ctypes.c_int64),
-                ("head_stride", ctypes.c_int64), ("heads", ctypes.c_int32),
-                ("reserved", ctypes.c_int32)]
-
-
-class Rotation(ctypes.Structure):
-    """tide_rotation."""
-    _fields_ = [("positions", ctypes.c_void_p), ("cos", ctypes.c_void_p),
-                ("sin", ctypes.c_void_p), ("table_rows", ctypes.c_int64),
-                ("table_stride", ctypes.c_int64), ("id_bytes", ctypes.c_int32),
-                ("pairs", ctypes.c_int32), ("adjacent", ctypes.c_int32),
-                ("reserved", ctypes.c_int32)]
+# The structures as bytes, which ctypes passes as a pointer: a call of a few
+# microseconds would spend two on objects of ctypes.Structure.
+Heads = struct.Struct("@Pqqii").pack        # tide_heads: data, strides, heads, reserved
+Rotation = struct.Struct("@PPPqqiiii").pack  # tide_rotation, in the header's order
 
 
 _I32, _I64, _VP, _F32, _F64 = (ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p, ctypes.c_float,
                                ctypes.c_double)
-_HP, _RP = ctypes.POINTER(Heads), ctypes.POINTER(Rotation)
 _SIGNATURES.update({
     "tide_sort_ids_workspace": [_I64, _I64, ctypes.POINTER(_I64)],
     "tide_sort_ids": [_VP, _I32, _I64, _I64, _VP, _VP, _VP, _I64, _VP],
@@ -44,9 +34,9 @@ _SIGNATURES.update({
                             _VP],
     "tide_token_logprobs_grad": [_I32, _VP, _I64, _I64, _I64, _VP, _I32, _VP, _VP, _VP, _VP, _VP,
                                  _I64, _VP],
-    "tide_norm_rotate": [_I32, _I64, _I32, _HP, _HP, _VP, _VP, _F32, _RP, _HP, _HP, _VP],
+    "tide_norm_rotate": [_I32, _I64, _I32, _VP, _VP, _VP, _VP, _F32, _VP, _VP, _VP, _VP],
     "tide_norm_rotate_grad_workspace": [_I64, _I32, _I32, ctypes.POINTER(_I64)],
-    "tide_norm_rotate_grad": [_I32, _I64, _I32, _HP, _HP, _HP, _HP, _VP, _VP, _F32, _RP, _HP, _HP,
+    "tide_norm_rotate_grad": [_I32, _I64, _I32, _VP, _VP, _VP, _VP, _VP, _VP, _F32, _VP, _VP, _VP,
                               _VP, _VP, _I32, _VP, _I64, _VP],
     "tide_grad_squares_workspace": [_I32, _VP, _I32, ctypes.POINTER(_I64)],
     "tide_grad_squares": [_I32, _VP, _VP, _I32, _VP, _I32, _VP, _I64, _VP],
@@ -191,16 +181,17 @@ def token_logprobs_grad(logits, targets, stats, dlogprob, dlogits, entropy=None,
 # -------------------------------------------------------------- norm, rotation
 
 def _heads(t, what: str, dtype, tokens: Optional[int], heads: Optional[int], dim: Optional[int],
-           dev) -> Heads:
+           dev) -> bytes:
     """tide_heads of a (tokens, heads, head_dim) tensor whose heads are contiguous."""
     if t.dtype is not dtype:
         raise TypeError("%s has dtype %s, expected %s" % (what, t.dtype, dtype))
     if t.dim() != 3:
         raise ValueError("%s has %d dimensions, expected 3" % (what, t.dim()))
     T, H, D = t.shape
-    for got, want, name in ((T, tokens, "tokens"), (H, heads, "heads"), (D, dim, "elements a head")):
-        if want is not None and got != want:
-            raise ValueError("%s has %d %s, expected %d" % (what, got, name, want))
+    if T != tokens or H != heads or D != dim:
+        for got, want, name in ((T, tokens, "tokens"), (H, heads, "heads"), (D, dim, "elements a head")):
+            if want is not None and got != want:
+                raise ValueError("%s has %d %s, expected %d" % (what, got, name, want))
     st, sh, sd = t.stride()
     if D > 1 and sd != 1 and t.numel():
         raise ValueError("%s: a head's elements are not adjacent" % what)
@@ -208,7 +199,7 @@ def _heads(t, what: str, dtype, tokens: Optional[int], heads: Optional[int], dim
     return Heads(t.data_ptr(), st if T > 1 else max(H * D, 1), sh if H > 1 else D, H, 0)
 
 
-def _rotation(positions, cos, sin, adjacent: bool, tokens: int, dev) -> Optional[Rotation]:
+def _rotation(positions, cos, sin, adjacent: bool, tokens: int, dev) -> Optional[bytes]:
     import torch
     if cos is None and sin is None:
         if positions is not None:

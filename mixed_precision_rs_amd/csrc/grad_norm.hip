@@ -22,6 +22,8 @@ template <class T>
 constexpr int kTileOf = kTileBytes / (int)sizeof(T);
 constexpr int kMostTensors = 128;      // in one launch's arguments
 constexpr int64_t kMostGroups = 8192;
+// Tiles that one workgroup sums alone, in one launch.
+constexpr int64_t kAlone = 8;
 // Tensors that together pass the memory-side cache (256 MiB) are read past the
 // caches (1.2 GB in 391 tensors: squares 63 us instead of 70 for each 0.4 GB,
 // clipping 143 instead of 149); smaller ones by ordinary loads, so that clipping
@@ -71,8 +73,9 @@ __device__ __forceinline__ void each_vector(const Tensors& a, int tile, F&& f) {
         f(i, e, hi - e < N ? (int)(hi - e) : N);
 }
 
+// Each workgroup's sum into partial; one workgroup alone writes the total.
 template <class T, bool kOnce>
-__global__ __launch_bounds__(kThreads) void sum_squares(Tensors a, double* partial) {
+__global__ __launch_bounds__(kThreads) void sum_squares(Tensors a, double* partial, double* total, int accumulate) {
     constexpr int N = kVecOf<T>;
     double sum = 0.0;
     for (int tile = blockIdx.x; tile < a.tiles; tile += gridDim.x)
@@ -83,7 +86,9 @@ __global__ __launch_bounds__(kThreads) void sum_squares(Tensors a, double* parti
             for (int c = 0; c < N; ++c) sum = __builtin_fma((double)v[c], (double)v[c], sum);
         });
     sum = block_sum<kThreads>(sum);
-    if (threadIdx.x == 0) *gbl_mut<double>(partial + blockIdx.x) = sum;
+    if (threadIdx.x) return;
+    if (total) *gbl_mut<double>(total) = accumulate ? *gbl<double>(total) + sum : sum;
+    else *gbl_mut<double>(partial + blockIdx.x) = sum;
 }
 
 constexpr int kSumThreads = 1024;
@@ -191,7 +196,7 @@ tide_status tide_grad_squares_workspace(int32_t dtype, const int64_t* elems, int
             groups += g;
             return hipSuccess;
         });
-        *bytes = groups * 8;
+        *bytes = groups <= kAlone ? 0 : groups * 8;
         return TIDE_OK;
     });
 }
@@ -218,15 +223,18 @@ tide_status tide_grad_squares(int32_t dtype, const void* const* grads, const int
         }
         const bool once = past_caches(elems, tensors, size);
         return on_stream(stream, [&](hipStream_t s) {
+            const bool alone = need == 0;          // no tile, or one launch of kAlone at most
+            bool none = true;
             const hipError_t e = each_launch(grads, nullptr, elems, tensors, size,
                                              [&](const Tensors& a, int64_t groups, int64_t before) {
-                double* to = (double*)workspace + before;
-                const dim3 grid((uint32_t)groups);
+                none = false;
                 const auto kernel = once ? (size == 2 ? sum_squares<uint16_t, true> : sum_squares<float, true>)
                                          : (size == 2 ? sum_squares<uint16_t, false> : sum_squares<float, false>);
-                return enqueue(kernel, grid, kThreads, 0, s, a, to);
+                return enqueue(kernel, dim3(alone ? 1 : (uint32_t)groups), kThreads, 0, s, a,
+                               alone ? nullptr : (double*)workspace + before, alone ? total : nullptr,
+                               accumulate ? 1 : 0);
             });
-            if (e != hipSuccess) return e;
+            if (e != hipSuccess || (alone && !none)) return e;
             return enqueue(sum_partials, dim3(1), kSumThreads, 0, s, (const double*)workspace, need / 8, total,
                            accumulate ? 1 : 0);
         });

@@ -112,14 +112,14 @@ def test_logprobs_refuse(call):
 
 def heads(i, token_stride=1024, head_stride=64, n=8, reserved=0):
     from mixed_precision_rs_amd._step import Heads
-    return Heads(None if i is None else at(i), token_stride, head_stride, n, reserved)
+    return Heads(0 if i is None else at(i), token_stride, head_stride, n, reserved)
 
 
 def rotation(**kw):
     from mixed_precision_rs_amd._step import Rotation
     ok = dict(positions=at(10), cos=at(11), sin=at(12), table_rows=100, table_stride=32, id_bytes=8, pairs=32, adjacent=0, reserved=0)
     ok.update(kw)
-    return Rotation(*ok.values())
+    return Rotation(*[v or 0 for v in ok.values()])
 
 
 def test_norm_rotate_refuses(call):
@@ -134,9 +134,8 @@ def test_norm_rotate_refuses(call):
     assert r(q=heads(0, token_stride=63)) == ARG and r(q=heads(0, head_stride=63)) == ARG
     assert r(q=heads(0, token_stride=100, head_stride=64)) == ARG                 # tokens and heads interleave
     assert r(q=heads(0, token_stride=1 << 62)) == OVER
-    bad = heads(0)
-    bad.data = at(0) + 1
-    assert r(q=bad) == ALIGN and r(qw=at(2) + 1) == ALIGN and r(kw=at(3) + 1) == ALIGN
+    from mixed_precision_rs_amd._step import Heads
+    assert r(q=Heads(at(0) + 1, 1024, 64, 8, 0)) == ALIGN and r(qw=at(2) + 1) == ALIGN and r(kw=at(3) + 1) == ALIGN
     assert r(qo=heads(0)) == ARG and r(ko=heads(4, n=2)) == ARG and r(qo=heads(2)) == ARG and r(ko=heads(11, n=2)) == ARG
     for kw in (dict(pairs=33), dict(pairs=-1), dict(reserved=1), dict(id_bytes=2), dict(cos=None), dict(sin=None), dict(table_stride=31),
                dict(positions=None, table_rows=4), dict(table_rows=-1)):
@@ -156,7 +155,7 @@ def test_norm_rotate_grad_refuses(call, tide):
     assert r(dqw=at(8) + 1) == ALIGN and r(rot=rotation(pairs=33)) == ARG
 
 
-def lists(*pointers, n=100):
+def lists(*pointers, n=100000):
     return (ctypes.c_void_p * len(pointers))(*pointers), (ctypes.c_int64 * len(pointers))(*[n] * len(pointers))
 
 
@@ -169,7 +168,9 @@ def test_grad_squares_refuses(call):
     assert r(total=at(0) + 8) == ARG and r(ws=at(1)) == ARG and r(total=at(3)) == ARG
     assert r(elems=(ctypes.c_int64 * 2)(5, -1)) == ARG and r(elems=(ctypes.c_int64 * 2)(1 << 62, 1 << 62)) == OVER
     need = ctypes.c_int64()
-    assert call("grad_squares_workspace", 0, n, 2, None) == ARG and call("grad_squares_workspace", 0, n, 2, need) == OK and need.value == 16
+    assert call("grad_squares_workspace", 0, n, 2, None) == ARG and call("grad_squares_workspace", 0, n, 2, need) == OK and need.value == 26 * 8
+    few = (ctypes.c_int64 * 2)(100, 7)
+    assert call("grad_squares_workspace", 0, few, 2, need) == OK and need.value == 0
     assert call("grad_squares_workspace", 1, None, 0, need) == OK and need.value == 0
 
 
@@ -180,14 +181,14 @@ def test_clip_refuses(call):
     assert r(dtype=2) == ARG and r(tensors=-1) == ARG and r(grads=None) == ARG and r(total=None) == ARG and r(total=at(2) + 4) == ALIGN
     assert r(most=-1.0) == ARG and r(most=math.nan) == ARG and r(norm=at(3) + 2) == ALIGN
     assert r(grads=lists(at(0), None)[0]) == ARG and r(out=lists(at(4), None)[0]) == ARG and r(out=lists(at(4), at(5) + 2)[0]) == ALIGN
-    assert r(out=lists(at(4), at(4) + 396)[0]) == ARG                          # two outputs share four bytes
+    assert r(out=lists(at(4), at(4) + 399996)[0]) == ARG                          # two outputs share four bytes
     assert r(out=lists(at(1), at(5))[0]) == ARG                                # an output is another gradient
     assert r(out=lists(at(0) + 4, at(5))[0]) == ARG                            # not quite in place
     assert r(out=lists(at(2), at(5))[0]) == ARG and r(norm=at(4)) == ARG and r(norm=at(2)) == ARG and r(norm=at(0) + 8) == ARG
     same = lists(at(0), at(0))[0]
     assert r(grads=same, out=None) == ARG and r(grads=same, out=same) == ARG   # twice in place
     if not torch.cuda.is_available():                                          # accepted: the call then finds no GPU
-        assert r(grads=same) == HIP and r(out=None) == HIP and r(out=lists(at(0), at(1) + 400)[0]) == HIP
+        assert r(grads=same) == HIP and r(out=None) == HIP and r(out=lists(at(0), at(1) + 400000)[0]) == HIP
 
 
 def test_windows_of_fused_rows_do_not_overlap(call):
