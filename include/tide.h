@@ -739,6 +739,11 @@ tide_status tide_embed_tokens_grad(int32_t dtype, const void* dout, int64_t dout
                                    int64_t grad_stride, int32_t accumulate, void* workspace,
                                    int64_t workspace_bytes, void* stream);
 
+/* Bytes of device workspace tide_token_logprobs needs (0 for many tokens).
+ * Host-only. Errors: INVALID_ARG, UNSUPPORTED. */
+tide_status tide_token_logprobs_workspace(int32_t dtype, int64_t tokens, int64_t vocab, int32_t top,
+                                          int64_t* bytes);
+
 /*
  * Log probabilities of given tokens from logits (tokens x vocab), in one pass,
  * in fp32. With m the largest logit of a row and s = sum exp(x - m):
@@ -758,13 +763,16 @@ tide_status tide_embed_tokens_grad(int32_t dtype, const void* dout, int64_t dout
  * -infinity, log probability -infinity and entropy 0. In a row that holds a NaN
  * or +infinity, log(s), entropy and log probabilities are NaN.
  *   targets: tokens ids of id_bytes (4 or 8: int32 or int64).
+ *   workspace: tide_token_logprobs_workspace bytes, 8-byte aligned (may be NULL
+ *            when that is 0); what it holds does not matter.
  * Errors: INVALID_ARG, ALIGNMENT, OVERFLOW, UNSUPPORTED (vocab past 2^31 - 1,
  * top past 32), HIP.
  */
 tide_status tide_token_logprobs(int32_t dtype, const void* logits, int64_t logits_stride,
                                 int64_t tokens, int64_t vocab, const void* targets,
                                 int32_t id_bytes, float* logprob, float* stats, float* entropy,
-                                int32_t top, int32_t* top_ids, float* top_logprobs, void* stream);
+                                int32_t top, int32_t* top_ids, float* top_logprobs,
+                                void* workspace, int64_t workspace_bytes, void* stream);
 
 /*
  * Gradient of tide_token_logprobs to the logits, in fp32, rounded once: with

@@ -79,6 +79,7 @@ from ._step import (  # noqa: F401
     sort_ids_workspace_bytes,
     token_logprobs,
     token_logprobs_grad,
+    token_logprobs_workspace_bytes,
 )
 
 lib()  # load now: no silent fallback exists

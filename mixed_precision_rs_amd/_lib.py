@@ -41,7 +41,8 @@ EXPORTS = ["tide_plan_create", "tide_plan_destroy", "tide_plan_dims", "tide_plan
            "tide_checkpoint_unpack", "tide_gated_silu", "tide_gated_silu_grad",
            "tide_weight_grads_workspace", "tide_weight_grads_bf16", "tide_sort_ids_workspace",
            "tide_sort_ids", "tide_embed_tokens", "tide_embed_tokens_grad_workspace",
-           "tide_embed_tokens_grad", "tide_token_logprobs", "tide_token_logprobs_grad",
+           "tide_embed_tokens_grad", "tide_token_logprobs",
+           "tide_token_logprobs_workspace", "tide_token_logprobs_grad",
            "tide_norm_rotate", "tide_norm_rotate_grad_workspace", "tide_norm_rotate_grad",
            "tide_grad_squares_workspace", "tide_grad_squares", "tide_clip_grads"]
 

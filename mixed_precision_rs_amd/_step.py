@@ -30,8 +30,9 @@ _SIGNATURES.update({
     "tide_embed_tokens_grad_workspace": [_I64, _I64, ctypes.POINTER(_I64)],
     "tide_embed_tokens_grad": [_I32, _VP, _I64, _I64, _I64, _VP, _VP, _I64, _F32, _VP, _I64, _I32,
                                _VP, _I64, _VP],
+    "tide_token_logprobs_workspace": [_I32, _I64, _I64, _I32, ctypes.POINTER(_I64)],
     "tide_token_logprobs": [_I32, _VP, _I64, _I64, _I64, _VP, _I32, _VP, _VP, _VP, _I32, _VP, _VP,
-                            _VP],
+                            _VP, _I64, _VP],
     "tide_token_logprobs_grad": [_I32, _VP, _I64, _I64, _I64, _VP, _I32, _VP, _VP, _VP, _VP, _VP,
                                  _I64, _VP],
     "tide_norm_rotate": [_I32, _I64, _I32, _VP, _VP, _VP, _VP, _F32, _VP, _VP, _VP, _VP],
@@ -126,14 +127,22 @@ def embed_tokens_grad(dout, offsets, order, grad, scale: float = 1.0, accumulate
 
 # ---------------------------------------------------------- log probabilities
 
+def token_logprobs_workspace_bytes(logits, top: int = 0) -> int:
+    """Bytes of workspace token_logprobs needs for these logits
+    (tide_token_logprobs_workspace)."""
+    return _bytes("tide_token_logprobs_workspace", _dtype_code(logits, "logits"), *logits.shape, top)
+
+
 def token_logprobs(logits, targets, logprob, stats=None, entropy=None, top_ids=None,
-                   top_logprobs=None, stream=None) -> None:
+                   top_logprobs=None, workspace=None, stream=None) -> None:
     """Log probabilities of the target tokens, entropies and the most probable
     alternatives in one pass over the logits (tide_token_logprobs). logits:
     (tokens, vocab) bf16 or fp32; targets: (tokens,) int32 or int64, anything
     outside [0, vocab) for a position that does not count; logprob, entropy:
     (tokens,) fp32; stats: (tokens, 2) fp32, for token_logprobs_grad; top_ids
-    (tokens, top) int32 and top_logprobs (tokens, top) fp32, top up to 32."""
+    (tokens, top) int32 and top_logprobs (tokens, top) fp32, top up to 32.
+    workspace: uint8 tensor of token_logprobs_workspace_bytes(), by default
+    allocated for the call."""
     import torch
     sh, sobj, dev = _on(stream, logits)
     code = _dtype_code(logits, "logits")
@@ -150,8 +159,11 @@ def token_logprobs(logits, targets, logprob, stats=None, entropy=None, top_ids=N
         top = top_ids.shape[-1]
         ip = _flat(top_ids, "top_ids", torch.int32, (n, top), dev)
         qp = _flat(top_logprobs, "top_logprobs", torch.float32, (n, top), dev)
+    need = _bytes("tide_token_logprobs_workspace", code, n, V, top)
+    wp, wn, w = _workspace(need, workspace, stream, dev)
     _run("tide_token_logprobs", (code, lp, ls, n, V, tp, targets.element_size(), pp, sp, ep, top,
-         ip, qp, sh), dev, [logits, targets, logprob, stats, entropy, top_ids, top_logprobs], sobj)
+         ip, qp, wp, wn, sh), dev, [logits, targets, logprob, stats, entropy, top_ids,
+         top_logprobs, w], sobj)
 
 
 def token_logprobs_grad(logits, targets, stats, dlogprob, dlogits, entropy=None, dentropy=None,

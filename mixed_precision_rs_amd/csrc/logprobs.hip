@@ -128,9 +128,10 @@ __device__ __forceinline__ int vector_of(const T* row, int64_t V, int64_t u, flo
     return n;
 }
 
-// The alternatives of a row, by a workgroup whose lane i has the vectors i, i +
-// kThreads, ... of it and has found the largest logit `most` of them, in vector
-// `unit` (-1: none above -infinity).
+// The alternatives among the vectors begin .. end - 1 of a row, by a workgroup whose
+// lane i has the vectors begin + i, begin + i + kThreads, ... and has found the
+// largest logit `most` of them, in vector `unit` (-1: none above -infinity).
+// emit(place, order) is called for each of the `top` places, with 0 for none.
 //
 // 64 groups of lanes put forward their best; the top-th of these is no better than
 // the top-th of all logits, and only lanes whose own best reaches it can hold an
@@ -145,12 +146,27 @@ struct TopSpace {
     uint16_t lanes[1024];
     int lanes_count, count;
 };
-template <class T, int kThreads>
-__device__ __forceinline__ void alternatives(const T* row, int64_t V, float most, int64_t unit, float m, float log_s,
-                                             int32_t top, int32_t* ids, float* logprobs, TopSpace& w) {
+// Ranks w.found[0 .. count) by all threads of the workgroup.
+template <class F>
+__device__ __forceinline__ void rank_found(const TopSpace& w, int count, int threads, int32_t top, F&& emit) {
+    for (int i = threadIdx.x; i < count; i += threads) {
+        const uint64_t o = w.found[i];
+        int at = 0, j = 0;
+        for (; j + 16 <= count; j += 16) {         // sixteen reads under way
+#pragma unroll
+            for (int k = 0; k < 16; ++k) at += w.found[j + k] > o ? 1 : 0;
+        }
+        for (; j < count; ++j) at += w.found[j] > o ? 1 : 0;
+        if (at < top) emit(at, o);
+    }
+    for (int i = threadIdx.x; i < top; i += threads)
+        if (i >= count) emit(i, 0);
+}
+template <class T, int kThreads, class F>
+__device__ __forceinline__ void alternatives(const T* row, int64_t V, int64_t begin, int64_t end, float most,
+                                             int64_t unit, int32_t top, TopSpace& w, F&& emit) {
     constexpr int N = kVecOf<T>, kGroup = kThreads / 64;
     const int tid = threadIdx.x, lane = tid & 63;
-    const int64_t units = (V + N - 1) / N;
     uint64_t mine = 0;
     if (unit >= 0) {
         float v[N];
@@ -171,11 +187,12 @@ __device__ __forceinline__ void alternatives(const T* row, int64_t V, float most
     const uint64_t least = last ? (uint64_t)__shfl((unsigned long long)c, __ffsll((long long)last) - 1) : 1;
     if (mine >= least) w.lanes[atomicAdd(&w.lanes_count, 1)] = (uint16_t)tid;
     __syncthreads();
-    const uint32_t per = (uint32_t)((units + kThreads - 1) / kThreads);
+    const uint32_t per = (uint32_t)((end - begin + kThreads - 1) / kThreads);
     const int64_t items = (int64_t)w.lanes_count * per;
     for (int64_t i = tid; i < items; i += kThreads) {
-        const int64_t l = items >> 32 ? i / per : (int64_t)((uint32_t)i / per), u = w.lanes[l] + (i - l * per) * kThreads;
-        if (u >= units) continue;
+        const int64_t l = items >> 32 ? i / per : (int64_t)((uint32_t)i / per);
+        const int64_t u = begin + w.lanes[l] + (i - l * per) * kThreads;
+        if (u >= end) continue;
         float v[N];
         const int n = vector_of(row, V, u, v);
 #pragma unroll
@@ -190,18 +207,7 @@ __device__ __forceinline__ void alternatives(const T* row, int64_t V, float most
     __syncthreads();
     const int count = w.count;
     if (count <= kFound) {
-        for (int i = tid; i < count; i += kThreads) {
-            const uint64_t o = w.found[i];
-            int at = 0;
-            for (int j = 0; j < count; ++j) at += w.found[j] > o ? 1 : 0;
-            if (at >= top) continue;
-            *gbl_mut<int32_t>(ids + at) = id_of(o);
-            *gbl_mut<float>(logprobs + at) = (logit_of(o) - m) - log_s;
-        }
-        if (tid >= count && tid < top) {
-            *gbl_mut<int32_t>(ids + tid) = -1;
-            *gbl_mut<float>(logprobs + tid) = kNegInf;
-        }
+        rank_found(w, count, kThreads, top, emit);
         return;
     }
     for (int32_t j = 0; j < top; ++j) {
@@ -212,15 +218,12 @@ __device__ __forceinline__ void alternatives(const T* row, int64_t V, float most
         uint64_t b = w.best[0];
 #pragma unroll
         for (int i = 1; i < kGroup; ++i) b = w.best[i] > b ? w.best[i] : b;
-        if (tid == 0) {
-            *gbl_mut<int32_t>(ids + j) = b ? id_of(b) : -1;
-            *gbl_mut<float>(logprobs + j) = b ? (logit_of(b) - m) - log_s : kNegInf;
-        }
+        if (tid == 0) emit(j, b);
         // The owner's next, looked for by its whole wave.
-        const int owner = (int)(id_of(b) / N % kThreads);
+        const int owner = (int)((id_of(b) / N - begin) % kThreads);
         if (b == 0 || owner >> 6 != tid >> 6) continue;
         uint64_t next = 0;
-        for (int64_t u = owner + (int64_t)lane * kThreads; u < units; u += 64 * kThreads) {
+        for (int64_t u = begin + owner + (int64_t)lane * kThreads; u < end; u += 64 * kThreads) {
             float v[N];
             const int n = vector_of(row, V, u, v);
 #pragma unroll
@@ -234,22 +237,62 @@ __device__ __forceinline__ void alternatives(const T* row, int64_t V, float most
     }
 }
 
-// One workgroup a row. A lane has 32 logits in hand at a time.
-template <class T, class Id, int kThreads, bool kEntropy, bool kTop>
-__global__ __launch_bounds__(kThreads) void row_logprobs(
-    const T* logits, int64_t stride, int64_t tokens, int64_t V, const Id* targets, float* logprob,
-    float* stats, float* entropy, int32_t top, int32_t* top_ids, float* top_logprobs) {
+// A row's results from its sums, by thread 0.
+struct Outputs {
+    float *logprob, *stats, *entropy;
+    int32_t* top_ids;
+    float* top_logprobs;
+    int32_t top;
+};
+template <class T, class Id>
+__device__ __forceinline__ void put_row(const Outputs& to, const T* row, int64_t r, int64_t V, const Id* targets,
+                                        const Sums& a, float log_s) {
+    const bool none = a.s == 0.0;                  // no logit above -infinity
+    const Id at = *gbl<Id>(targets + r);
+    float lp = 0.0f;
+    if (at >= 0 && (int64_t)at < V) {
+        float x;
+        if constexpr (sizeof(T) == 2) x = lo_bf16(*gbl<T>(row + at));
+        else x = *gbl<float>(row + at);
+        lp = none ? kNegInf : (x - a.m) - log_s;
+    }
+    *gbl_mut<float>(to.logprob + r) = lp;
+    if (to.stats) {
+        *gbl_mut<float>(to.stats + 2 * r) = none ? kNegInf : a.m;
+        *gbl_mut<float>(to.stats + 2 * r + 1) = log_s;
+    }
+    if (to.entropy) *gbl_mut<float>(to.entropy + r) = none ? 0.0f : log_s - (float)(a.t / a.s);
+}
+__device__ __forceinline__ void put_alternative(const Outputs& to, int64_t r, int at, uint64_t o, float m, float log_s) {
+    *gbl_mut<int32_t>(to.top_ids + r * to.top + at) = o ? id_of(o) : -1;
+    *gbl_mut<float>(to.top_logprobs + r * to.top + at) = o ? (logit_of(o) - m) - log_s : kNegInf;
+}
+
+// One workgroup a row, or, with kPart, a part of one, whose sums and best logits go
+// to the workspace. A lane has 32 logits in hand at a time.
+struct Parts {
+    Sums* sums;            // [row][parts]
+    uint64_t* found;       // [row][parts][top]
+    int64_t units;         // vectors of a part
+    int32_t parts;
+};
+template <class T, class Id, int kThreads, bool kEntropy, bool kTop, bool kPart>
+__global__ __launch_bounds__(kThreads) void row_logprobs(const T* logits, int64_t stride, int64_t tokens, int64_t V,
+                                                         const Id* targets, Outputs to, Parts parts) {
     constexpr int N = kVecOf<T>, KU = 32 / N, kWaves = kThreads / 64;
     __shared__ Sums part[kWaves];
     __shared__ std::conditional_t<kTop, TopSpace, int> space;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int64_t units = (V + N - 1) / N, whole = V / N;
+    const int64_t units = (V + N - 1) / N;
     for (int64_t r = blockIdx.x; r < tokens; r += gridDim.x) {
         const T* row = logits + r * stride;
+        const int64_t begin = kPart ? blockIdx.y * parts.units : 0;
+        const int64_t end = kPart && begin + parts.units < units ? begin + parts.units : units;
+        const int64_t whole = end < V / N ? end : V / N;
         Sums a{kLowest, 0.0, 0.0};
         float most = kNegInf;
         int64_t unit = -1;
-        for (int64_t u0 = 0; u0 < units; u0 += KU * kThreads) {
+        for (int64_t u0 = begin; u0 < end; u0 += KU * kThreads) {
             float v[KU][N];
             float m = a.m;
             if (u0 + KU * kThreads <= whole) {
@@ -261,7 +304,7 @@ __global__ __launch_bounds__(kThreads) void row_logprobs(
             } else {
 #pragma unroll
                 for (int j = 0; j < KU; ++j) {
-                    const int64_t u = u0 + j * kThreads + tid, left = V - u * N;
+                    const int64_t u = u0 + j * kThreads + tid, left = u < end ? V - u * N : 0;
 #pragma unroll
                     for (int c = 0; c < N; ++c) v[j][c] = kNegInf;
                     if (left <= 0) continue;
@@ -290,26 +333,48 @@ __global__ __launch_bounds__(kThreads) void row_logprobs(
             __syncthreads();
             a = join_lanes<kWaves>(part[lane % kWaves]);
         }
-        const bool none = a.s == 0.0;              // no logit above -infinity
-        const float log_s = none ? kNegInf : log_of(a.s);
-        if (tid == 0) {
-            const Id at = *gbl<Id>(targets + r);
-            float lp = 0.0f;
-            if (at >= 0 && (int64_t)at < V) {
-                float x;
-                if constexpr (sizeof(T) == 2) x = lo_bf16(*gbl<T>(row + at));
-                else x = *gbl<float>(row + at);
-                lp = none ? kNegInf : (x - a.m) - log_s;
-            }
-            *gbl_mut<float>(logprob + r) = lp;
-            if (stats) {
-                *gbl_mut<float>(stats + 2 * r) = none ? kNegInf : a.m;
-                *gbl_mut<float>(stats + 2 * r + 1) = log_s;
-            }
-            if (kEntropy) *gbl_mut<float>(entropy + r) = none ? 0.0f : log_s - (float)(a.t / a.s);
+        if constexpr (kPart) {
+            const int64_t p = r * parts.parts + blockIdx.y;
+            if (tid == 0) parts.sums[p] = a;
+            if constexpr (kTop)
+                alternatives<T, kThreads>(row, V, begin, end, most, unit, to.top, space,
+                                          [&](int at, uint64_t o) { parts.found[p * to.top + at] = o; });
+        } else {
+            const float log_s = a.s == 0.0 ? kNegInf : log_of(a.s);
+            if (tid == 0) put_row(to, row, r, V, targets, a, log_s);
+            if constexpr (kTop)
+                alternatives<T, kThreads>(row, V, begin, end, most, unit, to.top, space,
+                                          [&](int at, uint64_t o) { put_alternative(to, r, at, o, a.m, log_s); });
         }
-        if constexpr (kTop)
-            alternatives<T, kThreads>(row, V, most, unit, a.m, log_s, top, top_ids + r * top, top_logprobs + r * top, space);
+        __syncthreads();
+    }
+}
+
+// A row's parts joined, by one workgroup; the alternatives of the parts are ranked
+// as those of a row's lanes are.
+constexpr int kMostParts = 16, kJoinThreads = 256;
+template <class T, class Id>
+__global__ __launch_bounds__(kJoinThreads) void join_parts(const T* logits, int64_t stride, int64_t tokens, int64_t V,
+                                                           const Id* targets, Outputs to, Parts parts) {
+    __shared__ TopSpace space;
+    const int lane = threadIdx.x & 63;
+    for (int64_t r = blockIdx.x; r < tokens; r += gridDim.x) {
+        Sums a{kLowest, 0.0, 0.0};
+        if (lane % kMostParts < parts.parts) a = parts.sums[r * parts.parts + lane % kMostParts];
+        a = join_lanes<kMostParts>(a);
+        const float log_s = a.s == 0.0 ? kNegInf : log_of(a.s);
+        if (threadIdx.x == 0) put_row(to, logits + r * stride, r, V, targets, a, log_s);
+        if (to.top == 0) continue;
+        const int all = parts.parts * to.top;      // at most kFound
+        if (threadIdx.x == 0) space.count = 0;
+        __syncthreads();
+        for (int i = threadIdx.x; i < all; i += kJoinThreads) {
+            const uint64_t o = parts.found[r * all + i];
+            if (o) space.found[atomicAdd(&space.count, 1)] = o;
+        }
+        __syncthreads();
+        rank_found(space, space.count, kJoinThreads, to.top,
+                   [&](int at, uint64_t o) { put_alternative(to, r, at, o, a.m, log_s); });
         __syncthreads();
     }
 }
@@ -390,10 +455,26 @@ tide_status check(int32_t dtype, int64_t tokens, int64_t vocab, int32_t id_bytes
     return TIDE_OK;
 }
 
-// Threads of a row's workgroup.
+// Threads of a row's workgroup: as many as fill the GPU with the rows there are
+// (1024 threads with alternatives are one workgroup a CU). 257 rows of 50001 fp32
+// with 20 alternatives: 24 us with 512, 33 with 1024 (the last row alone); 700 rows:
+// 40 with 256, 42 with 512, 56 with 1024.
 int threads_of(int64_t tokens, int64_t units) {
     if (units <= 256) return 64;
-    return tokens < 1024 && units > 2048 ? 1024 : 256;
+    return units <= 2048 || tokens > 512 ? 256 : tokens > 256 ? 512 : 1024;
+}
+// Parts of a row, of 16 KiB at least, for few tokens. One row of 131072 bf16 with 8
+// alternatives: 12.3 us in 16 parts and their join, 17.2 in one workgroup; 32 rows
+// 14.4 and 18.3; 128 rows 21.6 and 21.0.
+int32_t parts_of(int64_t tokens, int64_t units) {
+    if (tokens < 1 || tokens > 64) return 1;
+    const int64_t p = units / 1024 < kMostParts ? units / 1024 : kMostParts;
+    return p < 2 ? 1 : (int32_t)p;
+}
+
+int64_t units_of(int32_t dtype, int64_t vocab) {
+    const int64_t n = dtype == TIDE_DTYPE_FP32 ? 4 : 8;
+    return (vocab + n - 1) / n;
 }
 
 template <class F>
@@ -406,16 +487,33 @@ hipError_t with_types(int32_t dtype, int32_t id_bytes, F&& go) {
 
 extern "C" {
 
+tide_status tide_token_logprobs_workspace(int32_t dtype, int64_t tokens, int64_t vocab, int32_t top,
+                                          int64_t* bytes) {
+    return guarded([&]() -> tide_status {
+        if (!bytes) return fail(TIDE_ERR_INVALID_ARG, "bytes is NULL");
+        TIDE_TRY(check(dtype, tokens, vocab, 4));
+        if (top < 0) return fail(TIDE_ERR_INVALID_ARG, "negative top");
+        if (top > kMostTop) return fail(TIDE_ERR_UNSUPPORTED, "%d alternatives: at most %d", top, kMostTop);
+        const int64_t parts = parts_of(tokens, units_of(dtype, vocab));
+        *bytes = parts > 1 ? tokens * parts * ((int64_t)sizeof(Sums) + 8 * top) : 0;
+        return TIDE_OK;
+    });
+}
+
 tide_status tide_token_logprobs(int32_t dtype, const void* logits, int64_t logits_stride,
                                 int64_t tokens, int64_t vocab, const void* targets,
                                 int32_t id_bytes, float* logprob, float* stats, float* entropy,
-                                int32_t top, int32_t* top_ids, float* top_logprobs, void* stream) {
+                                int32_t top, int32_t* top_ids, float* top_logprobs, void* workspace,
+                                int64_t workspace_bytes, void* stream) {
     return guarded([&]() -> tide_status {
         TIDE_TRY(check(dtype, tokens, vocab, id_bytes));
-        if (top < 0) return fail(TIDE_ERR_INVALID_ARG, "negative top");
-        if (top > kMostTop) return fail(TIDE_ERR_UNSUPPORTED, "%d alternatives: at most %d", top, kMostTop);
+        int64_t need = 0;
+        TIDE_TRY(tide_token_logprobs_workspace(dtype, tokens, vocab, top, &need));
+        if (need > 0 && (!workspace || workspace_bytes < need))
+            return fail(TIDE_ERR_INVALID_ARG, "workspace holds %lld bytes, %lld needed",
+                        (long long)(workspace ? workspace_bytes : 0), (long long)need);
         const int32_t size = dtype == TIDE_DTYPE_FP32 ? 4 : 2;
-        Mat rd[2], wr[5];
+        Mat rd[2], wr[6];
         TIDE_TRY(matrix("logits", logits, tokens, vocab, logits_stride, size, &rd[0]));
         TIDE_TRY(matrix("targets", targets, 1, tokens, tokens, id_bytes, &rd[1]));
         TIDE_TRY(matrix("logprob", logprob, 1, tokens, tokens, 4, &wr[0]));
@@ -423,28 +521,41 @@ tide_status tide_token_logprobs(int32_t dtype, const void* logits, int64_t logit
         TIDE_TRY(matrix("entropy", entropy, entropy ? 1 : 0, tokens, tokens, 4, &wr[2]));
         TIDE_TRY(matrix("top_ids", top_ids, tokens, top, top, 4, &wr[3]));
         TIDE_TRY(matrix("top_logprobs", top_logprobs, tokens, top, top, 4, &wr[4]));
-        TIDE_TRY(no_overlap(wr, 5, rd, 2));
+        TIDE_TRY(matrix("workspace", workspace, 1, need / 8, need / 8, 8, &wr[5]));
+        TIDE_TRY(no_overlap(wr, 6, rd, 2));
         if (tokens == 0) return TIDE_OK;
+        const Outputs to{logprob, stats, entropy, top_ids, top_logprobs, top};
+        const int64_t units = units_of(dtype, vocab);
+        Parts parts{(Sums*)workspace, nullptr, units, parts_of(tokens, units)};
+        parts.found = (uint64_t*)(parts.sums + tokens * parts.parts);
+        parts.units = (units + parts.parts - 1) / parts.parts;
         return on_stream(stream, [&](hipStream_t s) {
-            const dim3 grid((uint32_t)(tokens < (1 << 20) ? tokens : (1 << 20)));
-            const int threads = threads_of(tokens, vocab * size / 16);
+            const int threads = threads_of(tokens, units);
             return with_types(dtype, id_bytes, [&](auto type, auto id) {
                 using T = decltype(type);
                 using Id = decltype(id);
-                const auto go = [&](auto n, auto with_entropy, auto with_top) {
-                    return enqueue(row_logprobs<T, Id, n.value, with_entropy.value, with_top.value>, grid, n.value, 0, s,
-                                   (const T*)logits, logits_stride, tokens, vocab, (const Id*)targets, logprob, stats,
-                                   entropy, top, top_ids, top_logprobs);
+                const auto go = [&](auto n, auto split, auto with_entropy, auto with_top) {
+                    const dim3 grid((uint32_t)(tokens < (1 << 20) ? tokens : (1 << 20)), split.value ? parts.parts : 1);
+                    return enqueue(row_logprobs<T, Id, n.value, with_entropy.value, with_top.value, split.value>, grid,
+                                   n.value, 0, s, (const T*)logits, logits_stride, tokens, vocab, (const Id*)targets, to,
+                                   parts);
                 };
-                const auto with = [&](auto n) {
-                    using Yes = std::true_type;
-                    using No = std::false_type;
-                    if (entropy) return top ? go(n, Yes{}, Yes{}) : go(n, Yes{}, No{});
-                    return top ? go(n, No{}, Yes{}) : go(n, No{}, No{});
+                using Yes = std::true_type;
+                using No = std::false_type;
+                const auto with = [&](auto n, auto split) {
+                    if (entropy) return top ? go(n, split, Yes{}, Yes{}) : go(n, split, Yes{}, No{});
+                    return top ? go(n, split, No{}, Yes{}) : go(n, split, No{}, No{});
                 };
-                return threads == 64    ? with(std::integral_constant<int, 64>{})
-                       : threads == 256 ? with(std::integral_constant<int, 256>{})
-                                        : with(std::integral_constant<int, 1024>{});
+                if (parts.parts > 1) {
+                    const hipError_t e = with(std::integral_constant<int, 256>{}, Yes{});
+                    if (e != hipSuccess) return e;
+                    return enqueue(join_parts<T, Id>, dim3((uint32_t)tokens), kJoinThreads, 0, s, (const T*)logits,
+                                   logits_stride, tokens, vocab, (const Id*)targets, to, parts);
+                }
+                return threads == 64    ? with(std::integral_constant<int, 64>{}, No{})
+                       : threads == 256 ? with(std::integral_constant<int, 256>{}, No{})
+                       : threads == 512 ? with(std::integral_constant<int, 512>{}, No{})
+                                        : with(std::integral_constant<int, 1024>{}, No{});
             });
         });
     });

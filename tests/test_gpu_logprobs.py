@@ -126,7 +126,13 @@ def test_alternatives_that_one_lane_or_one_stretch_holds(tide, dtype):
         rows.append(x)
     x = torch.stack(rows).to(dtype)
     t = torch.arange(len(rows))
-    check(run(tide, x, t, top), step.logprobs(x, t, top), top, "stretches")
+    want = step.logprobs(x, t, top)
+    for times in (1, 7, 13, 24, 48):                     # few rows are split, more have a workgroup each, of fewer threads
+        got = run(tide, x.repeat(times, 1), t.repeat(times), top)
+        first = {k: v[: len(rows)] for k, v in got.items()}
+        check(first, want, top, "stretches")
+        for k, v in got.items():
+            assert torch.equal(v, first[k].repeat(times, *[1] * (v.dim() - 1))), k
 
 
 def test_outputs_left_out(tide):

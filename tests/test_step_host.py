@@ -95,13 +95,21 @@ def test_embed_grad_refuses(call, tide):
 
 def test_logprobs_refuse(call):
     r = table_of(call, "token_logprobs", dict(dtype=0, x=at(0), xs=100, tokens=10, vocab=100, targets=at(1), id_bytes=8, lp=at(2), st=at(3),
-                                              H=at(4), top=3, ids=at(5), tops=at(6), stream=None))
+                                              H=at(4), top=3, ids=at(5), tops=at(6), ws=None, wsn=0, stream=None))
     assert r(dtype=2) == ARG and r(id_bytes=3) == ARG and r(tokens=-1) == ARG and r(vocab=-1) == ARG and r(top=-1) == ARG
     assert r(top=33) == UNSUP and r(vocab=1 << 31) == UNSUP and r(xs=99) == ARG and r(xs=1 << 62) == OVER
     for n in ("x", "targets", "lp", "ids", "tops"):
         assert r(**{n: None}) == ARG and r(**{n: at(8) + 1}) == ALIGN, n
     assert r(st=at(8) + 2) == ALIGN and r(H=at(8) + 2) == ALIGN
     assert r(lp=at(0) + 4) == ARG and r(st=at(2)) == ARG and r(H=at(1)) == ARG and r(tops=at(5) + 4) == ARG
+    need = ctypes.c_int64()
+    assert call("token_logprobs_workspace", 0, 10, 131072, 3, need) == OK and need.value > 0
+    large = dict(vocab=131072, xs=131072, ws=at(7), wsn=need.value)
+    assert r(**{**large, "ws": None}) == ARG and r(**{**large, "wsn": need.value - 1}) == ARG and r(**{**large, "ws": at(7) + 4}) == ALIGN
+    assert r(**{**large, "ws": at(2)}) == ARG and r(**{**large, "ws": at(0)}) == ARG
+    assert call("token_logprobs_workspace", 0, 5000, 131072, 3, need) == OK and need.value == 0
+    assert call("token_logprobs_workspace", 0, -1, 5, 3, need) == ARG and call("token_logprobs_workspace", 3, 1, 5, 3, need) == ARG
+    assert call("token_logprobs_workspace", 0, 1, 5, 33, need) == UNSUP and call("token_logprobs_workspace", 0, 1, 5, 3, None) == ARG
     g = table_of(call, "token_logprobs_grad", dict(dtype=1, x=at(0), xs=100, tokens=10, vocab=100, targets=at(1), id_bytes=8, st=at(2),
                                                    d=at(3), H=at(4), h=at(5), dx=at(6), dxs=100, stream=None))
     assert g(dtype=2) == ARG and g(id_bytes=3) == ARG and g(tokens=-1) == ARG and g(H=None) == ARG and g(dxs=99) == ARG
