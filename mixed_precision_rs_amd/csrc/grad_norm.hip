@@ -7,6 +7,7 @@
 // an fp32 number is exact in it, and neither overflows nor vanishes.
 #include <algorithm>
 #include <climits>
+#include <type_traits>
 #include <vector>
 
 #include "device.hpp"
@@ -20,7 +21,6 @@ constexpr int kThreads = 256;
 constexpr int kTileBytes = 16384;
 template <class T>
 constexpr int kTileOf = kTileBytes / (int)sizeof(T);
-constexpr int kMostTensors = 128;      // in one launch's arguments
 constexpr int64_t kMostGroups = 8192;
 // Tiles that one workgroup sums alone, in one launch.
 constexpr int64_t kAlone = 8;
@@ -30,15 +30,21 @@ constexpr int64_t kAlone = 8;
 // finds there what the squares have read (53 MB: 19 us instead of 22-27).
 constexpr int64_t kPastCaches = (int64_t)192 << 20;
 
+// The tensors of one launch, in its arguments (below 4 KiB). Tensor i has the tiles
+// first[i] .. first[i + 1] - 1, the last of them with last[i] elements.
+template <bool kOut>
 struct Tensors {
-    const void* in[kMostTensors];
-    void* out[kMostTensors];
-    int64_t elems[kMostTensors];
-    int32_t first[kMostTensors];       // first tile
-    int32_t count, tiles;
+    static constexpr int kMost = kOut ? 160 : 256;
+    const void* in[kMost];
+    void* out[kOut ? kMost : 1];
+    int32_t first[kMost + 1];
+    uint16_t last[kMost];
+    int32_t count;
 };
+static_assert(sizeof(Tensors<true>) < 4000 && sizeof(Tensors<false>) < 4000, "launch arguments");
 
-__device__ __forceinline__ int tensor_of(const Tensors& a, int tile) {
+template <bool kOut>
+__device__ __forceinline__ int tensor_of(const Tensors<kOut>& a, int tile) {
     int lo = 0, hi = a.count - 1;
     while (lo < hi) {
         const int mid = (lo + hi + 1) / 2;
@@ -61,24 +67,23 @@ __device__ __forceinline__ double block_sum(double v) {
     return v;
 }
 
-// Calls f(pointer index base, elements left, tensor) for this thread's vectors of a tile.
-template <class T, class F>
-__device__ __forceinline__ void each_vector(const Tensors& a, int tile, F&& f) {
+// Calls f(tensor, element, elements left in the tile) for this thread's vectors of a tile.
+template <class T, bool kOut, class F>
+__device__ __forceinline__ void each_vector(const Tensors<kOut>& a, int tile, F&& f) {
     constexpr int N = kVecOf<T>;
     const int i = tensor_of(a, tile);
     const int64_t lo = (int64_t)(tile - a.first[i]) * kTileOf<T>;
-    const int64_t hi = a.elems[i] - lo < kTileOf<T> ? a.elems[i] : lo + kTileOf<T>;
+    const int n = tile + 1 == a.first[i + 1] ? a.last[i] : kTileOf<T>;
 #pragma unroll 4
-    for (int64_t e = lo + threadIdx.x * N; e < hi; e += kThreads * N)
-        f(i, e, hi - e < N ? (int)(hi - e) : N);
+    for (int e = threadIdx.x * N; e < n; e += kThreads * N) f(i, lo + e, n - e < N ? n - e : N);
 }
 
 // Each workgroup's sum into partial; one workgroup alone writes the total.
 template <class T, bool kOnce>
-__global__ __launch_bounds__(kThreads) void sum_squares(Tensors a, double* partial, double* total, int accumulate) {
+__global__ __launch_bounds__(kThreads) void sum_squares(Tensors<false> a, double* partial, double* total, int accumulate) {
     constexpr int N = kVecOf<T>;
     double sum = 0.0;
-    for (int tile = blockIdx.x; tile < a.tiles; tile += gridDim.x)
+    for (int tile = blockIdx.x; tile < a.first[a.count]; tile += gridDim.x)
         each_vector<T>(a, tile, [&](int i, int64_t e, int n) {
             float v[N];
             widen(load_row<kOnce>((const T*)a.in[i] + e, n), v);
@@ -101,16 +106,19 @@ __global__ __launch_bounds__(kSumThreads) void sum_partials(const double* partia
     if (threadIdx.x == 0) *gbl_mut<double>(total) = accumulate ? *gbl<double>(total) + sum : sum;
 }
 
-template <class T, bool kOnce>
-__global__ __launch_bounds__(kThreads) void clip(Tensors a, const double* total, double most, float* norm_to) {
+// Without kOut every tensor is clipped in place.
+template <class T, bool kOnce, bool kOut>
+__global__ __launch_bounds__(kThreads) void clip(Tensors<kOut> a, const double* total, double most, float* norm_to) {
     constexpr int N = kVecOf<T>;
     const double norm = sqrt(*gbl<double>(total));
     if (norm_to && blockIdx.x == 0 && threadIdx.x == 0) *gbl_mut<float>(norm_to) = (float)norm;
     const bool scaled = norm > most && norm < __builtin_inf();
+    if (!kOut && !scaled) return;
     const double factor = most / norm;
-    for (int tile = blockIdx.x; tile < a.tiles; tile += gridDim.x)
+    for (int tile = blockIdx.x; tile < a.first[a.count]; tile += gridDim.x)
         each_vector<T>(a, tile, [&](int i, int64_t e, int n) {
-            if (!scaled && a.in[i] == a.out[i]) return;
+            T* to = (T*)(kOut ? a.out[i] : a.in[i]);
+            if (!scaled && to == a.in[i]) return;
             u32x4 raw = load_row<kOnce>((const T*)a.in[i] + e, n);
             if (scaled) {
                 float v[N];
@@ -119,7 +127,7 @@ __global__ __launch_bounds__(kThreads) void clip(Tensors a, const double* total,
                 for (int c = 0; c < N; ++c) v[c] = (float)((double)v[c] * factor);
                 raw = narrow(v);
             }
-            store_row((T*)a.out[i] + e, n, raw);
+            store_row(to + e, n, raw);
         });
 }
 
@@ -143,17 +151,17 @@ bool past_caches(const int64_t* elems, int32_t tensors, int32_t size) {
     return all > kPastCaches / size;
 }
 
-// Calls go(Tensors, workgroups, workgroups before) for each launch: up to
-// kMostTensors tensors and 2^30 tiles (a larger tensor is cut).
-template <class F>
+// Calls go(Tensors, workgroups, workgroups before) for each launch: up to kMost
+// tensors and 2^30 tiles (a larger tensor is cut).
+template <bool kOut, class F>
 hipError_t each_launch(const void* const* in, void* const* out, const int64_t* elems, int32_t tensors,
                        int32_t size, F&& go) {
     const int64_t kMostTiles = (int64_t)1 << 30, tile = kTileBytes / size;
-    Tensors a{};
+    Tensors<kOut> a{};
     int64_t tiles = 0, groups = 0;
     const auto flush = [&]() -> hipError_t {
         if (a.count == 0) return hipSuccess;
-        a.tiles = (int32_t)tiles;
+        a.first[a.count] = (int32_t)tiles;
         const int64_t g = tiles < kMostGroups ? tiles : kMostGroups;
         const hipError_t e = go(a, g, groups);
         groups += g;
@@ -166,20 +174,49 @@ hipError_t each_launch(const void* const* in, void* const* out, const int64_t* e
             const int64_t left = elems[i] - at;
             const int64_t n = left < kMostTiles * tile ? left : kMostTiles * tile;
             const int64_t t = (n + tile - 1) / tile;
-            if (a.count == kMostTensors || tiles + t > kMostTiles) {
+            if (a.count == Tensors<kOut>::kMost || tiles + t > kMostTiles) {
                 const hipError_t e = flush();
                 if (e != hipSuccess) return e;
             }
             a.in[a.count] = in ? (const char*)in[i] + at * size : nullptr;
-            a.out[a.count] = out ? (char*)out[i] + at * size : (void*)a.in[a.count];
-            a.elems[a.count] = n;
+            if (kOut) a.out[a.count] = (char*)out[i] + at * size;
             a.first[a.count] = (int32_t)tiles;
+            a.last[a.count] = (uint16_t)(n - (t - 1) * tile);
             ++a.count;
             tiles += t;
             at += n;
         }
     }
     return flush();
+}
+
+// A range of addresses that is read or written.
+struct Range {
+    uintptr_t lo, hi;
+};
+void in_order(std::vector<Range>& r) {
+    const auto less = [](const Range& a, const Range& b) { return a.lo < b.lo; };
+    if (!std::is_sorted(r.begin(), r.end(), less)) std::sort(r.begin(), r.end(), less);
+}
+// INVALID_ARG where a range that is written shares a byte with another one that is
+// written, or with one that is read.
+tide_status check_ranges(std::vector<Range>& written, std::vector<Range>& read) {
+    in_order(written);
+    in_order(read);
+    const char* what = "a tensor that is written overlaps another one";
+    for (size_t i = 1; i < written.size(); ++i)
+        if (written[i].lo < written[i - 1].hi) return fail(TIDE_ERR_INVALID_ARG, "%s", what);
+    size_t w = 0;
+    uintptr_t end = 0;                             // of what is read so far
+    for (const Range& r : read) {
+        for (; w < written.size() && written[w].lo < r.lo; ++w)
+            if (written[w].lo < end) return fail(TIDE_ERR_INVALID_ARG, "%s", what);
+        if (w > 0 && written[w - 1].hi > r.lo) return fail(TIDE_ERR_INVALID_ARG, "%s", what);
+        end = std::max(end, r.hi);
+    }
+    for (; w < written.size(); ++w)
+        if (written[w].lo < end) return fail(TIDE_ERR_INVALID_ARG, "%s", what);
+    return TIDE_OK;
 }
 
 }  // namespace
@@ -192,7 +229,8 @@ tide_status tide_grad_squares_workspace(int32_t dtype, const int64_t* elems, int
         if (!bytes) return fail(TIDE_ERR_INVALID_ARG, "bytes is NULL");
         TIDE_TRY(check_sizes(dtype, elems, tensors));
         int64_t groups = 0;
-        (void)each_launch(nullptr, nullptr, elems, tensors, dtype == TIDE_DTYPE_FP32 ? 4 : 2, [&](const Tensors&, int64_t g, int64_t) {
+        (void)each_launch<false>(nullptr, nullptr, elems, tensors, dtype == TIDE_DTYPE_FP32 ? 4 : 2,
+                                 [&](const Tensors<false>&, int64_t g, int64_t) {
             groups += g;
             return hipSuccess;
         });
@@ -225,8 +263,8 @@ tide_status tide_grad_squares(int32_t dtype, const void* const* grads, const int
         return on_stream(stream, [&](hipStream_t s) {
             const bool alone = need == 0;          // no tile, or one launch of kAlone at most
             bool none = true;
-            const hipError_t e = each_launch(grads, nullptr, elems, tensors, size,
-                                             [&](const Tensors& a, int64_t groups, int64_t before) {
+            const hipError_t e = each_launch<false>(grads, nullptr, elems, tensors, size,
+                                                    [&](const Tensors<false>& a, int64_t groups, int64_t before) {
                 none = false;
                 const auto kernel = once ? (size == 2 ? sum_squares<uint16_t, true> : sum_squares<float, true>)
                                          : (size == 2 ? sum_squares<uint16_t, false> : sum_squares<float, false>);
@@ -253,46 +291,39 @@ tide_status tide_clip_grads(int32_t dtype, const void* const* grads, const int64
         TIDE_TRY(matrix("total", total, 1, 1, 1, 8, &rd[0]));
         TIDE_TRY(matrix("norm", norm, norm ? 1 : 0, 1, 1, 4, &small[0]));
         TIDE_TRY(no_overlap(small, 1, rd, 1));
-        // Every range that is read or written, in order of address: one that is
-        // written shares no byte with another, but for a tensor in place.
-        struct Range {
-            uintptr_t lo, hi;
-            bool written;
-        };
-        std::vector<Range> at;
-        at.reserve(2 * (size_t)tensors + 2);
-        at.push_back(Range{rd[0].base, rd[0].base + 8, false});
-        if (norm) at.push_back(Range{small[0].base, small[0].base + 4, true});
+        std::vector<Range> read{Range{rd[0].base, rd[0].base + 8}}, written;
+        read.reserve((size_t)tensors + 1);
+        written.reserve((size_t)tensors + 1);
+        if (norm) written.push_back(Range{small[0].base, small[0].base + 4});
+        bool elsewhere = false;
         for (int32_t i = 0; i < tensors; ++i) {
             Mat a, b;
             TIDE_TRY(matrix("one of the grads", grads[i], 1, elems[i], elems[i], size, &a));
             TIDE_TRY(matrix("one of the outputs", out ? out[i] : grads[i], 1, elems[i], elems[i], size, &b));
             if (a.rows == 0) continue;
-            if (a.base != b.base) at.push_back(Range{a.base, a.base + (uintptr_t)a.width, false});
-            at.push_back(Range{b.base, b.base + (uintptr_t)b.width, true});
+            if (a.base != b.base) {
+                read.push_back(Range{a.base, a.base + (uintptr_t)a.width});
+                elsewhere = true;
+            }
+            written.push_back(Range{b.base, b.base + (uintptr_t)b.width});
         }
-        std::sort(at.begin(), at.end(), [](const Range& a, const Range& b) { return a.lo < b.lo; });
-        uintptr_t end = 0, written_end = 0;
-        for (const Range& r : at) {
-            if (r.lo < (r.written ? end : written_end))
-                return fail(TIDE_ERR_INVALID_ARG, "a tensor that is written overlaps another one");
-            end = std::max(end, r.hi);
-            if (r.written) written_end = std::max(written_end, r.hi);
-        }
+        TIDE_TRY(check_ranges(written, read));
         const bool once = past_caches(elems, tensors, size);
         return on_stream(stream, [&](hipStream_t s) {
             bool first = true;
-            const hipError_t e = each_launch(grads, out, elems, tensors, size,
-                                             [&](const Tensors& a, int64_t groups, int64_t) {
+            const auto go = [&](const auto& a, int64_t groups, int64_t) {
+                constexpr bool kOut = std::is_same_v<std::decay_t<decltype(a)>, Tensors<true>>;
                 float* to = first ? norm : nullptr;
                 first = false;
                 const dim3 grid((uint32_t)groups);
-                const auto kernel = once ? (size == 2 ? clip<uint16_t, true> : clip<float, true>)
-                                         : (size == 2 ? clip<uint16_t, false> : clip<float, false>);
+                const auto kernel = once ? (size == 2 ? clip<uint16_t, true, kOut> : clip<float, true, kOut>)
+                                         : (size == 2 ? clip<uint16_t, false, kOut> : clip<float, false, kOut>);
                 return enqueue(kernel, grid, kThreads, 0, s, a, total, max_norm, to);
-            });
+            };
+            const hipError_t e = elsewhere ? each_launch<true>(grads, out, elems, tensors, size, go)
+                                           : each_launch<false>(grads, nullptr, elems, tensors, size, go);
             if (e != hipSuccess || !first || !norm) return e;
-            return enqueue(clip<float, false>, dim3(1), kThreads, 0, s, Tensors{}, total, max_norm, norm);
+            return enqueue(clip<float, false, false>, dim3(1), kThreads, 0, s, Tensors<false>{}, total, max_norm, norm);
         });
     });
 }

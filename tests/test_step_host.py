@@ -199,6 +199,33 @@ def test_clip_refuses(call):
         assert r(grads=same) == HIP and r(out=None) == HIP and r(out=lists(at(0), at(1) + 400000)[0]) == HIP
 
 
+def test_clip_refuses_every_shared_byte_and_nothing_else(call):
+    """Random small ranges, in place and not, against a comparison of every pair."""
+    if torch.cuda.is_available():
+        pytest.skip("the accepted calls would run on the fake addresses")
+    import random
+    rng = random.Random(1)
+    seen = {ARG: 0, HIP: 0}
+    for _ in range(3000):
+        n = rng.randint(1, 6)
+        size = [rng.randint(0, 3) for _ in range(n)]
+        spread = rng.choice([20, 60, 200])
+        src = [rng.randrange(spread) for _ in range(n)]
+        dst = [s if rng.random() < 0.4 else rng.randrange(spread) for s in src]
+        total, norm = 2 * rng.randrange(spread // 2), rng.randrange(spread)
+        reads = [(total, total + 2)] + [(a, a + k) for a, b, k in zip(src, dst, size) if a != b]
+        writes = [(norm, norm + 1)] + [(b, b + k) for b, k in zip(dst, size)]
+        meet = lambda x, y: x[0] < y[1] and y[0] < x[1] and x[0] < x[1] and y[0] < y[1]  # noqa: E731
+        bad = any(meet(w, r) for w in writes for r in reads) or any(
+            meet(writes[i], writes[j]) for i in range(len(writes)) for j in range(i))
+        place = lambda v: FAKE + 4 * v  # noqa: E731
+        got = call("clip_grads", 1, (ctypes.c_void_p * n)(*map(place, src)), (ctypes.c_int64 * n)(*size), n, place(total), 1.0,
+                   (ctypes.c_void_p * n)(*map(place, dst)), place(norm), None)
+        assert got == (ARG if bad else HIP), (src, dst, size, total, norm)
+        seen[got] += 1
+    assert min(seen.values()) > 300, seen
+
+
 def test_windows_of_fused_rows_do_not_overlap(call):
     """dq, dk as windows of one gradient of the fused projection pass the check."""
     if torch.cuda.is_available():
