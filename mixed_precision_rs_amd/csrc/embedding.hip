@@ -386,27 +386,44 @@ __global__ __launch_bounds__(kRowThreads) void embed_rows(const Id* ids, int64_t
 
 // ---- The table's gradient --------------------------------------------------------
 //
-// A row of the table with up to `chunk` tokens is summed by its own lanes. One with
-// more (the words that a text is full of) would keep them busy long after the
-// others: its tokens are summed chunk by chunk, at multiples of `chunk` places of
-// the order, by the waves of a kernel before, and its lanes add up those sums.
-// A chunk of places can hold pieces of two such rows: one that it begins inside
-// (or with), and one that begins in it and goes on behind it. row_of says whose
-// pieces they are, -1 where there is none.
+// First the tokens: the places of the order are cut into chunks, and a wave adds up
+// the tokens of a chunk one behind the other, in 64 vectors of columns. Where a row
+// of the table ends it goes out, unless it began before the chunk or goes on behind
+// it: those sums (of a frequent word, many) are left in the workspace. Then the
+// table: rows without tokens become zeros, rows whose sums were left are joined.
+// A kernel that reads and then one that writes: with the tokens added up among the
+// waves that clear (most of a large table) 16384 tokens in 131072 x 2048 took 126 us,
+// mixed through the whole of it 156-195, and so 30 and 78, the rate of a fill.
+//
+// Offsets that do not come from a sort may leave rows that no chunk finds whole:
+// owner says for each place whether the row that begins there was written, row_of
+// whose sums a chunk has left, and a row that neither names is added up by its own
+// lanes.
 struct Sorted {
     const int32_t* offsets;
     const int32_t* order;
     int64_t tokens, vocab;
 };
-struct Pieces {
-    float* sums;           // [chunk of places][2][padded]
-    int32_t* row_of;       // [chunk of places][2]
+struct Chunks {
+    float* sums;           // [chunk][2][padded]: of a row that begins before (or with) the chunk, of one behind
+    int32_t* row_of;       // [chunk][2]; -1: none
+    int32_t* owner;        // [place]; -1: none
     int64_t padded;        // elements of a sum
-    int32_t chunk;
+    int32_t size;          // places of a chunk; 0: no chunks
 };
-// Chunks: the row of the most tokens then has at most 256 sums up to 16384
-// tokens and 1024 up to 131072.
-int64_t chunk_of(int64_t tokens) { return tokens <= 16384 ? 64 : tokens <= 131072 ? 128 : 512; }
+template <class T>
+struct Grad {
+    T* data;
+    int64_t stride, width;
+    float scale;
+    int32_t accumulate;
+};
+// Places of a chunk. Many small ones keep the GPU busy: 16384 tokens of 2048 bf16
+// take 28 us with 16, 30 with 32, 40 with 64; 2000 of 1000 fp32, added, 18, 29 and 51;
+// but a row that has all the tokens then has as many sums to join: 512 in 97 us by
+// one wave, so that join_left does that where there may be more.
+int32_t chunk_of(int64_t tokens) { return tokens <= 4096 ? 16 : tokens <= 16384 ? 32 : tokens <= 1 << 20 ? 64 : 256; }
+constexpr int64_t kJoinTokens = 16384;
 int64_t chunks_of(int64_t tokens) {
     const int64_t c = chunk_of(tokens);
     return tokens <= c ? 0 : (tokens + c - 1) / c;
@@ -420,91 +437,172 @@ __device__ __forceinline__ void row_range(const Sorted& s, int64_t v, int64_t& l
     hi = hi > s.tokens ? s.tokens : hi;
 }
 
-// acc += the vectors at column `at` of the tokens order[lo .. hi), in order, KU
-// loads in flight. With kWave all lanes of the wave have the same lo and hi (some
-// may have no column: some <= 0): 64 entries of the order come by one load, a lane
-// each, so that no load of a token waits for another one.
-template <class T, int V, bool kWave, int KU>
-__device__ __forceinline__ void add_tokens(const Sorted& s, const T* dout, int64_t stride, int64_t lo, int64_t hi,
-                                           int64_t at, int some, float (&acc)[V]) {
-    constexpr int kRun = kWave ? 64 : KU;
-    for (int64_t i0 = lo; i0 < hi; i0 += kRun) {
-        const int n = hi - i0 < kRun ? (int)(hi - i0) : kRun;
-        uint32_t mine = ~0u;
-        if (kWave && (int)(threadIdx.x & 63) < n) mine = *gbl<uint32_t>(s.order + i0 + (threadIdx.x & 63));
+// First column of vector u: the last vector ends at the row's end (where the row
+// has one at all).
+template <int V>
+__device__ __forceinline__ int64_t column(int64_t u, int64_t width) {
+    return u > 0 && u * V > width - V ? width - V : u * V;
+}
+
+// Vector u of row v of the gradient from its sum; old is what the row holds there
+// (when it is added to).
+template <class T>
+__device__ __forceinline__ void put_vector(const Grad<T>& g, int64_t v, int64_t u, const float (&sum)[kVecOf<T>],
+                                           u32x4 old) {
+    constexpr int V = kVecOf<T>;
+    if (u * V >= g.width) return;
+    const int64_t at = column<V>(u, g.width);
+    const int some = g.width < V ? (int)g.width : V, seen = (int)(u * V - at);
+    T* to = g.data + v * g.stride + at;
+    float r[V];
+#pragma unroll
+    for (int c = 0; c < V; ++c) r[c] = sum[c] * g.scale;
+    if (!g.accumulate) {
+        store_row(to, some, narrow(r));
+        return;
+    }
+    float before[V];
+    widen(old, before);
+#pragma unroll
+    for (int c = 0; c < V; ++c) r[c] += before[c];
+    const u32x4 out = narrow(r);
+    if (seen == 0) {
+        store_row(to, some, out);
+        return;
+    }
+    // The first `seen` elements are those of the vector before, which adds to them.
+#pragma unroll
+    for (int c = 1; c < V; ++c) {
+        if (c < seen) continue;
+        if constexpr (sizeof(T) == 2) *gbl_mut<uint16_t>(to + c) = (uint16_t)(out[c / 2] >> (16 * (c & 1)));
+        else *gbl_mut<uint32_t>(to + c) = out[c];
+    }
+}
+template <class T>
+__device__ __forceinline__ u32x4 old_vector(const Grad<T>& g, int64_t v, int64_t u) {
+    constexpr int V = kVecOf<T>;
+    if (!g.accumulate || u * V >= g.width) return u32x4{};
+    return load_row(g.data + v * g.stride + column<V>(u, g.width), g.width < V ? (int)g.width : V);
+}
+
+// The rows that two places of the order belong to, by all 64 lanes: the last one
+// whose first place is not behind. Both are looked for at once.
+__device__ __forceinline__ void rows_at(const Sorted& s, int64_t p0, int64_t p1, int64_t& r0, int64_t& r1) {
+    int64_t end0 = s.vocab, end1 = s.vocab;
+    const int64_t lane = (threadIdx.x & 63) + 1;
+    r0 = r1 = 0;
+    while (end0 - r0 > 1 || end1 - r1 > 1) {
+        const int64_t step0 = (end0 - r0 + 63) / 64, step1 = (end1 - r1 + 63) / 64;
+        const int64_t i0 = r0 + lane * step0, i1 = r1 + lane * step1;
+        const int32_t o0 = *gbl<int32_t>(s.offsets + (i0 < end0 ? i0 : r0)), o1 = *gbl<int32_t>(s.offsets + (i1 < end1 ? i1 : r1));
+        r0 += __popcll(__ballot(i0 < end0 && o0 <= p0)) * step0;
+        r1 += __popcll(__ballot(i1 < end1 && o1 <= p1)) * step1;
+        end0 = r0 + step0 < end0 ? r0 + step0 : end0;
+        end1 = r1 + step1 < end1 ? r1 + step1 : end1;
+    }
+}
+
+template <class T, bool kAdd>
+__global__ __launch_bounds__(kRowThreads) void sum_chunks(Sorted s, Chunks to, const T* dout, int64_t stride,
+                                                          Grad<T> grad, int64_t waves, int tiles) {
+    constexpr int V = kVecOf<T>, KU = kAdd ? 8 : 16;
+    const int lane = threadIdx.x & 63;
+    const int64_t w = (int64_t)blockIdx.x * (kRowThreads / 64) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    if (w >= waves) return;
+    const int64_t b = w / tiles, u = (w - b * tiles) * 64 + lane;
+    const bool scribe = w == b * tiles;            // the wave that keeps the books of this chunk
+    const int64_t first = b * to.size, end = first + to.size < s.tokens ? first + to.size : s.tokens;
+    const int64_t at = column<V>(u, grad.width);
+    const int some = u * V >= grad.width ? 0 : grad.width < V ? (int)grad.width : V;
+    int32_t left[2] = {-1, -1};
+    // The row in hand: its places, those taken so far, and their sum.
+    int32_t v = -1;
+    int64_t lo = 0, hi = 0, from = 0;
+    float acc[V];
+    const auto finish = [&](int64_t place, u32x4 old) {
+        if (v < 0) return;
+        const int64_t begin = lo > first ? lo : first, stop = hi < end ? hi : end;
+        const bool whole = from == begin && place == stop, inside = lo >= first && hi <= end;
+        if (scribe && lane == 0 && from == lo) *gbl_mut<int32_t>(to.owner + lo) = whole && inside ? v : -1;
+        if (!whole) return;
+        if (inside) {
+            put_vector<T>(grad, v, u, acc, old);
+            return;
+        }
+        const int k = lo <= first ? 0 : 1;
+        left[0] = k ? left[0] : v;
+        left[1] = k ? v : left[1];
+        if (some == 0) return;
+        float* sum = to.sums + (2 * b + k) * to.padded + u * V;
+#pragma unroll
+        for (int i = 0; i < V / 4; ++i)
+            *gbl_mut<u32x4>(sum + 4 * i) = u32x4{__float_as_uint(acc[4 * i]), __float_as_uint(acc[4 * i + 1]),
+                                                 __float_as_uint(acc[4 * i + 2]), __float_as_uint(acc[4 * i + 3])};
+    };
+    u32x4 old_of_last{};
+    for (int64_t base = first; base < end; base += 64) {
+        const int n = end - base < 64 ? (int)(end - base) : 64;
+        // Lane i: the row of place base + i, its places, and the token there.
+        const int64_t place = base + (lane < n ? lane : n - 1);
+        const uint32_t token = *gbl<uint32_t>(s.order + place);
+        int64_t r0, r1;
+        rows_at(s, base, base + n - 1, r0, r1);
+        while (r0 < r1) {
+            const int64_t mid = r0 + (r1 - r0 + 1) / 2;
+            if (*gbl<int32_t>(s.offsets + mid) <= place) r0 = mid;
+            else r1 = mid - 1;
+        }
+        int64_t own_lo, own_hi;
+        row_range(s, r0, own_lo, own_hi);
+        const int32_t row = own_lo <= place && place < own_hi ? (int32_t)r0 : -1;
+        const int32_t row_lo = (int32_t)own_lo, row_hi = (int32_t)own_hi;
+        if (scribe && lane < n && (row < 0 || row_lo != place)) *gbl_mut<int32_t>(to.owner + place) = -1;
         for (int i = 0; i < n; i += KU) {
-            u32x4 raw[KU];
+            u32x4 raw[KU], old[kAdd ? KU : 1] = {};
 #pragma unroll
             for (int j = 0; j < KU; ++j) {
-                uint32_t t = ~0u;
-                if (kWave) t = __builtin_amdgcn_readlane(mine, (i + j) & 63);
-                else if (i + j < n) t = *gbl<uint32_t>(s.order + i0 + i + j);
+                const int l = (i + j) & 63;
+                const uint32_t t = __builtin_amdgcn_readlane(token, l);
                 raw[j] = u32x4{};
-                if (i + j < n && t < s.tokens && some > 0) raw[j] = load_row<true>(dout + (int64_t)t * stride + at, some);
+                if (i + j < n && t < s.tokens && some) raw[j] = load_row<true>(dout + (int64_t)t * stride + at, some);
+                if constexpr (kAdd) {
+                    const int32_t r = __builtin_amdgcn_readlane(row, l);
+                    if (i + j < n && r >= 0 && __builtin_amdgcn_readlane(row_hi, l) == base + i + j + 1)
+                        old[j] = old_vector<T>(grad, r, u);
+                }
             }
 #pragma unroll
             for (int j = 0; j < KU; ++j) {
-                float d[V];
-                widen(raw[j], d);
+                if (i + j < n) {
+                    const int l = (i + j) & 63;
+                    const int32_t r = __builtin_amdgcn_readlane(row, l);
+                    if (r != v) {
+                        finish(base + i + j, old_of_last);
+                        v = r;
+                        lo = __builtin_amdgcn_readlane(row_lo, l);
+                        hi = __builtin_amdgcn_readlane(row_hi, l);
+                        from = base + i + j;
 #pragma unroll
-                for (int c = 0; c < V; ++c) acc[c] += d[c];
+                        for (int c = 0; c < V; ++c) acc[c] = 0.0f;
+                    }
+                    float d[V];
+                    widen(raw[j], d);
+#pragma unroll
+                    for (int c = 0; c < V; ++c) acc[c] += d[c];
+                    if (kAdd) old_of_last = old[kAdd ? j : 0];
+                }
             }
         }
     }
+    finish(end, old_of_last);
+    if (scribe && lane < 2) *gbl_mut<int32_t>(to.row_of + 2 * b + lane) = lane ? left[1] : left[0];
 }
 
-// The row that place p of the order belongs to, by all 64 lanes: the last one
-// whose first place is not behind p.
-__device__ __forceinline__ int64_t row_at(const Sorted& s, int64_t p) {
-    int64_t lo = 0, hi = s.vocab;
-    while (hi - lo > 1) {
-        const int64_t step = (hi - lo + 63) / 64, i = lo + ((threadIdx.x & 63) + 1) * step;
-        const uint64_t before = __ballot(i < hi && *gbl<int32_t>(s.offsets + (i < hi ? i : lo)) <= p);
-        lo += __popcll(before) * step;
-        hi = lo + step < hi ? lo + step : hi;
-    }
-    return lo;
-}
-
-// A wave sums one of a chunk's two pieces in 64 vectors of columns.
-template <class T>
-__global__ __launch_bounds__(kRowThreads) void sum_pieces(Sorted s, Pieces to, const T* dout, int64_t stride,
-                                                          int64_t width, int64_t waves, int tiles) {
-    constexpr int V = kVecOf<T>;
-    const int64_t w = (int64_t)blockIdx.x * (kRowThreads / 64) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    if (w >= waves) return;
-    const int64_t piece = w / tiles, u = (w - piece * tiles) * 64 + (threadIdx.x & 63);
-    const int64_t first = (piece >> 1) * to.chunk, end = first + to.chunk < s.tokens ? first + to.chunk : s.tokens;
-    const int64_t place = piece & 1 ? end - 1 : first;
-    const int64_t v = row_at(s, place);
-    int64_t lo, hi;
-    row_range(s, v, lo, hi);
-    const bool mine = hi - lo > to.chunk && lo <= place && place < hi && (!(piece & 1) || lo > first);
-    if (u == 0) *gbl_mut<int32_t>(to.row_of + piece) = mine ? (int32_t)v : -1;
-    if (!mine) return;
-    const int64_t at = u > 0 && u * V > width - V ? width - V : u * V;
-    float acc[V] = {};
-    add_tokens<T, V, true, 16>(s, dout, stride, lo > first ? lo : first, hi < end ? hi : end, at,
-                           u * V >= width ? 0 : width < V ? (int)width : V, acc);
-    if (u * V >= width) return;
-    float* sum = to.sums + piece * to.padded + u * V;
-#pragma unroll
-    for (int i = 0; i < V / 4; ++i)
-        *gbl_mut<u32x4>(sum + 4 * i) = u32x4{__float_as_uint(acc[4 * i]), __float_as_uint(acc[4 * i + 1]),
-                                             __float_as_uint(acc[4 * i + 2]), __float_as_uint(acc[4 * i + 3])};
-}
-
-// acc += row v's pieces; false where they are not all there (offsets that do not
-// rise).
+// sum += the sums that the chunks b0 .. b1 have left of the row that begins at lo.
 template <int V>
-__device__ __forceinline__ bool add_pieces(const Pieces& from, int64_t v, int64_t lo, int64_t hi, int64_t u,
-                                           float (&acc)[V]) {
+__device__ __forceinline__ void add_sums(const Chunks& from, int64_t lo, int64_t b0, int64_t b1, int64_t u,
+                                         float (&sum)[V]) {
     constexpr int KU = 4;
-    const int64_t b0 = lo / from.chunk, b1 = (hi - 1) / from.chunk;
-    bool there = true;
-    for (int64_t b = b0; b <= b1; ++b)
-        there = there && *gbl<int32_t>(from.row_of + 2 * b + (lo <= b * from.chunk ? 0 : 1)) == v;
-    if (!there) return false;
     for (int64_t b = b0; b <= b1; b += KU) {
         u32x4 raw[KU][V / 4];
 #pragma unroll
@@ -513,99 +611,113 @@ __device__ __forceinline__ bool add_pieces(const Pieces& from, int64_t v, int64_
             for (int i = 0; i < V / 4; ++i) {
                 raw[j][i] = u32x4{};
                 if (b + j <= b1)
-                    raw[j][i] = *gbl<u32x4>(from.sums + (2 * (b + j) + (lo <= (b + j) * from.chunk ? 0 : 1)) * from.padded +
+                    raw[j][i] = *gbl<u32x4>(from.sums + (2 * (b + j) + (lo <= (b + j) * from.size ? 0 : 1)) * from.padded +
                                             u * V + 4 * i);
             }
 #pragma unroll
         for (int j = 0; j < KU; ++j)
 #pragma unroll
-            for (int c = 0; c < V; ++c) acc[c] += __uint_as_float(raw[j][c / 4][c % 4]);
+            for (int c = 0; c < V; ++c) sum[c] += __uint_as_float(raw[j][c / 4][c % 4]);
     }
+}
+// The sums of row v; false where they are not all there.
+template <int V>
+__device__ __forceinline__ bool add_left(const Chunks& from, int64_t v, int64_t lo, int64_t hi, int64_t u,
+                                         float (&sum)[V]) {
+    const int64_t b0 = lo / from.size, b1 = (hi - 1) / from.size;
+    int missing = 0;
+#pragma unroll 8
+    for (int64_t b = b0; b <= b1; ++b)
+        missing |= *gbl<int32_t>(from.row_of + 2 * b + (lo <= b * from.size ? 0 : 1)) ^ (int32_t)v;
+    if (missing) return false;
+    add_sums<V>(from, lo, b0, b1, u, sum);
     return true;
 }
 
-// Vector u of row v of the gradient (of a wave's or a group of lanes' 64 or fewer;
-// some <= 0: this lane has none).
-template <class T, bool kWave>
-__device__ __forceinline__ void grad_vector(const Sorted& s, const Pieces& from, const T* dout, int64_t stride,
-                                            int64_t width, float scale, T* row, int accumulate, int64_t v,
-                                            int64_t lo, int64_t hi, int64_t u, int64_t units) {
+// Rows of 16 chunks or more that begin in a chunk, by a workgroup for 64 vectors
+// each: its waves add up a run of the sums each, and the first wave the runs, in
+// order.
+constexpr int kJoinWaves = 16;
+template <class T>
+__global__ __launch_bounds__(64 * kJoinWaves) void join_left(Sorted s, Chunks from, Grad<T> grad, int64_t tiles) {
     constexpr int V = kVecOf<T>;
-    // The last vector ends at the row's end; `seen` of its elements are the one's before.
-    const int64_t at = u > 0 && u * V > width - V ? width - V : u * V;
-    const int some = u >= units ? 0 : width < V ? (int)width : V, seen = (int)(u * V - at);
-    float acc[V] = {};
-    if (lo < hi) {
-        const bool done = hi - lo > from.chunk && add_pieces<V>(from, v, lo, hi, u < units ? u : 0, acc);
-        if (!done) add_tokens<T, V, kWave, 8>(s, dout, stride, lo, hi, at, some, acc);
+    __shared__ float runs[kJoinWaves][V][64];
+    __shared__ int gone;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t b = blockIdx.x / tiles, tile = blockIdx.x - b * tiles, u = tile * 64 + lane;
+    int64_t v = *gbl<int32_t>(from.row_of + 2 * b + 1), lo = 0, hi = 0;
+    if (v < 0) v = *gbl<int32_t>(from.row_of + 2 * b);
+    if (v < 0) return;
+    row_range(s, v, lo, hi);
+    const int64_t last = (hi - 1) / from.size, all = last - b + 1, per = (all + kJoinWaves - 1) / kJoinWaves;
+    if (lo / from.size != b || all < kJoinWaves) return;
+    if (threadIdx.x == 0) gone = 0;
+    __syncthreads();
+    for (int64_t i = threadIdx.x; i < all; i += 64 * kJoinWaves)
+        if (*gbl<int32_t>(from.row_of + 2 * (b + i) + (lo <= (b + i) * from.size ? 0 : 1)) != v) gone = 1;
+    __syncthreads();
+    if (gone) return;
+    float sum[V] = {};
+    const int64_t b0 = b + wave * per, b1 = b0 + per - 1 < last ? b0 + per - 1 : last;
+    if (b0 <= b1) add_sums<V>(from, lo, b0, b1, u * V < grad.width ? u : 0, sum);
 #pragma unroll
-        for (int c = 0; c < V; ++c) acc[c] *= scale;
-    }
-    if (some <= 0) return;
-    if (!accumulate) {
-        store_row(row + at, some, narrow(acc));
+    for (int c = 0; c < V; ++c) runs[wave][c][lane] = sum[c];
+    __syncthreads();
+    if (wave) return;
+#pragma unroll
+    for (int c = 0; c < V; ++c) sum[c] = 0.0f;
+#pragma unroll 1
+    for (int w = 0; w < kJoinWaves; ++w)
+#pragma unroll
+        for (int c = 0; c < V; ++c) sum[c] += runs[w][c][lane];
+    put_vector<T>(grad, v, u, sum, old_vector<T>(grad, v, u));
+    if (tile == 0 && lane == 0) *gbl_mut<int32_t>(from.owner + lo) = (int32_t)v;
+}
+
+// Vector u of row v, unless it has been written.
+template <class T>
+__device__ __forceinline__ void finish_vector(const Sorted& s, const Chunks& from, const T* dout, int64_t stride,
+                                              const Grad<T>& grad, int64_t v, int64_t u) {
+    constexpr int V = kVecOf<T>;
+    int64_t lo, hi;
+    row_range(s, v, lo, hi);
+    const int some = u * V >= grad.width ? 0 : grad.width < V ? (int)grad.width : V;
+    const int64_t at = column<V>(u, grad.width);
+    if (lo >= hi) {
+        if (!grad.accumulate && some) store_row(grad.data + v * grad.stride + at, some, u32x4{});
         return;
     }
-    float old[V];
-    widen(load_row(row + at, some), old);
+    float sum[V] = {};
+    bool done = false;
+    if (from.size) {
+        if (*gbl<int32_t>(from.owner + lo) == v) return;
+        if (lo / from.size != (hi - 1) / from.size) done = add_left<V>(from, v, lo, hi, some ? u : 0, sum);
+    }
+    if (!done) {
+        for (int64_t i = lo; i < hi; ++i) {
+            const uint32_t t = *gbl<uint32_t>(s.order + i);
+            if (t >= s.tokens || !some) continue;
+            float d[V];
+            widen(load_row(dout + (int64_t)t * stride + at, some), d);
 #pragma unroll
-    for (int c = 0; c < V; ++c) acc[c] += old[c];
-    const u32x4 out = narrow(acc);
-    if (seen == 0) {
-        store_row(row + at, some, out);
-    } else {
-#pragma unroll
-        for (int c = 1; c < V; ++c) {
-            if (c < seen) continue;
-            if constexpr (sizeof(T) == 2) *gbl_mut<uint16_t>(row + at + c) = (uint16_t)(out[c / 2] >> (16 * (c & 1)));
-            else *gbl_mut<uint32_t>(row + at + c) = out[c];
+            for (int c = 0; c < V; ++c) sum[c] += d[c];
         }
     }
+    put_vector<T>(grad, v, u, sum, old_vector<T>(grad, v, u));
 }
 
-// Narrow rows: 2^lane_log2 lanes each.
-template <class T>
-__global__ __launch_bounds__(kRowThreads) void table_grad_narrow(Sorted s, Pieces from, const T* dout, int64_t stride,
-                                                                 int64_t width, float scale, T* grad,
-                                                                 int64_t grad_stride, int accumulate, int lane_log2) {
-    constexpr int V = kVecOf<T>;
-    const int64_t units = (width + V - 1) / V, per = kRowThreads >> lane_log2;
-    const int lane = threadIdx.x & ((1 << lane_log2) - 1);
-    for (int64_t v = (int64_t)blockIdx.x * per + (threadIdx.x >> lane_log2); v < s.vocab; v += (int64_t)gridDim.x * per) {
-        int64_t lo, hi;
-        row_range(s, v, lo, hi);
-        if (lane >= units || (accumulate && lo >= hi)) continue;
-        grad_vector<T, false>(s, from, dout, stride, width, scale, grad + v * grad_stride, accumulate, v, lo, hi, lane, units);
-    }
-}
-
-// Wide rows: a wave takes 64 vectors of one row, then those some waves further on.
-// Most rows of a large table have no token and are stores alone (131072 x 2048 in
-// 85 us, the rate of a fill); those that have wait for their loads, and stand
-// together where the frequent words do. Left so they are done in 28 us before the
-// others (16384 tokens: 113 us); with rows of distant stretches of the table taken
-// in turn, loads and stores mix, and the whole takes 142-181. 2048 workgroups that
-// stay take 145, and several rows a wave one behind the other 197 (4) to 472 (16):
-// rows that are used much then wait for each other.
+// Wide rows: a wave takes 64 vectors of one row of the table, then those some waves
+// further on. 32768 workgroups: 2048 that stay clear 131072 x 2048 in 108 us, these
+// in 85, the rate of a fill.
 constexpr int64_t kGradGroups = 32768;
 template <class T>
-__global__ __launch_bounds__(kRowThreads) void table_grad(Sorted s, Pieces from, const T* dout, int64_t stride,
-                                                          int64_t width, float scale, T* grad, int64_t grad_stride,
-                                                          int accumulate, int64_t tiles, int64_t step_rows,
-                                                          int64_t step_tiles) {
-    constexpr int V = kVecOf<T>;
-    const int64_t units = (width + V - 1) / V;
+__global__ __launch_bounds__(kRowThreads) void finish_table(Sorted s, Chunks from, const T* dout, int64_t stride,
+                                                            Grad<T> grad, int64_t tiles, int64_t step_rows,
+                                                            int64_t step_tiles) {
     const int64_t w = (int64_t)blockIdx.x * (kRowThreads / 64) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     int64_t v = w / tiles, tile = w - v * tiles;
     while (v < s.vocab) {
-        const int64_t u = tile * 64 + (threadIdx.x & 63);
-        T* row = grad + v * grad_stride;
-        int64_t lo, hi;
-        row_range(s, v, lo, hi);
-        if (lo < hi)
-            grad_vector<T, true>(s, from, dout, stride, width, scale, row, accumulate, v, lo, hi, u, units);
-        else if (!accumulate && u < units)
-            store_row(row + (u > 0 && u * V > width - V ? width - V : u * V), width < V ? (int)width : V, u32x4{});
+        finish_vector<T>(s, from, dout, stride, grad, v, tile * 64 + (threadIdx.x & 63));
         v += step_rows;
         tile += step_tiles;
         if (tile >= tiles) {
@@ -613,6 +725,34 @@ __global__ __launch_bounds__(kRowThreads) void table_grad(Sorted s, Pieces from,
             ++v;
         }
     }
+}
+
+// A gradient that is added to: only rows that no chunk has written whole. A wave
+// looks for them 64 at once, in rows far from each other, since those of frequent
+// words stand together, and then takes 64 vectors of each.
+template <class T>
+__global__ __launch_bounds__(kRowThreads) void finish_added(Sorted s, Chunks from, const T* dout, int64_t stride,
+                                                            Grad<T> grad, int64_t parts, int64_t tiles) {
+    const int lane = threadIdx.x & 63;
+    for (int64_t w = (int64_t)blockIdx.x * (kRowThreads / 64) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); w < parts * tiles;
+         w += (int64_t)gridDim.x * (kRowThreads / 64)) {
+        const int64_t part = w / tiles, tile = w - part * tiles, v = lane * parts + part;
+        int64_t lo = 0, hi = 0;
+        if (v < s.vocab) row_range(s, v, lo, hi);
+        bool open = lo < hi;
+        if (open && from.size) open = *gbl<int32_t>(from.owner + lo) != v;
+        for (uint64_t left = __ballot(open); left; left &= left - 1)
+            finish_vector<T>(s, from, dout, stride, grad, __builtin_ctzll(left) * parts + part, tile * 64 + lane);
+    }
+}
+
+// Narrow rows: 2^lane_log2 lanes each.
+template <class T>
+__global__ __launch_bounds__(kRowThreads) void finish_narrow(Sorted s, Chunks from, const T* dout, int64_t stride,
+                                                             Grad<T> grad, int lane_log2) {
+    const int64_t per = kRowThreads >> lane_log2;
+    for (int64_t v = (int64_t)blockIdx.x * per + (threadIdx.x >> lane_log2); v < s.vocab; v += (int64_t)gridDim.x * per)
+        finish_vector<T>(s, from, dout, stride, grad, v, threadIdx.x & ((1 << lane_log2) - 1));
 }
 
 tide_status check_ids(int32_t id_bytes, int64_t tokens, int64_t vocab) {
@@ -702,11 +842,10 @@ tide_status tide_embed_tokens_grad_workspace(int64_t tokens, int64_t width, int6
         if (!bytes) return fail(TIDE_ERR_INVALID_ARG, "bytes is NULL");
         TIDE_TRY(check_sorted(tokens, 0));
         if (width < 0) return fail(TIDE_ERR_INVALID_ARG, "negative width");
-        int64_t each;
-        const int64_t n = chunks_of(tokens);
+        const int64_t n = width ? chunks_of(tokens) : 0;
         *bytes = 0;
-        if (n && width && (__builtin_mul_overflow(n * 2, (width + 7) / 8 * 32, &each) ||
-                           __builtin_add_overflow(each, n * 8, bytes)))
+        if (n && (__builtin_mul_overflow(n * 8, padded_width(width) + 1, bytes) ||
+                  __builtin_add_overflow(*bytes, tokens * 4, bytes)))
             return fail(TIDE_ERR_OVERFLOW, "the workspace's size overflows int64");
         return TIDE_OK;
     });
@@ -737,28 +876,40 @@ tide_status tide_embed_tokens_grad(int32_t dtype, const void* dout, int64_t dout
         TIDE_TRY(no_overlap(wr, 2, rd, 3));
         if (vocab == 0 || width == 0) return TIDE_OK;
         return on_stream(stream, [&](hipStream_t s) {
-            const int64_t units = (width * size + 15) / 16, padded = padded_width(width), n = need ? chunks_of(tokens) : 0;
+            const int64_t units = (width * size + 15) / 16, tiles = (units + 63) / 64;
+            const int64_t padded = padded_width(width), n = need ? chunks_of(tokens) : 0;
             const Sorted sorted{offsets, order, tokens, vocab};
-            const Pieces pieces{(float*)workspace, (int32_t*)((float*)workspace + 2 * n * padded), padded,
-                                (int32_t)chunk_of(tokens)};
-            const RowGrid g = row_grid(vocab, units < 64 ? units : 64);
+            Chunks chunks{(float*)workspace, nullptr, nullptr, padded, n ? chunk_of(tokens) : 0};
+            chunks.row_of = (int32_t*)(chunks.sums + 2 * n * padded);
+            chunks.owner = chunks.row_of + 2 * n;
             const auto go = [&](auto type) {
                 using T = decltype(type);
+                const Grad<T> to{(T*)grad, grad_stride, width, scale, accumulate ? 1 : 0};
                 if (n) {
-                    const int64_t tiles = (units + 63) / 64, waves = 2 * n * tiles;
-                    const hipError_t e = enqueue(sum_pieces<T>, dim3((uint32_t)((waves + 3) / 4)), kRowThreads, 0, s,
-                                                 sorted, pieces, (const T*)dout, dout_stride, width, waves, (int)tiles);
+                    const int64_t waves = n * tiles;
+                    const auto kernel = accumulate ? sum_chunks<T, true> : sum_chunks<T, false>;
+                    const hipError_t e = enqueue(kernel, dim3((uint32_t)((waves + 3) / 4)), kRowThreads, 0, s, sorted,
+                                                 chunks, (const T*)dout, dout_stride, to, waves, (int)tiles);
                     if (e != hipSuccess) return e;
                 }
-                if (units <= 32)
-                    return enqueue(table_grad_narrow<T>, dim3(g.grid.x), kRowThreads, 0, s, sorted, pieces,
-                                   (const T*)dout, dout_stride, width, scale, (T*)grad, grad_stride, accumulate ? 1 : 0,
-                                   g.lane_log2);
-                const int64_t tiles = (units + 63) / 64, all = (vocab * tiles + 3) / 4;
-                const int64_t groups = all < kGradGroups ? all : kGradGroups, waves = 4 * groups;
-                return enqueue(table_grad<T>, dim3((uint32_t)groups), kRowThreads, 0, s, sorted, pieces, (const T*)dout,
-                               dout_stride, width, scale, (T*)grad, grad_stride, accumulate ? 1 : 0, tiles,
-                               waves / tiles, waves % tiles);
+                if (n && tokens > kJoinTokens) {
+                    const hipError_t e = enqueue(join_left<T>, dim3((uint32_t)(n * tiles)), 64 * kJoinWaves, 0, s, sorted,
+                                                 chunks, to, tiles);
+                    if (e != hipSuccess) return e;
+                }
+                if (accumulate) {
+                    const int64_t parts = (vocab + 63) / 64, groups = (parts * tiles + 3) / 4;
+                    return enqueue(finish_added<T>, dim3((uint32_t)(groups < kGradGroups ? groups : kGradGroups)),
+                                   kRowThreads, 0, s, sorted, chunks, (const T*)dout, dout_stride, to, parts, tiles);
+                }
+                if (units <= 32) {
+                    const RowGrid g = row_grid(vocab, units);
+                    return enqueue(finish_narrow<T>, dim3(g.grid.x), kRowThreads, 0, s, sorted, chunks, (const T*)dout,
+                                   dout_stride, to, g.lane_log2);
+                }
+                const int64_t all = (vocab * tiles + 3) / 4, groups = all < kGradGroups ? all : kGradGroups;
+                return enqueue(finish_table<T>, dim3((uint32_t)groups), kRowThreads, 0, s, sorted, chunks,
+                               (const T*)dout, dout_stride, to, tiles, 4 * groups / tiles, 4 * groups % tiles);
             };
             return size == 2 ? go(uint16_t{}) : go(float{});
         });

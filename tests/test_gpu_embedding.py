@@ -139,12 +139,13 @@ def test_table_gradient(tide, T, V, D, kind, pad, dtype):
             assert (w[:, : pad // 2] == 3.0).all() and (w[:, pad // 2 + D:] == 3.0).all()
 
 
-@pytest.mark.parametrize("T,V,kind", [(300, 7, "words"), (5000, 40, "words"), (9001, 3, "even"), (40000, 2, "one")])
+@pytest.mark.parametrize("T,V,kind,D", [
+    (300, 7, "words", 72), (5000, 40, "words", 72), (9001, 3, "even", 72), (40000, 2, "one", 72), (17001, 90, "words", 1033),
+    (4097, 4097, "even", 520), (16385, 3, "words", 1), (66000, 20, "falling", 72), (33, 5, "words", 600)])
 @pytest.mark.parametrize("dtype", [BF16, F32])
-def test_whole_numbers_bit_for_bit(tide, T, V, kind, dtype):
+def test_whole_numbers_bit_for_bit(tide, T, V, kind, D, dtype):
     """Sums of whole numbers are exact in fp32 in any order: a token left out, one
     taken twice or a sum joined in bf16 would show."""
-    D = 72
     ids = some_ids(T, V, T, kind)
     off, order = sort(tide, ids, V)
     dout, old = ref.whole((T, D), 9, T).to(dtype), ref.whole((V, D), 9, 3).to(dtype)
@@ -184,6 +185,27 @@ def test_offsets_and_order_of_other_making(tide):
     tide.embed_tokens_grad(dout.to(dev()), off.to(dev()), order.to(dev()), grad)
     want, lim = step.table_grad(dout, off, order, V, 1.0)
     ref.close(grad, want, lim + step.U * want.abs(), "clamped")
+
+
+@pytest.mark.parametrize("T", [17, 700, 5000, 17000])
+@pytest.mark.parametrize("more", [False, True])
+def test_offsets_that_do_not_rise(tide, T, more):
+    """Rows that overlap, that are empty or that go back, over chunks of the order:
+    each is the sum of its own places."""
+    g = torch.Generator().manual_seed(T)
+    V, D = 40, 40
+    off = torch.randint(-50, T + 50, (V + 1,), generator=g).to(torch.int32)
+    off[10:20] = torch.sort(off[10:20]).values
+    off[20:25] = T // 3
+    order = torch.randint(-5, T + 5, (T,), generator=g).to(torch.int32)
+    dout, old = ref.whole((T, D), 9, T).float(), ref.whole((V, D), 9, 3).float()
+    padded = torch.cat([dout.double(), torch.zeros(1, D, dtype=torch.float64)])
+    rows = padded[torch.where((order >= 0) & (order < T), order.long(), T)]
+    want = torch.stack([rows[max(int(off[v]), 0): max(min(int(off[v + 1]), T), 0)].sum(0)
+                        for v in range(V)]) + (old.double() if more else 0.0)
+    grad = old.to(dev()).clone()
+    tide.embed_tokens_grad(dout.to(dev()), off.to(dev()), order.to(dev()), grad, accumulate=more)
+    assert torch.equal(grad.cpu().double(), want)
 
 
 def test_large_offsets(tide):
