@@ -826,7 +826,8 @@ typedef struct tide_rotation {
  *     at least head_dim; heads of one tensor do not share memory.
  *   q_weight, k_weight: head_dim elements of the same type, NULL for ones.
  *   rotation: NULL for none.
- * Errors: INVALID_ARG, ALIGNMENT, OVERFLOW, UNSUPPORTED (head_dim), HIP.
+ * Errors: INVALID_ARG, ALIGNMENT, OVERFLOW, UNSUPPORTED (head_dim, tokens past
+ * 2^31 - 1, over 2^24 heads), HIP.
  */
 tide_status tide_norm_rotate(int32_t dtype, int64_t tokens, int32_t head_dim,
                              const tide_heads* q, const tide_heads* k, const void* q_weight,

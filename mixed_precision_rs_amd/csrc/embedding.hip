@@ -638,40 +638,45 @@ __device__ __forceinline__ bool add_left(const Chunks& from, int64_t v, int64_t 
 // each: its waves add up a run of the sums each, and the first wave the runs, in
 // order.
 constexpr int kJoinWaves = 16;
+constexpr int64_t kJoinGroups = (int64_t)1 << 20;
 template <class T>
-__global__ __launch_bounds__(64 * kJoinWaves) void join_left(Sorted s, Chunks from, Grad<T> grad, int64_t tiles) {
+__global__ __launch_bounds__(64 * kJoinWaves) void join_left(Sorted s, Chunks from, Grad<T> grad, int64_t tiles,
+                                                             int64_t parts) {
     constexpr int V = kVecOf<T>;
     __shared__ float runs[kJoinWaves][V][64];
     __shared__ int gone;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int64_t b = blockIdx.x / tiles, tile = blockIdx.x - b * tiles, u = tile * 64 + lane;
-    int64_t v = *gbl<int32_t>(from.row_of + 2 * b + 1), lo = 0, hi = 0;
-    if (v < 0) v = *gbl<int32_t>(from.row_of + 2 * b);
-    if (v < 0) return;
-    row_range(s, v, lo, hi);
-    const int64_t last = (hi - 1) / from.size, all = last - b + 1, per = (all + kJoinWaves - 1) / kJoinWaves;
-    if (lo / from.size != b || all < kJoinWaves) return;
-    if (threadIdx.x == 0) gone = 0;
-    __syncthreads();
-    for (int64_t i = threadIdx.x; i < all; i += 64 * kJoinWaves)
-        if (*gbl<int32_t>(from.row_of + 2 * (b + i) + (lo <= (b + i) * from.size ? 0 : 1)) != v) gone = 1;
-    __syncthreads();
-    if (gone) return;
-    float sum[V] = {};
-    const int64_t b0 = b + wave * per, b1 = b0 + per - 1 < last ? b0 + per - 1 : last;
-    if (b0 <= b1) add_sums<V>(from, lo, b0, b1, u * V < grad.width ? u : 0, sum);
+    for (int64_t part = blockIdx.x; part < parts; part += gridDim.x) {
+        const int64_t b = part / tiles, tile = part - b * tiles, u = tile * 64 + lane;
+        int64_t v = *gbl<int32_t>(from.row_of + 2 * b + 1), lo = 0, hi = 0;
+        if (v < 0) v = *gbl<int32_t>(from.row_of + 2 * b);
+        if (v < 0) continue;
+        row_range(s, v, lo, hi);
+        const int64_t last = (hi - 1) / from.size, all = last - b + 1, per = (all + kJoinWaves - 1) / kJoinWaves;
+        if (lo / from.size != b || all < kJoinWaves) continue;
+        __syncthreads();                           // of the part before: runs and gone are free
+        if (threadIdx.x == 0) gone = 0;
+        __syncthreads();
+        for (int64_t i = threadIdx.x; i < all; i += 64 * kJoinWaves)
+            if (*gbl<int32_t>(from.row_of + 2 * (b + i) + (lo <= (b + i) * from.size ? 0 : 1)) != v) gone = 1;
+        __syncthreads();
+        if (gone) continue;
+        float sum[V] = {};
+        const int64_t b0 = b + wave * per, b1 = b0 + per - 1 < last ? b0 + per - 1 : last;
+        if (b0 <= b1) add_sums<V>(from, lo, b0, b1, u * V < grad.width ? u : 0, sum);
 #pragma unroll
-    for (int c = 0; c < V; ++c) runs[wave][c][lane] = sum[c];
-    __syncthreads();
-    if (wave) return;
+        for (int c = 0; c < V; ++c) runs[wave][c][lane] = sum[c];
+        __syncthreads();
+        if (wave) continue;
 #pragma unroll
-    for (int c = 0; c < V; ++c) sum[c] = 0.0f;
+        for (int c = 0; c < V; ++c) sum[c] = 0.0f;
 #pragma unroll 1
-    for (int w = 0; w < kJoinWaves; ++w)
+        for (int w = 0; w < kJoinWaves; ++w)
 #pragma unroll
-        for (int c = 0; c < V; ++c) sum[c] += runs[w][c][lane];
-    put_vector<T>(grad, v, u, sum, old_vector<T>(grad, v, u));
-    if (tile == 0 && lane == 0) *gbl_mut<int32_t>(from.owner + lo) = (int32_t)v;
+            for (int c = 0; c < V; ++c) sum[c] += runs[w][c][lane];
+        put_vector<T>(grad, v, u, sum, old_vector<T>(grad, v, u));
+        if (tile == 0 && lane == 0) *gbl_mut<int32_t>(from.owner + lo) = (int32_t)v;
+    }
 }
 
 // Vector u of row v, unless it has been written.
@@ -893,8 +898,9 @@ tide_status tide_embed_tokens_grad(int32_t dtype, const void* dout, int64_t dout
                     if (e != hipSuccess) return e;
                 }
                 if (n && tokens > kJoinTokens) {
-                    const hipError_t e = enqueue(join_left<T>, dim3((uint32_t)(n * tiles)), 64 * kJoinWaves, 0, s, sorted,
-                                                 chunks, to, tiles);
+                    const int64_t parts = n * tiles;
+                    const hipError_t e = enqueue(join_left<T>, dim3((uint32_t)(parts < kJoinGroups ? parts : kJoinGroups)),
+                                                 64 * kJoinWaves, 0, s, sorted, chunks, to, tiles, parts);
                     if (e != hipSuccess) return e;
                 }
                 if (accumulate) {

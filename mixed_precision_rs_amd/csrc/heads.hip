@@ -18,6 +18,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kMostDim = 512;
+constexpr int32_t kMostHeads = 1 << 24;
 
 struct Heads {
     const void* data;
@@ -533,7 +534,7 @@ tide_status tide_norm_rotate(int32_t dtype, int64_t tokens, int32_t head_dim,
         TIDE_TRY(check_turn(rotation, tokens, head_dim, &turn, &rd[4]));
         TIDE_TRY(no_overlap(wr, 2, rd, 7));
         const int64_t all = (int64_t)hq.heads + hk.heads;
-        if (all > INT32_MAX) return fail(TIDE_ERR_UNSUPPORTED, "heads must be below 2^31");
+        if (all > kMostHeads) return fail(TIDE_ERR_UNSUPPORTED, "q and k have over %d heads", kMostHeads);
         if (all == 0) return TIDE_OK;
         return on_stream(stream, [&](hipStream_t s) {
             return with_slots(size, head_dim, turn.pairs, rotation && rotation->adjacent,
@@ -559,6 +560,7 @@ tide_status tide_norm_rotate_grad_workspace(int64_t tokens, int32_t heads, int32
         if (!bytes) return fail(TIDE_ERR_INVALID_ARG, "bytes is NULL");
         TIDE_TRY(check_dims(tokens, head_dim));
         if (heads < 0) return fail(TIDE_ERR_INVALID_ARG, "negative heads");
+        if (heads > kMostHeads) return fail(TIDE_ERR_UNSUPPORTED, "over %d heads", kMostHeads);
         *bytes = grad_groups(tokens, heads, head_dim) * 2 * head_dim * 4;
         return TIDE_OK;
     });
@@ -593,7 +595,7 @@ tide_status tide_norm_rotate_grad(int32_t dtype, int64_t tokens, int32_t head_di
         TIDE_TRY(matrix("dq_weight", dq_weight, dq_weight ? 1 : 0, head_dim, head_dim, size, &wr[2]));
         TIDE_TRY(matrix("dk_weight", dk_weight, dk_weight ? 1 : 0, head_dim, head_dim, size, &wr[3]));
         const int64_t all = (int64_t)hq.heads + hk.heads;
-        if (all > INT32_MAX) return fail(TIDE_ERR_UNSUPPORTED, "heads must be below 2^31");
+        if (all > kMostHeads) return fail(TIDE_ERR_UNSUPPORTED, "q and k have over %d heads", kMostHeads);
         int64_t need = 0;
         if (dq_weight || dk_weight) TIDE_TRY(tide_norm_rotate_grad_workspace(tokens, (int32_t)all, head_dim, &need));
         if (need > 0 && (!workspace || workspace_bytes < need))

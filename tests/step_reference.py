@@ -62,12 +62,11 @@ def logprobs(x, targets, top=0):
     d_logprob, d_log_s, d_entropy, d_top.
 
     exp(x - m) is off by the rounding of x - m (u |z|), of the product with log2(e)
-    and that constant (1.5 u |z|) and of the instruction (2 u). A lane adds its
-    terms one by one, at least 64 lanes a row (V / 64 additions), and brings its
-    sum to a new maximum at most once for each logit it has seen, each time off by
-    the same as one exp at the rise, the rises adding up to at most the row's
-    range; ten joins. So s is off by delta = (V / 64 * 4 + 30 + 5 range) u, range
-    cut at 200, where exp is 0."""
+    and that constant (1.5 u |z|) and of the instruction (2 u). With 64 lanes a row or
+    more, a sum takes at most V / 64 additions, and is brought to a new maximum at
+    most once for each, each time off by the same as one exp at the rise, the rises
+    adding up to at most the row's range; ten joins. So s is off by at most delta =
+    (V / 64 * 4 + 30 + 5 range) u, range cut at 200, where exp is 0."""
     x = x.double()
     T, V = x.shape
     out = {k: [] for k in ("logprob", "m", "log_s", "entropy", "top_ids", "top_logprobs", "d_logprob", "d_log_s",

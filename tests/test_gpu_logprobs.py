@@ -135,6 +135,27 @@ def test_alternatives_that_one_lane_or_one_stretch_holds(tide, dtype):
             assert torch.equal(v, first[k].repeat(times, *[1] * (v.dim() - 1))), k
 
 
+@pytest.mark.parametrize("T", [3, 70, 300, 600])
+def test_more_candidates_than_are_ranked_at_once(tide, T):
+    """A lane whose whole share of a long row is ahead of all others', and 32 of them,
+    for every number of lanes that a row may have."""
+    V, top, n = 262144, 32, 8
+    u = torch.arange(V) // n
+    for lanes in (256, 512, 1024):
+        one = torch.full((V,), -9.0)
+        mine = u % lanes == 5
+        one[mine] = (torch.arange(V)[mine] % 97).float() / 8
+        many = torch.where((u % lanes % (lanes // 64) == 0) & (u % lanes < lanes // 2), 1.0 + (u % lanes) // (lanes // 64), -9.0)
+        for row in (one, many):
+            x = row.to(BF16)
+            want = torch.sort(x.float(), descending=True, stable=True)
+            got = run(tide, x.expand(T, V).contiguous(), torch.arange(T), top)
+            assert (got["top_ids"].cpu() == want.indices[:top].int()).all()
+            log_s = torch.logsumexp(x.double(), 0)
+            room = (V / 16 + 30 + 5 * 42 + 8 * 50) * step.U          # the reference's: logits from -9 to 33, log s below 50
+            ref.close(got["top_logprobs"], (want.values[:top].double() - log_s).expand(T, top), room, "many")
+
+
 def test_outputs_left_out(tide):
     x, t = ref.normal((5, 777), BF16, 1), some_targets(5, 777, 1)
     full = run(tide, x, t, 4)
