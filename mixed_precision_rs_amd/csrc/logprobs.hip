@@ -455,13 +455,17 @@ tide_status check(int32_t dtype, int64_t tokens, int64_t vocab, int32_t id_bytes
     return TIDE_OK;
 }
 
-// Threads of a row's workgroup: as many as fill the GPU with the rows there are
-// (1024 threads with alternatives are one workgroup a CU). 257 rows of 50001 fp32
-// with 20 alternatives: 24 us with 512, 33 with 1024 (the last row alone); 700 rows:
-// 40 with 256, 42 with 512, 56 with 1024.
+// Threads of a row's workgroup: as many as give 4096 waves with the rows there are
+// (four a SIMD, what fits with alternatives), two vectors each at least, and four
+// waves for rows over 128 KiB. us with 64 / 256 threads: 4096 rows of 4000 bf16
+// 12 / 22, of 8000 18 / 25 (with 8 alternatives 27 / 44), of 32000 48 / 54, of 131072
+// 194 / 183; 200 rows of 16000 10 / 6. 257 rows of 50001 fp32 with 20 alternatives: 24
+// with 512, 33 with 1024; 700 rows 40 with 256, 42 with 512, 56 with 1024.
 int threads_of(int64_t tokens, int64_t units) {
-    if (units <= 256) return 64;
-    return units <= 2048 || tokens > 512 ? 256 : tokens > 256 ? 512 : 1024;
+    int waves = units > 8192 ? 4 : 1;
+    while (waves < 16 && 2 * waves * tokens <= 4096) waves *= 2;
+    while (waves > 1 && waves * 128 > units) waves /= 2;
+    return 64 * waves;
 }
 // Parts of a row, of 16 KiB at least, for few tokens. One row of 131072 bf16 with 8
 // alternatives: 12.3 us in 16 parts and their join, 17.2 in one workgroup; 32 rows
@@ -553,6 +557,7 @@ tide_status tide_token_logprobs(int32_t dtype, const void* logits, int64_t logit
                                    logits_stride, tokens, vocab, (const Id*)targets, to, parts);
                 }
                 return threads == 64    ? with(std::integral_constant<int, 64>{}, No{})
+                       : threads == 128 ? with(std::integral_constant<int, 128>{}, No{})
                        : threads == 256 ? with(std::integral_constant<int, 256>{}, No{})
                        : threads == 512 ? with(std::integral_constant<int, 512>{}, No{})
                                         : with(std::integral_constant<int, 1024>{}, No{});
