@@ -5,7 +5,9 @@
 // other lane: with halves as pairs it loads one vector from either half of the
 // rotated elements, with adjacent pairs two neighbouring vectors. The lanes of a
 // head join its sum of squares (and, in the gradient, one dot product) by
-// exchanges.
+// exchanges. Both are HBM streams that touch each byte once; the angles' tables,
+// one row a token, come from the caches.
+#include <algorithm>
 #include <climits>
 #include <cmath>
 
@@ -248,9 +250,11 @@ __global__ __launch_bounds__(kThreads) void rotate_heads(Heads q, Heads k, Heads
 
 // The gradient of one set of heads; partial (when not NULL) gets this
 // workgroup's sum of g * n, dim fp32 in element order. A wave takes 64 >> lane_log2
-// heads of a token at a time, then those some waves further on. (The next ones'
-// loads under way meanwhile: 51 us instead of 49 for 8191 tokens of 36 heads; 512 or
-// 2048 workgroups instead of 1024: 62 and 57.)
+// heads of a token at a time, then those some waves further on. Bound by HBM and by
+// the waves that 104 registers leave (four a SIMD): 8191 tokens of 36 heads of 128 in
+// 46 us, 231 MB. (The next ones' loads under way meanwhile were 4% slower, 512 or 2048
+// workgroups instead of 1024 26 and 16%, queries and then keys by the same workgroups
+// 9%.)
 struct Steps {
     int64_t t;             // the step between a wave's turns: tokens, and sets of heads
     int32_t part, parts;   // sets of heads of a token
@@ -258,7 +262,7 @@ struct Steps {
 template <class T, int W, int NS, bool kAdjacent>
 __device__ __forceinline__ void grad_of(const Heads& x, const Heads& dy, const Heads& dx, const void* w,
                                         const Turn& turn, int64_t tokens, int dim, float eps, int lane_log2,
-                                        Steps step, float* partial, float* joint) {
+                                        Steps step, int64_t group0, float* partial, float* joint) {
     using S = Slot<T, W, kAdjacent>;
     const int lanes = 1 << lane_log2, lane = threadIdx.x & (lanes - 1), group = threadIdx.x >> lane_log2;
     const int half = dim / 2, slots = half / W, at_once = 64 >> lane_log2;
@@ -271,7 +275,7 @@ __device__ __forceinline__ void grad_of(const Heads& x, const Heads& dy, const H
         S::where(s, half, turn.pairs, a[i], b[i]);
         if (s < slots) weights<T, W, kAdjacent>(w, a[i], b[i], wu[i], wv[i]);
     }
-    const int64_t w0 = (int64_t)blockIdx.x * (kThreads / 64) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t w0 = ((int64_t)blockIdx.x - group0) * (kThreads / 64) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     int64_t t = step.parts ? w0 / step.parts : tokens;
     int32_t part = (int32_t)(w0 - t * step.parts);
     while (t < tokens) {
@@ -362,39 +366,61 @@ __device__ __forceinline__ void grad_of(const Heads& x, const Heads& dy, const H
     }
 }
 
+// The first workgroups take the queries, the others the keys.
 template <class T, int W, int NS, bool kAdjacent>
 __global__ __launch_bounds__(kThreads) void rotate_heads_grad(Heads q, Heads k, Heads dqo, Heads dko,
                                                               Heads dq, Heads dk, const void* qw,
                                                               const void* kw, Turn turn, int64_t tokens,
                                                               int dim, float eps, int lane_log2, Steps of_q,
-                                                              Steps of_k, float* partial, int want_q, int want_k) {
+                                                              Steps of_k, int64_t of_queries, float* partial,
+                                                              int want_q, int want_k) {
     __shared__ float joint[kThreads * 2 * W * NS];
-    float* mine = partial + (int64_t)blockIdx.x * 2 * dim;
-    grad_of<T, W, NS, kAdjacent>(q, dqo, dq, qw, turn, tokens, dim, eps, lane_log2, of_q, want_q ? mine : nullptr, joint);
-    grad_of<T, W, NS, kAdjacent>(k, dko, dk, kw, turn, tokens, dim, eps, lane_log2, of_k, want_k ? mine + dim : nullptr,
-                                 joint);
+    float* mine = partial + (int64_t)blockIdx.x * dim;
+    if (blockIdx.x < of_queries)
+        grad_of<T, W, NS, kAdjacent>(q, dqo, dq, qw, turn, tokens, dim, eps, lane_log2, of_q, 0, want_q ? mine : nullptr,
+                                     joint);
+    else
+        grad_of<T, W, NS, kAdjacent>(k, dko, dk, kw, turn, tokens, dim, eps, lane_log2, of_k, of_queries,
+                                     want_k ? mine : nullptr, joint);
 }
 
-// Weights' gradients: the workgroups' sums in order, 16 runs of them at once.
-constexpr int kRuns = 16;
+// Weights' gradients: the workgroups' sums in order, 64 runs of them at once, 16
+// elements a workgroup (819 and 205 sums of 128: 4.6 us; 64 elements in 16 runs 6).
+constexpr int kRuns = 64, kColumns = 16;
 template <class T>
-__global__ __launch_bounds__(64 * kRuns) void join_weights(const float* partial, int64_t groups, int dim,
-                                                           T* dqw, T* dkw, int accumulate) {
-    __shared__ float part[kRuns][64];
-    const int e = blockIdx.x * 64 + (threadIdx.x & 63), run = threadIdx.x >> 6;
+__global__ __launch_bounds__(kRuns * kColumns) void join_weights(const float* partial, int64_t of_queries,
+                                                                 int64_t of_keys, int dim, T* dqw, T* dkw,
+                                                                 int accumulate) {
+    __shared__ float part[kRuns][kColumns];
+    const int c = threadIdx.x % kColumns, e = blockIdx.x * kColumns + c, run = threadIdx.x / kColumns;
     T* to = blockIdx.y ? dkw : dqw;
     if (!to) return;
+    const int64_t first = blockIdx.y ? of_queries : 0, groups = blockIdx.y ? of_keys : of_queries;
     const int64_t per = (groups + kRuns - 1) / kRuns;
+    const int64_t end = (run + 1) * per < groups ? (run + 1) * per : groups;
     float sum = 0.0f;
     if (e < dim)
-#pragma unroll 16
-        for (int64_t g = run * per; g < (run + 1) * per; ++g)
-            sum += g < groups ? *gbl<float>(partial + (2 * g + blockIdx.y) * dim + e) : 0.0f;
-    part[run][threadIdx.x & 63] = sum;
+        for (int64_t g = run * per; g < end; g += 16) {
+            float v[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) v[i] = g + i < end ? *gbl<float>(partial + (first + g + i) * dim + e) : 0.0f;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) sum += v[i];
+        }
+    part[run][c] = sum;
+    __syncthreads();
+    if (run < 8) {
+        sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sum += part[8 * run + i][c];
+    }
+    __syncthreads();
+    if (run < 8) part[run][c] = sum;
     __syncthreads();
     if (run || e >= dim) return;
     sum = 0.0f;
-    for (int i = 0; i < kRuns; ++i) sum += part[i][threadIdx.x];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sum += part[i][c];
     if constexpr (sizeof(T) == 2) {
         if (accumulate) sum += lo_bf16(*gbl<T>(to + e));
         *gbl_mut<T>(to + e) = (T)pack_bf16(sum, 0.0f);
@@ -475,26 +501,32 @@ tide_status check_turn(const tide_rotation* r, int64_t tokens, int32_t dim, Turn
     return TIDE_OK;
 }
 
-// Calls go(T, W, NS, adjacent, lane_log2), with the widest slots of W pairs that
-// lie on one side of the rotated elements' end each: whole vectors, half ones of
-// bf16, or single pairs.
+// Pairs of a slot: the widest slots that lie on one side of the rotated elements'
+// end each: whole vectors, half ones of bf16, or single pairs.
+int slot_pairs(int32_t size, int dim, int pairs) {
+    const auto fits = [&](int w) { return dim / 2 % w == 0 && pairs % w == 0; };
+    return size == 2 && fits(8) ? 8 : fits(4) ? 4 : 1;
+}
+int lanes_log2(int32_t size, int dim, int pairs) {
+    const int slots = dim / 2 / slot_pairs(size, dim, pairs);
+    int lg = 0;
+    while (lg < 6 && (1 << lg) < slots) ++lg;
+    return lg;
+}
+// Calls go(T, W, NS, adjacent).
 template <class F>
 hipError_t with_slots(int32_t size, int dim, int pairs, bool adjacent, F&& go) {
-    const int half = dim / 2;
-    const auto fits = [&](int w) { return half % w == 0 && pairs % w == 0; };
     const auto with = [&](auto type, auto w, auto ns) {
-        const int slots = half / w.value;
-        int lg = 0;
-        while (lg < 6 && (1 << lg) < slots) ++lg;
-        return adjacent ? go(type, w, ns, std::true_type{}, lg) : go(type, w, ns, std::false_type{}, lg);
+        return adjacent ? go(type, w, ns, std::true_type{}) : go(type, w, ns, std::false_type{});
     };
     using One = std::integral_constant<int, 1>;
     using Four = std::integral_constant<int, 4>;
     using Eight = std::integral_constant<int, 8>;
     using Most = std::integral_constant<int, kMostDim / 128>;
+    const int w = slot_pairs(size, dim, pairs);
     if (size == 2)
-        return fits(8) ? with(uint16_t{}, Eight{}, One{}) : fits(4) ? with(uint16_t{}, Four{}, One{}) : with(uint16_t{}, One{}, Most{});
-    return fits(4) ? with(float{}, Four{}, One{}) : with(float{}, One{}, Most{});
+        return w == 8 ? with(uint16_t{}, Eight{}, One{}) : w == 4 ? with(uint16_t{}, Four{}, One{}) : with(uint16_t{}, One{}, Most{});
+    return w == 4 ? with(float{}, Four{}, One{}) : with(float{}, One{}, Most{});
 }
 
 tide_status check_type(int32_t dtype) {
@@ -536,9 +568,10 @@ tide_status tide_norm_rotate(int32_t dtype, int64_t tokens, int32_t head_dim,
         const int64_t all = (int64_t)hq.heads + hk.heads;
         if (all > kMostHeads) return fail(TIDE_ERR_UNSUPPORTED, "q and k have over %d heads", kMostHeads);
         if (all == 0) return TIDE_OK;
+        const int lg = lanes_log2(size, head_dim, turn.pairs);
         return on_stream(stream, [&](hipStream_t s) {
             return with_slots(size, head_dim, turn.pairs, rotation && rotation->adjacent,
-                              [&](auto type, auto w, auto ns, auto adjacent, int lg) {
+                              [&](auto type, auto w, auto ns, auto adjacent) {
                 const auto go = [&](auto kh) {
                     const int64_t at_once = 64 >> lg, sets = (all + at_once - 1) / at_once;
                     const int64_t parts = (sets + kh.value - 1) / kh.value, waves = tokens * parts;
@@ -606,26 +639,33 @@ tide_status tide_norm_rotate_grad(int32_t dtype, int64_t tokens, int32_t head_di
             return fail(TIDE_ERR_ALIGNMENT, "workspace is not 16-byte aligned");
         TIDE_TRY(no_overlap(wr, 5, rd, 9));
         if (head_dim == 0 || (all == 0 && need == 0)) return TIDE_OK;
-        const int64_t groups = grad_groups(tokens, all, head_dim);
+        // The workgroups, shared by queries and keys as their waves' turns are.
+        const int lg = lanes_log2(size, head_dim, turn.pairs);
+        const int64_t at_once = 64 >> lg, groups = grad_groups(tokens, all, head_dim);
+        const int64_t turns_q = (hq.heads + at_once - 1) / at_once, turns_k = (hk.heads + at_once - 1) / at_once;
+        const int64_t of_queries = turns_q ? std::max<int64_t>(groups * turns_q / (turns_q + turns_k), 1) : dq_weight ? 1 : 0;
+        const int64_t of_keys = turns_k ? std::max<int64_t>(groups - of_queries, 1) : dk_weight ? 1 : 0;
+        const auto steps = [](int64_t turns, int64_t of) {
+            const int64_t waves = of * (kThreads / 64);
+            return turns ? Steps{waves / turns, (int32_t)(waves % turns), (int32_t)turns} : Steps{};
+        };
         return on_stream(stream, [&](hipStream_t s) {
             const hipError_t e = with_slots(size, head_dim, turn.pairs, rotation && rotation->adjacent,
-                                            [&](auto type, auto w, auto ns, auto adjacent, int lg) {
-                const int64_t waves = groups * (kThreads / 64);
-                const auto steps = [&](int32_t heads) {
-                    const int64_t at_once = 64 >> lg, parts = (heads + at_once - 1) / at_once;
-                    return parts ? Steps{waves / parts, (int32_t)(waves % parts), (int32_t)parts} : Steps{};
-                };
+                                            [&](auto type, auto w, auto ns, auto adjacent) {
                 return enqueue(rotate_heads_grad<decltype(type), w.value, ns.value, adjacent.value>,
-                               dim3((uint32_t)groups), kThreads, 0, s, hq, hk, gq, gk, xq, xk, q_weight, k_weight,
-                               turn, tokens, (int)head_dim, eps, lg, steps(hq.heads), steps(hk.heads),
-                               (float*)workspace, dq_weight ? 1 : 0, dk_weight ? 1 : 0);
+                               dim3((uint32_t)(of_queries + of_keys)), kThreads, 0, s, hq, hk, gq, gk, xq, xk, q_weight,
+                               k_weight, turn, tokens, (int)head_dim, eps, lg, steps(turns_q, of_queries),
+                               steps(turns_k, of_keys), of_queries, (float*)workspace, dq_weight ? 1 : 0,
+                               dk_weight ? 1 : 0);
             });
             if (e != hipSuccess || need == 0) return e;
-            const dim3 grid((uint32_t)((head_dim + 63) / 64), 2);
-            return size == 2 ? enqueue(join_weights<uint16_t>, grid, 64 * kRuns, 0, s, (const float*)workspace, groups,
-                                       (int)head_dim, (uint16_t*)dq_weight, (uint16_t*)dk_weight, accumulate ? 1 : 0)
-                             : enqueue(join_weights<float>, grid, 64 * kRuns, 0, s, (const float*)workspace, groups,
-                                       (int)head_dim, (float*)dq_weight, (float*)dk_weight, accumulate ? 1 : 0);
+            const dim3 grid((uint32_t)((head_dim + kColumns - 1) / kColumns), 2);
+            const auto join = [&](auto type) {
+                using T = decltype(type);
+                return enqueue(join_weights<T>, grid, kRuns * kColumns, 0, s, (const float*)workspace, of_queries, of_keys,
+                               (int)head_dim, (T*)dq_weight, (T*)dk_weight, accumulate ? 1 : 0);
+            };
+            return size == 2 ? join(uint16_t{}) : join(float{});
         });
     });
 }
