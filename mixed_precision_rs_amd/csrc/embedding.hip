@@ -397,7 +397,7 @@ __global__ __launch_bounds__(kRowThreads) void embed_rows(const Id* ids, int64_t
 // table: rows without tokens become zeros, rows whose sums were left are joined.
 // A kernel that reads and then one that writes: with the tokens added up among the
 // waves that clear (most of a large table) 16384 tokens in 131072 x 2048 took 126 us,
-// mixed through the whole of it 156-195, and so 30 and 78, the rate of a fill.
+// mixed through the whole of it 156-195, and so 30 and 74.
 //
 // Offsets that do not come from a sort may leave rows that no chunk finds whole:
 // owner says for each place whether the row that begins there was written, row_of
@@ -715,24 +715,35 @@ __device__ __forceinline__ void finish_vector(const Sorted& s, const Chunks& fro
     put_vector<T>(grad, v, u, sum, old_vector<T>(grad, v, u));
 }
 
-// Wide rows: a wave takes 64 vectors of one row of the table, then those some waves
-// further on. 32768 workgroups: 2048 that stay clear 131072 x 2048 in 108 us, these
-// in 85, the rate of a fill.
-constexpr int64_t kGradGroups = 32768;
+// Wide rows: a wave takes 64 vectors of two rows, far from each other, since those
+// of frequent words stand together. A lane looks up a row, so that both wait once
+// before they are cleared. 131072 x 2048 bf16, 16384 tokens: 74 us, the rate of a
+// fill; with one row a wave 118, with 4 94, with 8 106, in half the workgroups 89.
+constexpr int kRowsAtOnce = 2;
+constexpr int64_t kTableGroups = 65536, kAddedGroups = 32768;
 template <class T>
 __global__ __launch_bounds__(kRowThreads) void finish_table(Sorted s, Chunks from, const T* dout, int64_t stride,
-                                                            Grad<T> grad, int64_t tiles, int64_t step_rows,
-                                                            int64_t step_tiles) {
-    const int64_t w = (int64_t)blockIdx.x * (kRowThreads / 64) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    int64_t v = w / tiles, tile = w - v * tiles;
-    while (v < s.vocab) {
-        finish_vector<T>(s, from, dout, stride, grad, v, tile * 64 + (threadIdx.x & 63));
-        v += step_rows;
-        tile += step_tiles;
-        if (tile >= tiles) {
-            tile -= tiles;
-            ++v;
+                                                            Grad<T> grad, int64_t parts, int64_t tiles) {
+    constexpr int V = kVecOf<T>;
+    const int lane = threadIdx.x & 63;
+    for (int64_t w = (int64_t)blockIdx.x * (kRowThreads / 64) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+         w < parts * tiles; w += (int64_t)gridDim.x * (kRowThreads / 64)) {
+        const int64_t part = w / tiles, u = (w - part * tiles) * 64 + lane, v = lane * parts + part;
+        int64_t lo = 0, hi = 0;
+        const bool mine = lane < kRowsAtOnce && v < s.vocab;
+        if (mine) row_range(s, v, lo, hi);
+        const uint64_t clear = __ballot(mine && lo >= hi);
+        bool open = lo < hi;
+        if (open && from.size) open = *gbl<int32_t>(from.owner + lo) != v;
+        if (u * V < grad.width) {
+            T* to = grad.data + part * grad.stride + column<V>(u, grad.width);
+            const int some = grad.width < V ? (int)grad.width : V;
+#pragma unroll
+            for (int j = 0; j < kRowsAtOnce; ++j)
+                if (clear >> j & 1) store_row(to + j * parts * grad.stride, some, u32x4{});
         }
+        for (uint64_t left = __ballot(open); left; left &= left - 1)
+            finish_vector<T>(s, from, dout, stride, grad, __builtin_ctzll(left) * parts + part, u);
     }
 }
 
@@ -909,7 +920,7 @@ tide_status tide_embed_tokens_grad(int32_t dtype, const void* dout, int64_t dout
                 }
                 if (accumulate) {
                     const int64_t parts = (vocab + 63) / 64, groups = (parts * tiles + 3) / 4;
-                    return enqueue(finish_added<T>, dim3((uint32_t)(groups < kGradGroups ? groups : kGradGroups)),
+                    return enqueue(finish_added<T>, dim3((uint32_t)(groups < kAddedGroups ? groups : kAddedGroups)),
                                    kRowThreads, 0, s, sorted, chunks, (const T*)dout, dout_stride, to, parts, tiles);
                 }
                 if (units <= 32) {
@@ -917,9 +928,9 @@ tide_status tide_embed_tokens_grad(int32_t dtype, const void* dout, int64_t dout
                     return enqueue(finish_narrow<T>, dim3(g.grid.x), kRowThreads, 0, s, sorted, chunks, (const T*)dout,
                                    dout_stride, to, g.lane_log2);
                 }
-                const int64_t all = (vocab * tiles + 3) / 4, groups = all < kGradGroups ? all : kGradGroups;
-                return enqueue(finish_table<T>, dim3((uint32_t)groups), kRowThreads, 0, s, sorted, chunks,
-                               (const T*)dout, dout_stride, to, tiles, 4 * groups / tiles, 4 * groups % tiles);
+                const int64_t parts = (vocab + kRowsAtOnce - 1) / kRowsAtOnce, groups = (parts * tiles + 3) / 4;
+                return enqueue(finish_table<T>, dim3((uint32_t)(groups < kTableGroups ? groups : kTableGroups)), kRowThreads, 0, s,
+                               sorted, chunks, (const T*)dout, dout_stride, to, parts, tiles);
             };
             return size == 2 ? go(uint16_t{}) : go(float{});
         });
