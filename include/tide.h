@@ -778,6 +778,7 @@ tide_status tide_token_logprobs(int32_t dtype, const void* logits, int64_t logit
  * Gradient of tide_token_logprobs to the logits, in fp32, rounded once: with
  * lp = x - stats[t][0] - stats[t][1] and p = exp(lp),
  *   dlogits[t, i] = dlogprob[t] * ([i = target] - p) - dentropy[t] * p * (lp + entropy[t]).
+ * A probability below 2^-126 (the smallest normal fp32 number) counts as 0.
  * A row whose target is outside [0, vocab) has no first term, whatever
  * dlogprob holds there; without dentropy (NULL; then entropy may be NULL) its
  * logits are not read and its gradient is zeros, as is that of a row in which

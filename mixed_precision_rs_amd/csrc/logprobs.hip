@@ -383,8 +383,11 @@ __global__ __launch_bounds__(kJoinThreads) void join_parts(const T* logits, int6
 }
 
 // p = exp(x - m - log s) = 2^(x log2(e) - c) 2^d, as in the forward pass; the
-// factor 2^d goes to the row's factors. A stream of reads and writes: 4096 x 131072
-// bf16 in 361 us (5.6 TB/s). A lane has KU vectors in hand at a time (one: 497 us).
+// factor 2^d goes to the row's factors. c has to come from the same fp32 log2(e) that x
+// is multiplied by: then its error (1.3e-8 of it) is one of x - m - log s, with another
+// constant one of x, which a row far from zero makes as large as it likes. A stream of
+// reads and writes: 4096 x 131072 bf16 in 361 us (5.6 TB/s). A lane has KU vectors in
+// hand at a time (one: 497 us).
 constexpr int kGradVectors = 4;
 template <class T, class Id, int kThreads, bool kEntropy>
 __global__ __launch_bounds__(kThreads) void row_logprobs_grad(
@@ -399,7 +402,7 @@ __global__ __launch_bounds__(kThreads) void row_logprobs_grad(
         const float d = at >= 0 ? *gbl<float>(dlogprob + r) : 0.0f;
         const float h = kEntropy ? *gbl<float>(dentropy + r) : 0.0f, H = kEntropy ? *gbl<float>(entropy + r) : 0.0f;
         const bool zero = (at < 0 && !kEntropy) || m == kNegInf, tame = fabsf(m) < kTame;
-        const double exact = ((double)m + (double)log_s) * 0x1.71547652b82fep+0;
+        const double exact = ((double)m + (double)log_s) * (double)kLog2e;
         const float c0 = (float)exact, rest = (float)((double)c0 - exact), f = __builtin_amdgcn_exp2f(rest);
         for (int64_t u0 = (int64_t)blockIdx.y * KU * kThreads; u0 < units; u0 += (int64_t)gridDim.y * KU * kThreads) {
             float v[KU][N];

@@ -219,6 +219,37 @@ def test_gradient_of_masked_rows(tide, dtype):
     assert torch.isnan(dx[:2]).all() and torch.isfinite(dx[2]).all()
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("V", [300, 9001])
+@pytest.mark.parametrize("shift", [40, -40, 300, -300, 5000, -5000, 60000, -60000, 70000])
+def test_rows_far_from_zero(tide, shift, V, dtype):
+    """A constant added to a row changes neither its probabilities nor what their
+    error may be: each row moved by about `shift`, some of them confident, where the
+    target's gradient is d (1 - p), a difference of nearly equal numbers."""
+    say("far from zero", shift, V, dtype)
+    T = 8
+    x = ref.normal((T, V), F32, V, 3.0) + shift
+    t = torch.tensor([3, V - 1, 0, 17, V // 2, -1, 5, 250])
+    for r, above in ((0, 14.0), (1, 25.0), (4, 18.0), (6, 60.0)):
+        x[r, t[r]] = x[r].max() + above
+    x[7, ::3] = -INF
+    x = x.to(dtype)
+    got = run(tide, x, t, 4)
+    check(got, step.logprobs(x, t, 4), 4, "far")
+    d, h = 1 + ref.normal((T,), F32, 3).abs(), ref.normal((T,), F32, 4)
+    for with_h in (False, True):
+        kw = {"entropy": got["entropy"], "dentropy": h.to(dev())} if with_h else {}
+        want, lim = step.logprobs_grad(x, t, got["stats"].cpu(), d, got["entropy"].cpu(), h if with_h else None)
+        # p is the product of 2^q and a factor within 2^(2^-8) of 1; the instruction gives 0 for a 2^q below 2^-126.
+        # So p is off by up to 2^-125 besides, and p (lp + H), where p is that small and lp from -88 on falling, by
+        # 2^-125 (88 + |H|).
+        tiny = d + (h.abs() * (88 + got["entropy"].cpu().abs()) if with_h else 0.0)
+        lim = lim + (step.HALF[dtype] + 2 * step.U) * want.abs() + 2.0 ** -125 * tiny.double()[:, None]
+        dx = torch.empty(T, V, dtype=dtype, device=dev())
+        tide.token_logprobs_grad(x.to(dev()), t.to(dev()), got["stats"], d.to(dev()), dx, **kw)
+        ref.close(dx, want, lim, "gradient")
+
+
 def test_gradient_against_differences(tide):
     """sum_t d_t logprob_t + h_t entropy_t at logits a step apart, in 64 bits."""
     T, V, eps = 4, 60, 1e-5
