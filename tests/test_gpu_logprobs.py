@@ -167,6 +167,26 @@ def test_outputs_left_out(tide):
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("top", [0, 7])
+@pytest.mark.parametrize("T,V", [(3, 50001), (3, 600), (1100, 2100), (600, 4200), (300, 8300), (70, 16500)])
+def test_without_entropy(tide, T, V, top, dtype):
+    """Rows in parts, and by workgroups of 64 to 1024 threads, whose entropy is not asked for."""
+    say("without entropy", T, V, top, dtype)
+    x = ref.normal((3, V), dtype, V, 3.0)
+    x[1, : V - 5] = -INF                                # fewer than `top` are left
+    x[2, V // 2] = INF if top else NAN
+    t = torch.tensor([V - 1, V - 3, -100])
+    rows = torch.arange(T) % 3
+    f = lambda *s: torch.full(s, 55.0, device=dev())  # noqa: E731
+    got = {"logprob": f(T), "stats": f(T, 2)}
+    if top:
+        got.update(top_ids=torch.full((T, top), 55, dtype=torch.int32, device=dev()), top_logprobs=f(T, top))
+    tide.token_logprobs(x[rows].to(dev()), t[rows].to(dev()), **got)
+    want = {k: v[rows] for k, v in step.logprobs(x, t, top).items()}
+    check({**got, "entropy": want["entropy"]}, want, top, "without entropy")
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("pad", [0, 3])
 @pytest.mark.parametrize("T,V", [(1, 1), (2, 3), (9, 64), (5, 65), (11, 1000), (3, 2047), (2, 50001), (0, 8), (3, 0)])
 def test_gradient(tide, T, V, pad, dtype):
