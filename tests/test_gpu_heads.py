@@ -214,6 +214,33 @@ def test_many_tokens_and_the_same_bits(tide):
         ref.close(found[0][2 + i], ww, lw + 2.0 ** -8 * ww.abs(), "dw")
 
 
+MANY = [  # T, Hq, Hk, D, pairs, adjacent: 16384 heads and more, of which a wave takes two sets
+    (2100, 8, 1, 128, 64, False), (2053, 7, 1, 128, 64, True), (1700, 8, 2, 80, 20, False), (1700, 6, 4, 80, 40, True),
+    (600, 20, 8, 64, 32, False), (1100, 12, 3, 256, 64, False), (16400, 1, 0, 64, 32, False), (550, 24, 6, 512, 256, True),
+    (1100, 14, 1, 96, 0, False), (5, 3300, 7, 16, 8, False)]
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("layout", ["fused", "odd"])
+@pytest.mark.parametrize("T,Hq,Hk,D,pairs,adjacent", MANY)
+def test_forward_of_many_heads(tide, T, Hq, Hk, D, pairs, adjacent, layout, dtype):
+    """Sets of heads that end in a wave's first or second, odd numbers of sets, keys
+    that begin inside a set."""
+    say("many heads", T, Hq, Hk, D, pairs, adjacent, layout, dtype)
+    c = Case(T, Hq, Hk, D, pairs, adjacent, dtype, layout, seed=T + D, ids=torch.int32 if layout == "odd" else torch.int64)
+    q, k = c.pair(c.q, c.k)
+    qo, ko = c.pair(torch.full_like(c.q, 3.0), torch.full_like(c.k, 3.0))
+    tide.norm_rotate(q, k, qo, ko, eps=1e-5, **c.kw_args(5 if layout == "odd" else 0))
+    for got, x, w, what in ((qo, c.q, c.qw, "q"), (ko, c.k, c.kw, "k")):
+        want, lim = step.norm_rotate(x, w, *c.where(1e-5))
+        ref.close(got, want, lim + step.HALF[dtype] * want.abs(), what)
+    if layout == "odd":                                                   # what lies between heads and rows
+        assert (torch.as_strided(qo, (T, Hq, 3), qo.stride(), qo.storage_offset() + D) == 3.0).all()
+        assert not Hk or (torch.as_strided(ko, (T, Hk, 3), ko.stride(), ko.storage_offset() + D) == 3.0).all()
+    elif Hk:                                                              # the values' window
+        assert (torch.as_strided(ko, (T, Hk, D), ko.stride(), ko.storage_offset() + Hk * D) == 3.0).all()
+
+
 def test_heads_past_two_gib(tide):
     T, H, D = 3, 4, 64
     big = torch.zeros(T, 1 << 30, dtype=BF16, device=dev())
