@@ -159,6 +159,24 @@ def test_whole_numbers_bit_for_bit(tide, T, V, kind, D, dtype):
         assert torch.equal(grad.cpu(), want.float().to(dtype))
 
 
+@pytest.mark.parametrize("V,kind", [(90, "words"), (5000, "even"), (20000, "even"), (3, "one")])
+@pytest.mark.parametrize("dtype,D", [(BF16, 24), (F32, 9)])
+def test_whole_numbers_of_a_million_tokens(tide, V, kind, dtype, D):
+    """Over 2^20 tokens, of which a wave takes 256 in turns of 64: rows that end in a
+    turn, cross several, and cross chunks. Sums below 2^24 in magnitude: exact."""
+    T = (1 << 20) + 777
+    say("a million tokens", V, kind, dtype)
+    ids = some_ids(T, V, V, kind)
+    off, order = sort(tide, ids, V)
+    dout, old = ref.whole((T, D), 3, V).to(dtype), ref.whole((V, D), 9, 3).to(dtype)
+    want = torch.zeros(V + 1, D, dtype=torch.float64)
+    want.index_add_(0, torch.where((ids >= 0) & (ids < V), ids, V), 2.0 * dout.double())
+    for more in (False, True):
+        grad = old.to(dev()).clone()
+        tide.embed_tokens_grad(dout.to(dev()), off, order, grad, scale=2.0, accumulate=more)
+        assert torch.equal(grad.cpu(), (want[:V] + (old.double() if more else 0.0)).float().to(dtype)), more
+
+
 def test_a_row_of_nan_stays_in_its_row(tide):
     T, V, D = 500, 6, 40
     ids = some_ids(T, V, 3, "even")
