@@ -131,6 +131,26 @@ def test_many_tiles_and_the_same_bits(tide):
     assert torch.equal(out, (big.double() * f).float().to(BF16))
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_tensors_that_pass_the_caches(tide, dtype):
+    """Over 192 MiB in all, into outputs and in place, tensors at odd elements."""
+    g = torch.Generator(device=dev()).manual_seed(3)
+    n = (200 << 20) // dtype.itemsize
+    big = torch.randn(n + 9, generator=g, device=dev(), dtype=dtype)
+    sizes = [n // 3 + 1, 5, n // 7, 16384, n - n // 3 - n // 7 - 16384 - 6]
+    parts = list(big[3: n + 3].split(sizes))
+    total = total_of(tide, parts)
+    want = float((big[3: n + 3].double() ** 2).sum())
+    assert abs(float(total) - want) <= 2 * (n + 8) * 2.0 ** -53 * want           # both sums
+    out = torch.full((n + 9,), 3.0, dtype=dtype, device=dev())
+    tide.clip_grads(parts, total, 100.0, out=list(out[1: n + 1].split(sizes)))
+    clipped = (big.double() * (100.0 / math.sqrt(float(total)))).float().to(dtype)
+    assert torch.equal(out[1: n + 1], clipped[3: n + 3]) and (out[:1] == 3.0).all() and (out[n + 1:] == 3.0).all()
+    edges = big[:3].clone(), big[n + 3:].clone()
+    tide.clip_grads(parts, total, 100.0)
+    assert torch.equal(big[3: n + 3], clipped[3: n + 3]) and torch.equal(big[:3], edges[0]) and torch.equal(big[n + 3:], edges[1])
+
+
 def test_tensor_past_two_gib(tide):
     n = (1 << 31) + 100
     t = torch.zeros(n, dtype=BF16, device=dev())
