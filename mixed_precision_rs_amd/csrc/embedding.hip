@@ -548,7 +548,7 @@ __global__ __launch_bounds__(kRowThreads) void sum_chunks(Sorted s, Chunks to, c
         const int n = end - base < 64 ? (int)(end - base) : 64;
         // Lane i: the row of place base + i, its places, and the token there.
         const int64_t place = base + (lane < n ? lane : n - 1);
-        const uint32_t token = *gbl<uint32_t>(s.order + place);
+        uint32_t token = *gbl<uint32_t>(s.order + place);
         int64_t r0, r1;
         rows_at(s, base, base + n - 1, r0, r1);
         while (r0 < r1) {
@@ -560,6 +560,7 @@ __global__ __launch_bounds__(kRowThreads) void sum_chunks(Sorted s, Chunks to, c
         row_range(s, r0, own_lo, own_hi);
         const int32_t row = own_lo <= place && place < own_hi ? (int32_t)r0 : -1;
         const int32_t row_lo = (int32_t)own_lo, row_hi = (int32_t)own_hi;
+        if (row < 0) token = ~0u;                  // of no row: what the order holds there is not read
         if (scribe && lane < n && (row < 0 || row_lo != place)) *gbl_mut<int32_t>(to.owner + place) = -1;
         for (int i = 0; i < n; i += KU) {
             u32x4 raw[KU], old[kAdd ? KU : 1] = {};

@@ -177,6 +177,36 @@ def test_whole_numbers_of_a_million_tokens(tide, V, kind, dtype, D):
         assert torch.equal(grad.cpu(), (want[:V] + (old.double() if more else 0.0)).float().to(dtype)), more
 
 
+@pytest.mark.parametrize("more", [False, True])
+def test_places_without_a_token_cost_nothing(tide, more):
+    """A batch of padding but for a few tokens: what sort_ids left of an earlier batch
+    behind the last row is not gone through. With those places' rows of dout read, 1
+    GiB, the calls took 1.9 and 1.6 times as long as with an order that holds none."""
+    T, V, D = 65536, 300, 8192
+    ids = torch.full((T,), -1)
+    ids[::500] = torch.arange(len(ids[::500])) % V
+    off, order = sort(tide, ids, V)
+    n = int(off[V])
+    assert n == len(ids[::500])
+    stale = torch.randperm(T, generator=torch.Generator().manual_seed(1)).to(torch.int32).to(dev())
+    stale[:n] = order[:n]
+    dout = torch.randn(T, D, device=dev(), dtype=BF16)
+    work = torch.empty(tide.embed_tokens_grad_workspace_bytes(T, D), dtype=torch.uint8, device=dev())
+    grads, best = [torch.zeros(V, D, dtype=BF16, device=dev()) for _ in range(2)], [1e9, 1e9]
+    for turn in range(20):
+        for i, o in enumerate((order, stale)):
+            a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+            grads[i].zero_()
+            a.record()
+            tide.embed_tokens_grad(dout, off, o, grads[i], accumulate=more, workspace=work)
+            b.record()
+            b.synchronize()
+            best[i] = min(best[i], a.elapsed_time(b))
+        assert torch.equal(*grads)
+    say("padded batch", more, best)
+    assert best[1] < 1.3 * best[0], best
+
+
 def test_a_row_of_nan_stays_in_its_row(tide):
     T, V, D = 500, 6, 40
     ids = some_ids(T, V, 3, "even")
