@@ -293,6 +293,27 @@ def test_gradient_against_differences(tide):
         assert abs(float(dx[r, c]) - diff) < 2e-5 * (1 + float(d[r].abs() + h[r].abs())), (r, c)
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("V,times", [(700, 1), (700, 1000), (9000, 50), (40000, 1), (40000, 20), (40000, 100)])
+def test_nan_of_every_kind_is_no_alternative(tide, V, times, dtype):
+    """Quiet and signalling NaN of both signs beside the largest logits: the row's log
+    probabilities are NaN, its alternatives all others."""
+    bits, kind = ([0x7FC0, 0x7F81, 0xFFC0, 0xFF81, 0x7FFF], torch.int16) if dtype is BF16 else (
+        [0x7FC00000, 0x7F800001, 0xFFC00000, 0xFF800001, 0x7FFFFFFF], torch.int32)
+    wrap = 1 << (8 * dtype.itemsize)
+    say("NaN of every kind", V, times, dtype)
+    top = 32
+    x = ref.normal((len(bits), V), dtype, 5, 3.0)
+    for r, b in enumerate(bits):
+        x[r, 16:48] = 30.0 + torch.arange(32).to(dtype)
+        x.view(kind)[r, 16:48:3] = b if b < wrap // 2 else b - wrap
+    assert torch.isnan(x[:, 16:48:3]).all()
+    got = run(tide, x.repeat(times, 1), torch.full((len(bits) * times,), 17), top)
+    want = torch.sort(torch.where(torch.isnan(x), -INF, x.float()), dim=1, descending=True, stable=True).indices[:, :top].int()
+    assert torch.equal(got["top_ids"].cpu(), want.repeat(times, 1))
+    assert all(torch.isnan(got[k]).all() for k in ("logprob", "entropy", "top_logprobs")) and torch.isnan(got["stats"][:, 1]).all()
+
+
 def test_rows_past_two_gib(tide):
     T, V = 9, 1 << 28
     x = torch.zeros(T, V, dtype=BF16, device=dev())
