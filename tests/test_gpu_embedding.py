@@ -177,6 +177,22 @@ def test_whole_numbers_of_a_million_tokens(tide, V, kind, dtype, D):
         assert torch.equal(grad.cpu(), (want[:V] + (old.double() if more else 0.0)).float().to(dtype)), more
 
 
+@pytest.mark.parametrize("dtype,D", [(BF16, 11), (F32, 3)])
+def test_a_table_of_many_short_rows(tide, dtype, D):
+    """More rows than the waves that clear and join look at in one turn."""
+    T, V = 70001, 9_000_011
+    ids = torch.cat([some_ids(T - 20001, V, 1, "even"), some_ids(20001, V, 2, "words")])
+    ids[::7] = V - 1
+    off, order = sort(tide, ids, V)
+    dout = ref.whole((T, D), 9, 1).to(dtype)
+    want = torch.zeros(V + 1, D, dtype=torch.float64)
+    want.index_add_(0, torch.where((ids >= 0) & (ids < V), ids, V), dout.double())
+    for more in (False, True):
+        grad = torch.full((V, D), 2.0, dtype=dtype, device=dev())
+        tide.embed_tokens_grad(dout.to(dev()), off, order, grad, accumulate=more)
+        assert torch.equal(grad.cpu(), (want[:V] + (2.0 if more else 0.0)).float().to(dtype)), more
+
+
 @pytest.mark.parametrize("more", [False, True])
 def test_places_without_a_token_cost_nothing(tide, more):
     """A batch of padding but for a few tokens: what sort_ids left of an earlier batch

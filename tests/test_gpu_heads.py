@@ -241,6 +241,22 @@ def test_forward_of_many_heads(tide, T, Hq, Hk, D, pairs, adjacent, layout, dtyp
         assert (torch.as_strided(ko, (T, Hk, D), ko.stride(), ko.storage_offset() + Hk * D) == 3.0).all()
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_more_tokens_than_waves(tide, dtype):
+    """Over 2^24 tokens of one short head: what they are in pieces."""
+    T = (1 << 24) + 4099
+    g = torch.Generator(device=dev()).manual_seed(1)
+    x = torch.randn(T, 1, 8, generator=g, device=dev(), dtype=dtype)
+    out, part = torch.empty_like(x), torch.empty_like(x)
+    tide.norm_rotate(x, None, out, None, eps=1e-5)
+    for a, b in zip(x.split(1 << 20), part.split(1 << 20)):
+        tide.norm_rotate(a, None, b, None, eps=1e-5)
+    assert torch.equal(out, part)
+    for at in (slice(0, 50), slice(T - 50, T)):
+        want, lim = step.norm_rotate(x[at].cpu(), None, None, None, None, 1e-5, False)
+        ref.close(out[at], want, lim + step.HALF[dtype] * want.abs(), "ends")
+
+
 def test_heads_past_two_gib(tide):
     T, H, D = 3, 4, 64
     big = torch.zeros(T, 1 << 30, dtype=BF16, device=dev())

@@ -314,6 +314,25 @@ def test_nan_of_every_kind_is_no_alternative(tide, V, times, dtype):
     assert all(torch.isnan(got[k]).all() for k in ("logprob", "entropy", "top_logprobs")) and torch.isnan(got["stats"][:, 1]).all()
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_more_rows_than_workgroups(tide, dtype):
+    """Over 2^20 rows that repeat 1009: the bits of those alone."""
+    T, V, top = (1 << 20) + 4099, 19, 3
+    x, t = ref.normal((1009, V), dtype, 1, 3.0), some_targets(1009, V, 2)
+    few = run(tide, x, t, top)
+    check(few, step.logprobs(x, t, top), top, "few")
+    at = torch.arange(T, device=dev()) % 1009
+    x, t = x.to(dev()), t.to(dev())
+    got = run(tide, x[at], t[at], top)
+    for k, v in got.items():
+        assert torch.equal(v, few[k][at]), k
+    d = ref.normal((1009,), F32, 3).to(dev())
+    one, dx = torch.empty_like(x), x[at]
+    tide.token_logprobs_grad(x, t, few["stats"], d, one, entropy=few["entropy"], dentropy=d)
+    tide.token_logprobs_grad(dx, t[at], got["stats"], d[at], dx, entropy=got["entropy"], dentropy=d[at])
+    assert torch.equal(dx, one[at])
+
+
 def test_rows_past_two_gib(tide):
     T, V = 9, 1 << 28
     x = torch.zeros(T, V, dtype=BF16, device=dev())
