@@ -1,6 +1,7 @@
-// Device helpers shared by the training-layer kernels (tokens.hip,
-// checkpoint.hip, weight_grads.hip): 16-byte row vectors of bf16 or fp32 at any
-// element alignment, exact widening, rounding to nearest even.
+// Device helpers shared by the training layer's kernels (tokens.hip, checkpoint.hip,
+// weight_grads.hip) and those at a step's ends (embedding.hip, logprobs.hip, heads.hip,
+// grad_norm.hip): 16-byte row vectors of bf16 or fp32 at any element alignment, exact
+// widening, rounding to nearest even.
 #pragma once
 
 #include <hip/hip_runtime.h>

@@ -350,14 +350,16 @@ hipError_t launch_sort(const Id* ids, int64_t n, int64_t vocab, int32_t* offsets
                    (const int32_t*)w.valid, vocab, offsets);
 }
 
-// First element of vector u of a row: the last vector ends at the row's end.
+// First element of vector u of a row: the last vector ends at the row's end (where
+// the row has one at all).
 template <int V>
 __device__ __forceinline__ int64_t at_vector(int64_t u, int64_t width) {
     return u > 0 && u * V > width - V ? width - V : u * V;
 }
 
-// A copy of rows, scaled on the way: 16384 tokens of 8192 bf16 in 58 us, 268 MB of it
-// written (33 of 2048 in 2.4).
+// A copy of rows, scaled on the way. 16384 tokens of 8192 bf16 write 268 MB: 86 us where
+// 12900 rows are read for them, 58 where ids are as unevenly used as words are (5400
+// rows); 16384 of 2048 21 and 16 us, 33 of 2048 2.4.
 template <class T, class Id>
 __global__ __launch_bounds__(kRowThreads) void embed_rows(const Id* ids, int64_t tokens,
                                                           const T* table, int64_t table_stride,
@@ -422,10 +424,22 @@ struct Grad {
     float scale;
     int32_t accumulate;
 };
-// Places of a chunk. Many small ones keep the GPU busy: 16384 tokens of 2048 bf16
-// take 28 us with 16, 30 with 32, 40 with 64; 2000 of 1000 fp32, added, 18, 29 and 51;
-// but a row that has all the tokens then has as many sums to join: 512 in 97 us by
-// one wave, so that join_left does that where there may be more.
+// Places of a chunk. Small ones keep the GPU busy; but a row that has all the tokens
+// then has as many sums: up to kJoinTokens one wave joins them (512 at most, in 97 us),
+// above join_left does, 7-25 us more whatever it finds. us of the calls on a table of
+// 131072 x 2048 bf16, for even ids, ids as unevenly used as words, and one id:
+//   tokens   chunks of 16   of 32         of 64         of 64, join_left  of 256, join_left
+//     4096    95 100  98    106 106  98   121 121 105   124 124 110
+//     4097    98 100  97    107 107  99   120 120 105   123 124 111
+//     8000   102 102 142    107 105 101   121 120 105   124 124 114
+//    16384   101 112 240    102 112 154   111 120 108   117 125 116
+//    16385   104 113 243    102 111 154   109 120 108   115 125 118
+//    32768   126 121 444    124 123 251   123 130 163   133 139 131
+//   100000   211 195 1295   214 180 701   221 188 400   245 213 206
+//     2^20                                              1304 1244 1247    1124 1016 899
+//     2^21                                              2531 2392 2657    2027 1869 1709
+// The rule bounds the worst row at the price of the others, which pay 8 us for it behind
+// 4096 tokens and 13 behind 16384; its last border could stand further in.
 int32_t chunk_of(int64_t tokens) { return tokens <= 4096 ? 16 : tokens <= 16384 ? 32 : tokens <= 1 << 20 ? 64 : 256; }
 constexpr int64_t kJoinTokens = 16384;
 int64_t chunks_of(int64_t tokens) {
@@ -441,13 +455,6 @@ __device__ __forceinline__ void row_range(const Sorted& s, int64_t v, int64_t& l
     hi = hi > s.tokens ? s.tokens : hi;
 }
 
-// First column of vector u: the last vector ends at the row's end (where the row
-// has one at all).
-template <int V>
-__device__ __forceinline__ int64_t column(int64_t u, int64_t width) {
-    return u > 0 && u * V > width - V ? width - V : u * V;
-}
-
 // Vector u of row v of the gradient from its sum; old is what the row holds there
 // (when it is added to).
 template <class T>
@@ -455,7 +462,7 @@ __device__ __forceinline__ void put_vector(const Grad<T>& g, int64_t v, int64_t 
                                            u32x4 old) {
     constexpr int V = kVecOf<T>;
     if (u * V >= g.width) return;
-    const int64_t at = column<V>(u, g.width);
+    const int64_t at = at_vector<V>(u, g.width);
     const int some = g.width < V ? (int)g.width : V, seen = (int)(u * V - at);
     T* to = g.data + v * g.stride + at;
     float r[V];
@@ -486,7 +493,7 @@ template <class T>
 __device__ __forceinline__ u32x4 old_vector(const Grad<T>& g, int64_t v, int64_t u) {
     constexpr int V = kVecOf<T>;
     if (!g.accumulate || u * V >= g.width) return u32x4{};
-    return load_row(g.data + v * g.stride + column<V>(u, g.width), g.width < V ? (int)g.width : V);
+    return load_row(g.data + v * g.stride + at_vector<V>(u, g.width), g.width < V ? (int)g.width : V);
 }
 
 // The rows that two places of the order belong to, by all 64 lanes: the last one
@@ -516,7 +523,7 @@ __global__ __launch_bounds__(kRowThreads) void sum_chunks(Sorted s, Chunks to, c
     const int64_t b = w / tiles, u = (w - b * tiles) * 64 + lane;
     const bool scribe = w == b * tiles;            // the wave that keeps the books of this chunk
     const int64_t first = b * to.size, end = first + to.size < s.tokens ? first + to.size : s.tokens;
-    const int64_t at = column<V>(u, grad.width);
+    const int64_t at = at_vector<V>(u, grad.width);
     const int some = u * V >= grad.width ? 0 : grad.width < V ? (int)grad.width : V;
     int32_t left[2] = {-1, -1};
     // The row in hand: its places, those taken so far, and their sum.
@@ -692,7 +699,7 @@ __device__ __forceinline__ void finish_vector(const Sorted& s, const Chunks& fro
     int64_t lo, hi;
     row_range(s, v, lo, hi);
     const int some = u * V >= grad.width ? 0 : grad.width < V ? (int)grad.width : V;
-    const int64_t at = column<V>(u, grad.width);
+    const int64_t at = at_vector<V>(u, grad.width);
     if (lo >= hi) {
         if (!grad.accumulate && some) store_row(grad.data + v * grad.stride + at, some, u32x4{});
         return;
@@ -737,7 +744,7 @@ __global__ __launch_bounds__(kRowThreads) void finish_table(Sorted s, Chunks fro
         bool open = lo < hi;
         if (open && from.size) open = *gbl<int32_t>(from.owner + lo) != v;
         if (u * V < grad.width) {
-            T* to = grad.data + part * grad.stride + column<V>(u, grad.width);
+            T* to = grad.data + part * grad.stride + at_vector<V>(u, grad.width);
             const int some = grad.width < V ? (int)grad.width : V;
 #pragma unroll
             for (int j = 0; j < kRowsAtOnce; ++j)

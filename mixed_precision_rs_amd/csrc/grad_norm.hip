@@ -18,10 +18,10 @@ using namespace tide;
 namespace {
 
 constexpr int kThreads = 256;
-// Each changed alone, over 1.2 GB of bf16 in 391 tensors, the medians of the
-// launches of the squares and of clipping: as it is 100 and 174 us; tiles of 8 KiB
-// 112 and 168, of 32 98 and 172, of 64 104 and 182; 2048 workgroups 106 and 177,
-// 16384 100 and 170, with 2 us more for joining their sums.
+// Each changed alone, over 1.2 GB of bf16 in 391 tensors, the median launch of the two
+// that the squares take and of the three that clipping takes: as it is 100 and 174 us;
+// tiles of 8 KiB 112 and 168, of 32 98 and 172, of 64 104 and 182; 2048 workgroups 106
+// and 177, 16384 100 and 170, with 2 us more for joining their sums.
 constexpr int kTileBytes = 16384;
 template <class T>
 constexpr int kTileOf = kTileBytes / (int)sizeof(T);
@@ -29,7 +29,7 @@ constexpr int64_t kMostGroups = 8192;
 // Tiles that one workgroup sums alone, in one launch.
 constexpr int64_t kAlone = 8;
 // Tensors that together pass the memory-side cache (256 MiB) are read past the
-// caches (those launches: 100 us instead of 106, clipping 174 instead of 179);
+// caches (the same launches: 100 us instead of 106, clipping 174 instead of 179);
 // smaller ones by ordinary loads, so that clipping finds there what the squares
 // have read (53 MB: 18.4 us instead of 20.7).
 constexpr int64_t kPastCaches = (int64_t)192 << 20;
